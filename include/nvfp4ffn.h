@@ -6,8 +6,10 @@
  *   (up to 64 rows per call, in passes of 16),
  *   x, out BF16;  gate [I, H], up [I, H], down [H, I] NVFP4;  act = SiLU | GeLU-tanh.
  *
- * Beside it: a LoRA delta overlay on the same FFN, and the FFN and GEMV on
- * block-scaled FP8 weights (the w8a16 calls near the end of this header).
+ * Beside it: a LoRA delta overlay on the same FFN, the FFN and GEMV on
+ * block-scaled FP8 weights (the w8a16 calls), and the attention side of a
+ * decode layer (norm, rotary positions, 8-bit paged cache, attention; near
+ * the end of this header).
  *
  * What the calls restate (Atlas engine pages):
  *  - "spark_model/layers/dense_ffn.rs", module doc comment: the dense SwiGLU
@@ -373,6 +375,163 @@ size_t ffn_swiglu_w8a16_workspace_bytes(int M, int H, int I);
 nvfp4_status ffn_swiglu_w8a16(const void* x, int M, int H, int I, const void* gate_up_packed,
                               const void* down_packed, nvfp4_act act, void* out, void* ws,
                               size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------ attention side of a layer */
+
+/*
+ * What a decode layer runs beside the projections and the FFN: the norms in
+ * front of them, rotary positions, and attention over a paged key/value cache
+ * of 8-bit floats.  Conventions as for every call (status codes, validation
+ * before any launch, asynchronous on `stream`, 16-byte aligned bf16 and code
+ * buffers).  These calls take any number of token rows.  Results are
+ * bit-reproducible.  They use programmatic dependent launch where noted, but
+ * read no input before the preceding kernel on `stream` has completed.
+ */
+
+/*
+ * Root-mean-square norm of x + residual, [M, H] bf16:
+ *   r = x + residual (fp32; residual may be NULL for none)
+ *   sum_out = bf16(r)                        (NULL to leave it out)
+ *   y = r * (mean(r^2) + eps)^(-1/2) * (weight + weight_bias),   out = bf16(y)
+ * weight (device) bf16 [H].  M >= 1, H a multiple of 16, 16 <= H <= 32768,
+ * eps >= 0.  sum_out may be x or residual, and out may be x or residual (not
+ * the buffer that sum_out is); other overlaps are NVFP4_ERR_ALIAS.
+ */
+nvfp4_status add_rmsnorm_bf16(const void* x, const void* residual, const void* weight, int M,
+                              int H, float eps, float weight_bias, void* sum_out, void* out,
+                              cudaStream_t stream);
+
+/*
+ * The same norm into 8 bits: for each row and group of 128 columns (the last
+ * one may be shorter) scale = max(amax|y| / 448, 2^-126), or 1 when amax is 0,
+ * and code = E4M3(y / scale), to nearest even, saturated, NaN kept.
+ *   codes (device, out) u8 [M, H];  scales (device, out) fp32 [M, ceil(H/128)].
+ * Neither overlaps another buffer.
+ */
+nvfp4_status add_rmsnorm_e4m3(const void* x, const void* residual, const void* weight, int M,
+                              int H, float eps, float weight_bias, void* sum_out, uint8_t* codes,
+                              float* scales, cudaStream_t stream);
+
+/* How rotary frequencies change for contexts longer than the trained one. */
+typedef enum {
+    ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot_dim) */
+    ROPE_LINEAR = 1, /* f_i / factor */
+    ROPE_BASE = 2,   /* base * factor^(rot_dim/(rot_dim-2)) in place of base */
+    ROPE_RAMP = 3    /* f_i * (g + (1-g)/factor), g = clamp((turns - slow)/(fast - slow), 0, 1),
+                        turns = f_i * context / 2 pi */
+} rope_scaling;
+
+/*
+ * Table of rotations (a load-time call, fp64 arithmetic):
+ *   table (device, out) fp32 [positions, rot_dim/2, 2] = magnitude * (cos, sin)(p * f_i).
+ * rot_dim a multiple of 16 up to 256, base > 1; factor > 0 unless ROPE_PLAIN;
+ * context > 0 and 0 <= slow < fast for ROPE_RAMP (ignored otherwise).
+ */
+nvfp4_status rope_table(int positions, int rot_dim, double base, rope_scaling scaling,
+                        double factor, double context, double slow, double fast, double magnitude,
+                        float* table, cudaStream_t stream);
+
+/*
+ * The cache: pages of `page` tokens, each page holding every head of one
+ * block of tokens, E4M3 codes with one fp32 scale per page and head:
+ *   k[page][head][row][d] = k_scales[page][head] * e4m3(k_codes[page][head][row][d])
+ * page a power of two in 16..256, head_dim 64, 128 or 256.  Scales are
+ * positive and finite.
+ */
+typedef struct {
+    void* k_codes;   /* (device) u8 [pages, kv_heads, page, head_dim] */
+    void* v_codes;   /* (device) the same */
+    float* k_scales; /* (device) [pages, kv_heads] */
+    float* v_scales; /* (device) the same */
+    int pages, kv_heads, page, head_dim;
+} kv8_cache;
+
+/*
+ * A batch of sequences and their new tokens.  Tokens q_start[b] ..
+ * q_start[b+1] - 1 of the call's rows belong to sequence b and take the last
+ * positions of its kv_len[b]: with n of them, the i-th has position
+ * kv_len[b] - n + i.  Position p lies in page page_table[b][p / page], row
+ * p % page.  n may be 0 (the sequence takes no part).
+ * The lists live on the device and are not read by the host.  The kernels
+ * check them: a page outside the cache, a length beyond the table, decreasing
+ * or too large q_start, n > kv_len or a position beyond the rotation table
+ * reads and writes nothing outside the buffers (what it concerns is left out:
+ * not written, or masked) and sets the status word.
+ */
+typedef struct {
+    const int* q_start;    /* (device) [batch + 1], from 0, not decreasing */
+    const int* kv_len;     /* (device) [batch], the new tokens included */
+    const int* page_table; /* (device) [batch, table_width] */
+    int* status;           /* (device) one word, zeroed once by the caller, or NULL */
+    int batch;             /* 1..1024 */
+    int table_width;       /* pages a sequence can have; table_width * page < 2^31 - 256 */
+} kv8_batch;
+
+/* Synchronises `stream`, reads and clears the batch's status word: NVFP4_OK, or
+ * NVFP4_ERR_RANGE when a call met an index outside its buffers since. */
+nvfp4_status kv8_batch_status(const kv8_batch* batch, cudaStream_t stream);
+
+/*
+ * Writes the batch's new tokens into the cache, with rotary positions:
+ *   k, v (device) bf16 [tokens, kv_heads, head_dim], k_stride and v_stride
+ *        values between tokens (multiples of 8: views of a fused projection);
+ *   rope (device) fp32 [rope_positions, rot_dim/2, 2], or NULL for no rotation:
+ *        the first rot_dim values of each head of q and k turn in pairs
+ *        (i, i + rot_dim/2), or (2i, 2i+1) when interleaved:
+ *        (a cos - b sin, b cos + a sin), in fp32;
+ *   q (device) bf16 [tokens, heads, head_dim] with q_stride -> q_out (device,
+ *        out) bf16 [tokens, heads, head_dim] contiguous, rotated and rounded;
+ *        both NULL to leave q out.  q_out may be q when q is contiguous.
+ * For each head of k (rotated, not rounded in between) and v, and each page
+ * that gets new tokens:
+ *   need  = the smallest 2^e with max|new values| <= 448 * 2^e, e in -60..119
+ *   scale = max(old scale, need) when rows in front of the new ones hold
+ *           tokens of the page, else need
+ *   codes = E4M3(value / scale) (nearest even, saturated, NaN kept; NaN does
+ *           not enter the maximum); the older rows' codes are re-scaled by
+ *           old scale / scale when it changed.
+ * A page that gets new tokens belongs to one sequence of the batch.
+ */
+nvfp4_status kv8_append(const kv8_cache* cache, const kv8_batch* batch, int tokens, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                        int64_t q_stride, int heads, void* q_out, const float* rope,
+                        int rope_positions, int rot_dim, int interleaved, cudaStream_t stream);
+
+/*
+ * Reads the batch's tokens back (the positions that kv8_append with this batch
+ * writes; a whole sequence when it has kv_len[b] tokens in the batch):
+ *   k_out, v_out (device, out) bf16 [tokens, kv_heads, head_dim] =
+ *   bf16(scale * code).
+ */
+nvfp4_status kv8_read(const kv8_cache* cache, const kv8_batch* batch, int tokens, void* k_out,
+                      void* v_out, cudaStream_t stream);
+
+/* Workspace bytes for kv8_attention on the current device (0 for invalid
+ * arguments); contract as for nvfp4_gemv (zero-fill once, calls sharing one
+ * ordered). */
+size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* batch, int tokens,
+                                     int heads);
+
+/*
+ * Attention of the batch's tokens over the cache (which holds them already).
+ * The query at position p sees key j <= p and, with window > 0, only
+ * j > p - window or j < sinks (sinks first tokens stay visible):
+ *   s_j = softmax_scale * q . k_j,   out = sum_j softmax(s)_j v_j,
+ *   lse = log(sum_j e^(s_j))
+ *   q (device) bf16 [tokens, heads, head_dim], q_stride values between tokens
+ *        (a multiple of 8); head h reads the cache's head h / (heads/kv_heads);
+ *   out (device, out) bf16 [tokens, heads, head_dim] contiguous;
+ *   lse (device, out) fp32 [tokens, heads], or NULL;
+ *   ws (device) >= kv8_attention_workspace_bytes.
+ * A query that sees nothing gets 0 and -infinity.  Masked keys and values do
+ * not enter the result, whatever they hold.  Scores, maxima and sums are fp32.
+ * heads a multiple of kv_heads; window, sinks >= 0 (sinks without a window
+ * have no effect).
+ */
+nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int heads,
+                           const kv8_cache* cache, const kv8_batch* batch, float softmax_scale,
+                           int window, int sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
 
 /* ------------------------------------------------------------------ utilities */
 

@@ -1,0 +1,146 @@
+// rmsnorm.cu -- root-mean-square norm of x + residual, in one pass:
+//   r = x + residual (fp32),  sum = bf16(r)
+//   y = r * (mean(r^2) + eps)^(-1/2) * (weight + weight_bias)
+// stored as bf16(y), or as E4M3 codes with one fp32 scale per row and 128
+// columns: scale = max(amax / 448, 2^-126) (1 for a group of zeros),
+// code = e4m3(y / scale), which saturates and keeps NaN.
+//
+// One block per row; a thread holds its 8-column vectors of r in registers
+// between the sum of squares and the output, so x and the residual are read
+// once.  The sum, the norm and y stay in fp32 (the residual stream's rounding
+// to bf16 does not enter the norm).
+#include "kv8.cuh"
+
+namespace nvf {
+
+namespace {
+
+struct NormArgs {
+    const uint4* x;
+    const uint4* residual;  // or null
+    const uint4* weight;
+    uint4* sum_out;         // or null
+    uint4* out;             // bf16 output, or null
+    uint2* codes;           // E4M3 output, or null
+    float* scales;
+    int vecs;               // H / 8
+    int groups;             // ceil(H / 128)
+    float inv_h, eps, weight_bias;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(a[i]);
+        v[2 * i + 1] = bf16_hi(a[i]);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                      bf16x2(v[6], v[7]));
+}
+
+// kVecs: vectors per thread.  The vectors of a warp are consecutive, so 16
+// lanes hold one group of 128 columns.
+template <int kVecs>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t row = blockIdx.x;
+    const uint4* x = a.x + row * a.vecs;
+    float r[kVecs][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int c = tid + i * blockDim.x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[i][e] = 0.0f;
+        if (c < a.vecs) {
+            unpack8(x[c], r[i]);
+            if (a.residual) {
+                float o[8];
+                unpack8(a.residual[row * a.vecs + c], o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[i][e] += o[e];
+            }
+            if (a.sum_out) a.sum_out[row * a.vecs + c] = pack8(r[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    __shared__ float part[32];
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    float total = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    const float inv = rsqrtf(total * a.inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int c = tid + i * blockDim.x;
+        const bool live = c < a.vecs;
+        float y[8];
+        if (live) {
+            unpack8(a.weight[c], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = r[i][e] * inv * (y[e] + a.weight_bias);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+        }
+        if (a.out) {
+            if (live) a.out[row * a.vecs + c] = pack8(y);
+            continue;
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float scale = top == 0.0f ? 1.0f : fmaxf(__fdiv_rn(top, 448.0f), 1.17549435e-38f);
+        if (live) {
+            float q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(y[e], scale);
+            a.codes[row * a.vecs + c] = make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
+                                                   f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
+            if ((c & 15) == 0) a.scales[row * a.groups + (c >> 4)] = scale;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* weight, int M,
+                               int H, float eps, float weight_bias, void* sum_out, void* out,
+                               uint8_t* codes, float* scales, cudaStream_t s) {
+    NormArgs a;
+    a.x = reinterpret_cast<const uint4*>(x);
+    a.residual = reinterpret_cast<const uint4*>(residual);
+    a.weight = reinterpret_cast<const uint4*>(weight);
+    a.sum_out = reinterpret_cast<uint4*>(sum_out);
+    a.out = reinterpret_cast<uint4*>(out);
+    a.codes = reinterpret_cast<uint2*>(codes);
+    a.scales = scales;
+    a.vecs = H / 8;
+    a.groups = (H + 127) / 128;
+    a.inv_h = 1.0f / (float)H;
+    a.eps = eps;
+    a.weight_bias = weight_bias;
+    const int per = (a.vecs + 1023) / 1024;
+    if (per > 4) return cudaErrorInvalidValue;
+    const int kv = per <= 1 ? 1 : per <= 2 ? 2 : 4;
+    const int threads = ((a.vecs + kv - 1) / kv + 31) / 32 * 32;
+    if (kv == 1)
+        add_rmsnorm_kernel<1><<<M, threads, 0, s>>>(a);
+    else if (kv == 2)
+        add_rmsnorm_kernel<2><<<M, threads, 0, s>>>(a);
+    else
+        add_rmsnorm_kernel<4><<<M, threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace nvf

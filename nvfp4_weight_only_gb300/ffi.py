@@ -20,6 +20,10 @@ NVFP4_ACT_SILU = 0
 NVFP4_ACT_GELU_TANH = 1
 NVFP4_SRC_F32 = 0
 NVFP4_SRC_BF16 = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_RAMP = 3
 
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ERR_ALIGN",
                 4: "NVFP4_ERR_RANGE", 5: "NVFP4_ERR_WORKSPACE", 6: "NVFP4_ERR_CUDA",
@@ -38,6 +42,8 @@ EXPORTS = [
     "w8a16_repacked_bytes", "w8a16_repacked_gate_up_bytes", "w8a16_repack",
     "w8a16_repack_gate_up", "w8a16_unpack", "w8a16_gemv_workspace_bytes", "w8a16_gemv",
     "ffn_swiglu_w8a16_workspace_bytes", "ffn_swiglu_w8a16",
+    "add_rmsnorm_bf16", "add_rmsnorm_e4m3", "rope_table", "kv8_batch_status", "kv8_append",
+    "kv8_read", "kv8_attention_workspace_bytes", "kv8_attention",
     "nvfp4_workspace_init", "nvfp4_workspace_status", "nvfp4_status_string",
 ]
 # Every symbol declared in include/nvfp4ffn_testing.h (test hooks).
@@ -68,6 +74,7 @@ def load(build_if_missing: bool = False):
                            "(or __graft_entry__.build()) first")
     L = ctypes.CDLL(LIB_PATH)
     vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+    i64, f64 = ctypes.c_int64, ctypes.c_double
     sig = {
         "nvfp4_quantize_scratch_bytes": (sz, [i32, i32]),
         "nvfp4_quantize": (i32, [vp, i32, i32, i32, vp, vp, ctypes.POINTER(f32), vp, sz, vp]),
@@ -102,6 +109,15 @@ def load(build_if_missing: bool = False):
         "w8a16_gemv": (i32, [vp, i32, i32, vp, i32, vp, vp, sz, vp]),
         "ffn_swiglu_w8a16_workspace_bytes": (sz, [i32, i32, i32]),
         "ffn_swiglu_w8a16": (i32, [vp, i32, i32, i32, vp, vp, i32, vp, vp, sz, vp]),
+        "add_rmsnorm_bf16": (i32, [vp, vp, vp, i32, i32, f32, f32, vp, vp, vp]),
+        "add_rmsnorm_e4m3": (i32, [vp, vp, vp, i32, i32, f32, f32, vp, vp, vp, vp]),
+        "rope_table": (i32, [i32, i32, f64, i32, f64, f64, f64, f64, f64, vp, vp]),
+        "kv8_batch_status": (i32, [vp, vp]),
+        "kv8_append": (i32, [vp, vp, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, i32, i32,
+                             vp]),
+        "kv8_read": (i32, [vp, vp, i32, vp, vp, vp]),
+        "kv8_attention_workspace_bytes": (sz, [vp, vp, i32, i32]),
+        "kv8_attention": (i32, [vp, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, vp, sz, vp]),
         "nvfp4_workspace_init": (i32, [vp, sz, vp]),
         "nvfp4_workspace_status": (i32, [vp, vp]),
         "nvfp4_status_string": (ctypes.c_char_p, [i32]),
@@ -125,6 +141,15 @@ def _ptr(t):
 
 def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _addr(t):
+    """The address as a plain number: what the newer calls pass (no wrapper object per argument)."""
+    return t.data_ptr() if t is not None else None
+
+
+def _raw_stream(t):
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _cuda(t, name, dtype=None):
@@ -437,4 +462,213 @@ def ffn_swiglu_w8a16(x: torch.Tensor, gate_up_packed: torch.Tensor, down_packed:
     _check("ffn_swiglu_w8a16",
            L.ffn_swiglu_w8a16(_ptr(x), M, H, I, _ptr(gate_up_packed), _ptr(down_packed), int(act),
                               _ptr(out), _ptr(ws), ws.numel(), _stream(x.device)))
+    return out
+
+
+# ------------------------------------------------------------------ attention side of a layer
+
+def _rows(t, name, heads_dim):
+    """A bf16 [tokens, heads, head_dim] view whose rows are contiguous: its token stride."""
+    _on_cuda(t, name, torch.bfloat16)
+    T, heads, dim = t.shape
+    if dim != heads_dim:
+        raise ValueError(f"{name} must have head_dim {heads_dim}, got {dim}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have contiguous heads")
+    return t.stride(0) if T > 1 else heads * dim
+
+
+def _on_cuda(t, name, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _shaped(t, name, dtype, shape):
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _norm_args(x, weight, residual, sum_out):
+    _cuda(x, "x", torch.bfloat16)
+    M, H = x.shape
+    _shaped(weight, "weight", torch.bfloat16, (H,))
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        if t is not None:
+            _shaped(t, name, torch.bfloat16, (M, H))
+    return M, H
+
+
+def add_rmsnorm_bf16(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                     residual: torch.Tensor = None, sum_out: torch.Tensor = None,
+                     weight_bias: float = 0.0, out: torch.Tensor = None) -> torch.Tensor:
+    """bf16 norm of x + residual; the sum goes to sum_out (which may be residual) when given."""
+    M, H = _norm_args(x, weight, residual, sum_out)
+    if out is None:
+        out = torch.empty_like(x)
+    _shaped(out, "out", torch.bfloat16, (M, H))
+    _check("add_rmsnorm_bf16",
+           load().add_rmsnorm_bf16(_addr(x), _addr(residual), _addr(weight), M, H, eps,
+                                   weight_bias, _addr(sum_out), _addr(out), _raw_stream(x)))
+    return out
+
+
+def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                     residual: torch.Tensor = None, sum_out: torch.Tensor = None,
+                     weight_bias: float = 0.0, codes: torch.Tensor = None,
+                     scales: torch.Tensor = None):
+    """(codes u8 [M, H], scales fp32 [M, ceil(H/128)]) of the norm of x + residual."""
+    M, H = _norm_args(x, weight, residual, sum_out)
+    if codes is None:
+        codes = torch.empty((M, H), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((M, (H + 127) // 128), dtype=torch.float32, device=x.device)
+    _shaped(codes, "codes", torch.uint8, (M, H))
+    _shaped(scales, "scales", torch.float32, (M, (H + 127) // 128))
+    _check("add_rmsnorm_e4m3",
+           load().add_rmsnorm_e4m3(_addr(x), _addr(residual), _addr(weight), M, H, eps,
+                                   weight_bias, _addr(sum_out), _addr(codes), _addr(scales),
+                                   _raw_stream(x)))
+    return codes, scales
+
+
+def rope_table(positions: int, rot_dim: int, base: float, device, scaling: int = ROPE_PLAIN,
+               factor: float = 1.0, context: float = 1.0, slow: float = 1.0, fast: float = 32.0,
+               magnitude: float = 1.0) -> torch.Tensor:
+    """fp32 [positions, rot_dim/2, 2] rotations (cos, sin) for kv8_append."""
+    table = torch.empty((positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    if not table.is_cuda:
+        raise ValueError("device must be a CUDA device")
+    _check("rope_table", load().rope_table(positions, rot_dim, base, scaling, factor, context, slow,
+                                           fast, magnitude, _addr(table), _raw_stream(table)))
+    return table
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] + [
+        (n, ctypes.c_int) for n in ("pages", "kv_heads", "page", "head_dim")]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table", "status")] + [
+        (n, ctypes.c_int) for n in ("batch", "table_width")]
+
+
+class Kv8Cache:
+    """The paged E4M3 cache (kv8_cache): codes u8 [pages, kv_heads, page, head_dim] and fp32 scales
+    [pages, kv_heads] for k and v.  Holds the tensors and their description."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        _cuda(k_codes, "k_codes", torch.uint8)
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, kv_heads, page, head_dim]")
+        _shaped(v_codes, "v_codes", torch.uint8, k_codes.shape)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _shaped(t, name, torch.float32, k_codes.shape[:2])
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = (k_codes, v_codes, k_scales,
+                                                                    v_scales)
+        self.pages, self.kv_heads, self.page, self.head_dim = k_codes.shape
+        self.struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                   v_scales.data_ptr(), *k_codes.shape)
+        self.ref = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page, head_dim, device):
+        """A cache whose pages hold nothing yet."""
+        codes = [torch.empty((pages, kv_heads, page, head_dim), dtype=torch.uint8, device=device)
+                 for _ in "kv"]
+        scales = [torch.ones((pages, kv_heads), dtype=torch.float32, device=device) for _ in "kv"]
+        return cls(*codes, *scales)
+
+
+class Kv8Batch:
+    """The sequences of one step (kv8_batch): q_start int32 [batch + 1], kv_len int32 [batch] and
+    page_table int32 [batch, table_width], all read on the device when a call runs, so a program
+    may advance them in place.  Owns a status word, which kv8_batch_status reads."""
+
+    def __init__(self, q_start, kv_len, page_table):
+        _cuda(kv_len, "kv_len", torch.int32)
+        batch = kv_len.numel()
+        _shaped(kv_len, "kv_len", torch.int32, (batch,))
+        _shaped(q_start, "q_start", torch.int32, (batch + 1,))
+        _cuda(page_table, "page_table", torch.int32)
+        if page_table.dim() != 2 or page_table.shape[0] != batch:
+            raise ValueError("page_table must be [batch, table_width]")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.status = torch.zeros(1, dtype=torch.int32, device=kv_len.device)
+        self.struct = _BatchStruct(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+                                   self.status.data_ptr(), batch, page_table.shape[1])
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kv8_batch_status(batch: Kv8Batch) -> int:
+    """Synchronise, read and clear the batch's status word (0 = OK, 4 = an index out of range)."""
+    return load().kv8_batch_status(batch.ref, _raw_stream(batch.status))
+
+
+def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tensor,
+               q: torch.Tensor = None, q_out: torch.Tensor = None, rope: torch.Tensor = None,
+               interleaved: bool = False):
+    """Write k, v [tokens, kv_heads, head_dim] into the cache, k rotated by the rope table; with
+    q [tokens, heads, head_dim] given, return it rotated (contiguous, in q_out when given)."""
+    k_stride = _rows(k, "k", cache.head_dim)
+    v_stride = _rows(v, "v", cache.head_dim)
+    T = k.shape[0]
+    if k.shape[1] != cache.kv_heads or v.shape[:2] != k.shape[:2]:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim]")
+    heads = q_stride = positions = rot = 0
+    if q is not None:
+        q_stride = _rows(q, "q", cache.head_dim)
+        heads = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q must have the tokens of k")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _shaped(q_out, "q_out", torch.bfloat16, q.shape)
+    if rope is not None:
+        _cuda(rope, "rope", torch.float32)
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError("rope must be [positions, rot_dim/2, 2]")
+        positions, rot = rope.shape[0], 2 * rope.shape[1]
+    _check("kv8_append",
+           load().kv8_append(cache.ref, batch.ref, T, _addr(k), k_stride, _addr(v), v_stride,
+                             _addr(q), q_stride, heads, _addr(q_out), _addr(rope), positions, rot,
+                             1 if interleaved else 0, _raw_stream(k)))
+    return q_out
+
+
+def kv8_read(cache: Kv8Cache, batch: Kv8Batch, k_out: torch.Tensor, v_out: torch.Tensor):
+    """Read the batch's tokens back: k_out, v_out bf16 [tokens, kv_heads, head_dim]."""
+    T = k_out.shape[0]
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _shaped(t, name, torch.bfloat16, (T, cache.kv_heads, cache.head_dim))
+    _check("kv8_read", load().kv8_read(cache.ref, batch.ref, T, _addr(k_out), _addr(v_out),
+                                       _raw_stream(k_out)))
+    return k_out, v_out
+
+
+def kv8_attention_workspace_bytes(cache: Kv8Cache, batch: Kv8Batch, tokens: int, heads: int) -> int:
+    return load().kv8_attention_workspace_bytes(cache.ref, batch.ref, tokens, heads)
+
+
+def kv8_attention(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, softmax_scale: float,
+                  window: int = 0, sinks: int = 0, ws: torch.Tensor = None,
+                  out: torch.Tensor = None, lse: torch.Tensor = None) -> torch.Tensor:
+    """out bf16 [tokens, heads, head_dim]: attention of q over the cache, which already holds the
+    batch's tokens; log-sum-exps go to lse fp32 [tokens, heads] when given."""
+    q_stride = _rows(q, "q", cache.head_dim)
+    T, heads = q.shape[:2]
+    if ws is None:
+        ws = workspace(kv8_attention_workspace_bytes(cache, batch, T, heads), q.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _shaped(out, "out", torch.bfloat16, q.shape)
+    if lse is not None:
+        _shaped(lse, "lse", torch.float32, (T, heads))
+    _check("kv8_attention",
+           load().kv8_attention(_addr(q), q_stride, T, heads, cache.ref, batch.ref, softmax_scale,
+                                window, sinks, _addr(out), _addr(lse), _addr(ws), ws.numel(),
+                                _raw_stream(q)))
     return out
