@@ -6,16 +6,43 @@
 //   s_j = softmax_scale * k_scale * (q . k_code_j),  out = sum_j softmax(s)_j v_scale v_code_j
 // lse = log(sum exp s).  A query that sees nothing gives 0 and -inf.
 //
-// One block per token and query head; each warp takes every fourth key with a
-// running maximum and sum (fp32), the lanes split the head, and the warps'
-// states are joined at the end.
+// What bounds it: the cache's bytes for one or a few new tokens (2 * head_dim
+// bytes per key and kv head, 4 * rows flops per byte), so every byte of the
+// cache is copied once per unit and the products run on the tensor cores.
+//
+// Unit: one sequence, one kv head and a tile of kRows rows (new tokens x the
+// query heads that share the kv head).  A unit's visible keys form tiles of
+// kTile keys.  All units' tiles, in order, are cut into one equal range per
+// block (lengths are read on the device, so ragged batches balance and a
+// captured graph follows them); the 8 warps of a block take a range's tiles in
+// turn, each with its own ring of asynchronous copies and its own running
+// softmax, and their states are joined in shared memory.  A unit that several
+// blocks share is joined by the last of them to finish, in the order of the
+// ranges, so results do not depend on timing.
+//
+// Products: keys (values' columns) are the 16-row operand and the new rows the
+// 8-column one, m16n8k16 with f16 operands and f32 sums; E4M3 codes are exact
+// in f16, q is scaled per row by a power of two into f16's range (as exact as
+// bf16 down to 2^-28 of the row's largest value).  S^T = K q^T leaves a key's
+// scores of two rows in a thread; P^T reaches the operand layout of
+// O^T = V^T P^T by an 8x8 transpose (movmatrix).  The order of keys within 16
+// and of the head's values is free, so each thread reads 16-byte pieces.
+//
+// Softmax with a scale per page: with t = log2(e) s + log2(v_scale), the
+// weights are P = 2^(t - max t + 14), so O = sum P v_code needs no scale per
+// key and l = sum P / v_scale restores the denominator.  P is rounded to f16
+// (11 bits, kept normal down to 2^-28 of the largest); t, maxima, l and O are
+// fp32.
 #include "kv8.cuh"
 
 namespace nvf {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr float kBias = 14.0f;  // the largest weight is 2^14 in f16
+constexpr int kMinTiles = 8;    // least tiles per block: one per warp
 
 struct AttentionArgs {
     Kv8CacheArgs c;
@@ -23,121 +50,806 @@ struct AttentionArgs {
     const __nv_bfloat16* q;
     __nv_bfloat16* out;
     float* lse;  // or null
+    int* counters;
+    float* partials;
     long long q_stride;
     int heads, group;
-    float scale;  // softmax_scale
+    float scale;  // softmax_scale * log2(e)
     int window, sinks;
 };
 
+template <int kDim, int kNT>
+struct Shape {
+    static constexpr int kRows = 8 * kNT;
+    static constexpr int kTile = kDim == 256 ? 16 : 32;
+    static constexpr int kStages = kDim == 64 ? 6 : 3;
+    static constexpr int kStageBytes = 2 * kTile * kDim;
+    static constexpr int kSteps = kDim / 16;  // k16 steps of q . k, m16 tiles of the head
+    static constexpr int kRowFloats = kDim + 4;
+    // shared memory: ring, page scales of each stage, q fragments, row scales,
+    // warps' maxima and sums, prefix sums of tiles
+    static constexpr int kScalesAt = kWarps * kStages * kStageBytes;
+    static constexpr int kQAt = kScalesAt + kWarps * kStages * 16;
+    static constexpr int kRowScaleAt = kQAt + kNT * kSteps * 32 * 8;
+    static constexpr int kMaxAt = kRowScaleAt + kRows * 4;
+    static constexpr int kSumAt = kMaxAt + kWarps * kRows * 4;
+    static constexpr int kPrefixAt = kSumAt + kWarps * kRows * 4;
+    static constexpr int kBytes = kPrefixAt + (kKv8MaxBatch + 1) * 8;
+    // fp32 words of one partial state: O, maxima, sums
+    static constexpr int kPartial = kRows * kDim + 2 * kRows;
+    static_assert(kRows * kRowFloats * 4 <= kStages * kStageBytes, "states fit a warp's ring");
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kPrefixAt % 8 == 0, "alignment");
+};
+
+// The keys of one unit: [lo, hi) and the sinks in front, as tiles.
+struct Keys {
+    int lo, hi;        // hi <= 0: none
+    int lo_max, hi_min;  // visible to every row of the tile
+    int sink_tiles, tiles;
+};
+
+template <int kTile, int kRows>
+__device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int len, int r) {
+    Keys k;
+    const int i0 = r * kRows / a.group;
+    const int i1 = min((r * kRows + kRows - 1) / a.group, len - 1);
+    k.hi_min = first + i0 + 1;
+    k.hi = first + i1 + 1;
+    k.lo = a.window > 0 ? max(k.hi_min - a.window, 0) : 0;
+    k.lo_max = a.window > 0 ? max(k.hi - a.window, 0) : 0;
+    const int lo_tile = k.lo / kTile;
+    k.sink_tiles = min((min(a.sinks, k.lo) + kTile - 1) / kTile, lo_tile);
+    // a tile that holds no key writes the empty result
+    k.tiles = k.hi > 0 ? k.sink_tiles + (k.hi + kTile - 1) / kTile - lo_tile : 1;
+    return k;
+}
+
+__device__ __forceinline__ int row_tiles(const AttentionArgs& a, int len, int rows) {
+    return (int)(((long long)len * a.group + rows - 1) / rows);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(full ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool full) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(full ? 4 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float lds32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// Byte offset of 16-byte piece `piece` of row `row` in a tile: rows of 128 or
+// 256 bytes XOR the low piece bits with the row; two 64-byte rows share a line
+// of 128.  With the orders of keys and values below, the 8 (or 16) lanes of
+// one access phase then touch all 32 banks once.
 template <int kDim>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attention_kernel(const AttentionArgs a) {
-    constexpr int kPer = kDim / 32;  // values of the head per lane, as pairs 64 apart
-    const int head = blockIdx.y, t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = kv8_owner(a.bt, t);
-    int hi = 0, lo = 0, sinks = 0;
-    if (b < a.bt.batch) {
-        const Kv8Seq s = kv8_seq(a.bt, b);
-        if (s.bad) kv8_report(a.bt);
-        hi = max(s.kv - s.len + (t - s.q0) + 1, 0);
-        lo = a.window > 0 ? max(hi - a.window, 0) : 0;
-        sinks = min(a.sinks, lo);
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    if constexpr (kDim == 64) {
+        const int line = row >> 1;
+        const int p = (((row & 1) << 2) | piece) ^ (((line & 1) << 1) | ((line & 2) << 1));
+        return line * 128 + p * 16;
     } else {
-        kv8_report(a.bt);
+        return row * kDim + ((piece & ~7) | ((piece ^ row) & 7)) * 16;
     }
-    float q[kPer], o[kPer];
-    const __nv_bfloat16* qh = a.q + t * a.q_stride + (size_t)head * kDim;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        q[i] = __bfloat162float(qh[i * 32 + lane]);
-        o[i] = 0.0f;
+}
+
+// Bytes of w that are E4M3's NaN, as 0x80 each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+template <int kDim, int kNT>
+class Worker {
+    using S = Shape<kDim, kNT>;
+    static constexpr int kTile = S::kTile;
+    static constexpr int kMt = kTile / 16;              // m16 tiles of keys
+    static constexpr int kGroupMt = kNT == 4 ? 1 : kMt;  // of them per softmax step
+    static constexpr bool kQInRegs = kNT < 4;
+    static constexpr int kWords = kDim / 32;  // 32-bit words of a value row that a lane holds
+
+public:
+    const AttentionArgs& a;
+    const int lane, warp, g, c, tg;
+    const uint32_t smem;
+    // the unit
+    int b, head, first, len, q0, r;
+    Keys keys;
+    // the state: column pairs (2c, 2c + 1) of each n8 tile
+    float o[kNT][S::kSteps][4];
+    float top[kNT][2], sum[kNT][2];
+    uint2 qf[kQInRegs ? kNT : 1][kQInRegs ? S::kSteps : 1];
+    float row_scale[kNT][2];
+    int page[2];  // pages of the next tile to be copied: -1 outside the cache, -2 no key
+
+    __device__ __forceinline__ Worker(const AttentionArgs& args, uint32_t base)
+        : a(args), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), g(lane >> 2), c(lane & 3),
+          tg(((lane >> 2) & 1) << 2 | (lane >> 3)), smem(base) {}
+
+    __device__ __forceinline__ int tile_start(int x) const {
+        return (x < keys.sink_tiles ? x : keys.lo / kTile + x - keys.sink_tiles) * kTile;
     }
-    const int size = 1 << a.bt.page_shift, kv_head = head / a.group;
-    float m = -INFINITY, l = 0.0f;
-    for (int x = warp; x < sinks + hi - lo; x += kWarps) {
-        const int j = x < sinks ? x : lo + x - sinks;
-        const int page = kv8_page(a.bt, a.c, b, j >> a.bt.page_shift);
-        if (page < 0) continue;
-        const size_t at = (size_t)page * a.c.kv_heads + kv_head;
-        const size_t row = (at << a.bt.page_shift) + (j & (size - 1));
-        const uint8_t* k = a.c.k_codes + row * kDim;
-        const uint8_t* v = a.c.v_codes + row * kDim;
-        float s = 0.0f;
+
+    __device__ __forceinline__ void find_pages(int x, int end) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s = fmaf(q[i], e4m3_to_f32(k[i * 32 + lane]), s);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale * a.c.k_scales[at];
-        const float top = fmaxf(m, s);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float keep = expf(m - base), p = expf(s - base);
-        const float pv = p * a.c.v_scales[at];
-        l = l * keep + p;
-        m = top;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + pv * e4m3_to_f32(v[i * 32 + lane]);
+        for (int h = 0; h < kMt; ++h) {
+            const int j = tile_start(x) + 16 * h;
+            page[h] = -2;
+            if (x < end && j < keys.hi) {
+                const int p = a.bt.page_table[(size_t)b * a.bt.table_width + (j >> a.bt.page_shift)];
+                page[h] = p >= 0 && p < a.c.pages ? p : -1;
+            }
+        }
     }
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kDim];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+
+    // Starts the copy of tile x (pages found before) and finds the pages of the
+    // warp's next one.
+    __device__ __forceinline__ void issue(int x, int end, int stage) {
+        if (x < end) {
+            const uint32_t dst = smem + (warp * S::kStages + stage) * S::kStageBytes;
+            const int j0 = tile_start(x);
+            const int mask = (1 << a.bt.page_shift) - 1;
+            size_t from[kMt];
+#pragma unroll
+            for (int h = 0; h < kMt; ++h) {
+                const size_t at = (size_t)max(page[h], 0) * a.c.kv_heads + head;
+                from[h] = ((at << a.bt.page_shift) + ((j0 + 16 * h) & mask)) * kDim;
+                if (page[h] == -1 && lane == 0) kv8_report(a.bt);
+            }
+            constexpr int kPieces = kDim / 16;
+            constexpr int kIters = kTile * kPieces / 32;
+#pragma unroll
+            for (int it = 0; it < kIters; ++it) {
+                const int row = (it * 32 + lane) / kPieces, piece = (it * 32 + lane) % kPieces;
+                // both halves of an iteration lie in the same 16 rows
+                const int h = (it * 32) / (16 * kPieces);
+                const int j = j0 + row;
+                const bool live =
+                    page[h] >= 0 && j < keys.hi && (j >= keys.lo || j < a.sinks);
+                const size_t off = from[h] + (row - 16 * h) * kDim + piece * 16;
+                const uint32_t to = dst + piece_at<kDim>(row, piece);
+                cp_async16(to, a.c.k_codes + (live ? off : 0), live);
+                cp_async16(to + kTile * kDim, a.c.v_codes + (live ? off : 0), live);
+            }
+            if (lane < 2 * kMt) {
+                const int p = kMt == 2 && (lane & 1) ? page[kMt - 1] : page[0];
+                const float* s = lane < kMt ? a.c.k_scales : a.c.v_scales;
+                const uint32_t to =
+                    smem + S::kScalesAt + (warp * S::kStages + stage) * 16 + lane * 4;
+                cp_async4(to, s + (p >= 0 ? (size_t)p * a.c.kv_heads + head : 0), p >= 0);
+            }
+            find_pages(x + kWarps, end);
+        }
+        cp_async_commit();
     }
+
+    // q rows of n-tile `nt` as operand fragments, by one warp: lane (g, c) holds
+    // row g's values 16 (c + 4h) + 4j + 0..3 for step 4h + j.
+    __device__ __forceinline__ void stage_q(int nt) {
+        const int row = r * S::kRows + nt * 8 + g;
+        const int i = row / a.group;
+        const bool live = i < len;
+        const __nv_bfloat16* src =
+            a.q + (long long)(q0 + (live ? i : 0)) * a.q_stride +
+            (size_t)(head * a.group + (live ? row - i * a.group : 0)) * kDim;
+        uint32_t w[kDim / 64][8];
+        float big = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) so[warp][i * 32 + lane] = o[i];
-    __syncthreads();
-    float top = -INFINITY;
+        for (int h = 0; h < kDim / 64; ++h) {
+            const uint4* p = reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h));
+            const uint4 x = live ? p[0] : make_uint4(0, 0, 0, 0);
+            const uint4 y = live ? p[1] : make_uint4(0, 0, 0, 0);
+            w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
+            w[h][4] = y.x, w[h][5] = y.y, w[h][6] = y.z, w[h][7] = y.w;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float total = 0.0f;
+            for (int e = 0; e < 8; ++e)
+                big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[h][e])), fabsf(bf16_hi(w[h][e]))));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^e that brings the row's largest value into [2^14, 2^15)
+        const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 126);
+        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+        const uint32_t at = smem + S::kQAt + nt * S::kSteps * 256 + lane * 8;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sl[w] * expf(sm[w] - base);
-    for (int d = threadIdx.x; d < kDim; d += kWarps * 32) {
-        float v = 0.0f;
+        for (int h = 0; h < kDim / 64; ++h)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += so[w][d] * expf(sm[w] - base);
-        const float r = total == 0.0f ? 0.0f : v / total;
-        a.out[((size_t)t * a.heads + head) * kDim + d] = __float2bfloat16_rn(r);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u0 = w[h][2 * j], u1 = w[h][2 * j + 1];
+                asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (4 * h + j) * 256),
+                             "r"(f16x2(bf16_lo(u0) * up, bf16_hi(u0) * up)),
+                             "r"(f16x2(bf16_lo(u1) * up, bf16_hi(u1) * up))
+                             : "memory");
+            }
+        if (c == 0)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + S::kRowScaleAt + (nt * 8 + g) * 4),
+                         "f"(a.scale * __uint_as_float((uint32_t)(127 - e) << 23))
+                         : "memory");
     }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[(size_t)t * a.heads + head] = total == 0.0f ? -INFINITY : base + logf(total);
+
+    __device__ __forceinline__ void begin() {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+            for (int m = 0; m < S::kSteps; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[nt][e] = -INFINITY;
+                sum[nt][e] = 0.0f;
+                row_scale[nt][e] = lds32(smem + S::kRowScaleAt + (nt * 8 + 2 * c + e) * 4);
+            }
+            if constexpr (kQInRegs)
+#pragma unroll
+                for (int k = 0; k < S::kSteps; ++k)
+                    qf[nt][k] = lds64(smem + S::kQAt + (nt * S::kSteps + k) * 256 + lane * 8);
+        }
+    }
+
+    __device__ __forceinline__ uint2 q_fragment(int nt, int k) const {
+        if constexpr (kQInRegs)
+            return qf[nt][k];
+        else
+            return lds64(smem + S::kQAt + (nt * S::kSteps + k) * 256 + lane * 8);
+    }
+
+    // Whether row column e of n-tile nt sees key j.
+    __device__ __forceinline__ bool sees(int nt, int e, int j, bool page_ok) const {
+        const int i = (r * S::kRows + nt * 8 + 2 * c + e) / a.group;
+        const int hi = first + i + 1;
+        const int lo = a.window > 0 ? hi - a.window : 0;
+        return page_ok && i < len && j < hi && (j >= lo || j < a.sinks);
+    }
+
+    // V^T fragments (values g and g + 8 of m16 tiles 2i and 2i + 1) of four keys'
+    // words x0..x3, times P^T.
+    template <bool kSecond>
+    __device__ __forceinline__ static void v_fragment(uint32_t x0, uint32_t x1, uint32_t x2,
+                                                      uint32_t x3, uint32_t (&f)[4]) {
+        const uint32_t lo = prmt(x0, x1, kSecond ? 0x7362 : 0x5140);
+        const uint32_t hi = prmt(x2, x3, kSecond ? 0x7362 : 0x5140);
+        f[0] = e4m3x2_to_f16x2(lo);
+        f[1] = e4m3x2_hi_to_f16x2(lo);
+        f[2] = e4m3x2_to_f16x2(hi);
+        f[3] = e4m3x2_hi_to_f16x2(hi);
+    }
+
+    // One m16 tile of keys: O^T += V^T P^T.  guard: some row does not see some
+    // key of the tile; a NaN value then must not reach it through 0 * NaN, so
+    // NaNs are taken out of the product and put into the rows that see them.
+    __device__ __forceinline__ void accumulate(uint32_t v_at, int mt, const uint32_t (&p)[kNT][2],
+                                               bool guard, int j0, bool page_ok) {
+        uint32_t w[4][kWords];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = mt * 16 + 4 * k + c;
+            if constexpr (kDim == 64) {
+                const uint2 x = lds64(v_at + piece_at<64>(row, g >> 1) + (g & 1) * 8);
+                w[k][0] = x.x, w[k][1] = x.y;
+            } else {
+#pragma unroll
+                for (int u = 0; u < kDim / 128; ++u) {
+                    const uint4 x = lds128(v_at + piece_at<kDim>(row, tg + 8 * u));
+                    w[k][4 * u] = x.x, w[k][4 * u + 1] = x.y;
+                    w[k][4 * u + 2] = x.z, w[k][4 * u + 3] = x.w;
+                }
+            }
+        }
+        if (guard) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) any |= nan_bytes(w[k][i]);
+            if (__any_sync(0xffffffffu, any != 0)) {
+                // 1 where a row sees a key
+                uint32_t see[kNT][2];
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = j0 + mt * 16 + tg + 8 * e;
+                        see[nt][e] = transpose8x8(f16x2(sees(nt, 0, j, page_ok) ? 1.0f : 0.0f,
+                                                        sees(nt, 1, j, page_ok) ? 1.0f : 0.0f));
+                    }
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t bad = nan_bytes(w[k][i]) >> 7;
+                        w[k][i] &= ~(bad * 0xffu);
+                        x[k] = bad * 0x38u;  // E4M3's 1
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t f[4];
+                        if (half)
+                            v_fragment<true>(x[0], x[1], x[2], x[3], f);
+                        else
+                            v_fragment<false>(x[0], x[1], x[2], x[3], f);
+#pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt) {
+                            float seen[4];
+                            mma_f16_16816_zero(seen, f[0], f[1], f[2], f[3], see[nt][0],
+                                               see[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (seen[e] > 0.0f) o[nt][2 * i + half][e] = NAN;
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t f[4];
+            v_fragment<false>(w[0][i], w[1][i], w[2][i], w[3][i], f);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+                mma_f16_16816(o[nt][2 * i], f[0], f[1], f[2], f[3], p[nt][0], p[nt][1]);
+            v_fragment<true>(w[0][i], w[1][i], w[2][i], w[3][i], f);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+                mma_f16_16816(o[nt][2 * i + 1], f[0], f[1], f[2], f[3], p[nt][0], p[nt][1]);
+        }
+    }
+
+    __device__ __forceinline__ void consume(int x, int stage) {
+        const uint32_t k_at = smem + (warp * S::kStages + stage) * S::kStageBytes;
+        const uint32_t v_at = k_at + kTile * kDim;
+        const uint32_t scales = smem + S::kScalesAt + (warp * S::kStages + stage) * 16;
+        const int j0 = tile_start(x);
+        bool page_ok[kMt];
+        float ks[kMt], vs[kMt];
+        bool guard = j0 + kTile > keys.hi_min ||
+                     (j0 < keys.lo_max && j0 + kTile > a.sinks);
+#pragma unroll
+        for (int m = 0; m < kMt; ++m) {
+            ks[m] = lds32(scales + m * 4);
+            vs[m] = lds32(scales + (kMt + m) * 4);
+            page_ok[m] = vs[m] > 0.0f;  // copied as 0 without a page
+            guard |= !page_ok[m];
+            vs[m] = fmaxf(vs[m], 1.17549435e-38f);
+        }
+#pragma unroll
+        for (int m0 = 0; m0 < kMt; m0 += kGroupMt) {
+            float s[kGroupMt][kNT][4];
+#pragma unroll
+            for (int m = 0; m < kGroupMt; ++m) {
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[m][nt][e] = 0.0f;
+#pragma unroll
+                for (int h = 0; h < kDim / 64; ++h) {
+                    const int row = (m0 + m) * 16 + tg;
+                    const uint4 x = lds128(k_at + piece_at<kDim>(row, c + 4 * h));
+                    const uint4 y = lds128(k_at + piece_at<kDim>(row + 8, c + 4 * h));
+                    const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a0 = e4m3x2_to_f16x2(wx[j]), a2 = e4m3x2_hi_to_f16x2(wx[j]);
+                        const uint32_t a1 = e4m3x2_to_f16x2(wy[j]), a3 = e4m3x2_hi_to_f16x2(wy[j]);
+#pragma unroll
+                        for (int nt = 0; nt < kNT; ++nt) {
+                            const uint2 q = q_fragment(nt, 4 * h + j);
+                            mma_f16_16816(s[m][nt], a0, a1, a2, a3, q.x, q.y);
+                        }
+                    }
+                }
+            }
+            // t = log2(e) s + log2(v_scale), maxima over the keys
+            float most[kNT][2];
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) most[nt][0] = most[nt][1] = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < kGroupMt; ++m) {
+                const float lv = __log2f(vs[m0 + m]);
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float t = fmaf(s[m][nt][e], row_scale[nt][e & 1] * ks[m0 + m], lv);
+                        if (guard) {
+                            const int j = j0 + (m0 + m) * 16 + tg + 8 * (e >> 1);
+                            if (!sees(nt, e & 1, j, page_ok[m0 + m])) t = -INFINITY;
+                        }
+                        s[m][nt][e] = t;
+                        most[nt][e & 1] = fmaxf(most[nt][e & 1], t);
+                    }
+            }
+            bool grown = false;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = most[nt][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                    most[nt][e] = fmaxf(v, top[nt][e]);
+                    grown |= v > top[nt][e];
+                }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float keep =
+                            most[nt][e] == -INFINITY ? 1.0f : exp2_fast(top[nt][e] - most[nt][e]);
+                        top[nt][e] = most[nt][e];
+                        sum[nt][e] *= keep;
+#pragma unroll
+                        for (int m = 0; m < S::kSteps; ++m) {
+                            o[nt][m][e] *= keep;
+                            o[nt][m][e + 2] *= keep;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < kGroupMt; ++m) {
+                const float inv = __fdividef(1.0f, vs[m0 + m]);
+                uint32_t p[kNT][2];
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float base = top[nt][e & 1] == -INFINITY ? 0.0f : top[nt][e & 1];
+                        w[e] = exp2_fast(s[m][nt][e] - (base - kBias));
+                    }
+                    sum[nt][0] = fmaf(w[0] + w[2], inv, sum[nt][0]);
+                    sum[nt][1] = fmaf(w[1] + w[3], inv, sum[nt][1]);
+                    p[nt][0] = transpose8x8(f16x2(w[0], w[1]));
+                    p[nt][1] = transpose8x8(f16x2(w[2], w[3]));
+                }
+                accumulate(v_at, m0 + m, p, guard, j0, page_ok[m0 + m]);
+            }
+        }
+    }
+
+    // The warp's state into its part of shared memory.
+    __device__ __forceinline__ void put_state() {
+        const uint32_t mine = smem + warp * S::kStages * S::kStageBytes;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = sum[nt][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                const int row = nt * 8 + 2 * c + e;
+                if (g == 0) {
+                    const uint32_t at = smem + (warp * S::kRows + row) * 4;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + S::kMaxAt), "f"(top[nt][e])
+                                 : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + S::kSumAt), "f"(v)
+                                 : "memory");
+                }
+#pragma unroll
+                for (int m = 0; m < S::kSteps; ++m) {
+                    // value of the head: pairs within the lane's 16-byte (8-byte) pieces
+                    const int d = kDim == 64 ? 8 * g + 2 * m
+                                             : 16 * (tg + 8 * (m / 8)) + 2 * (m % 8);
+                    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(
+                                     mine + (row * S::kRowFloats + d) * 4),
+                                 "f"(o[nt][m][e]), "f"(o[nt][m][e + 2])
+                                 : "memory");
+                }
+            }
+    }
+};
+
+// out and lse of one row from its joined state.
+template <int kDim>
+__device__ __forceinline__ void store_row(const AttentionArgs& a, int q0, int len, int head,
+                                          int row, int d, float4 v, float top, float sum) {
+    const int i = row / a.group;
+    if (i >= len) return;
+    const size_t at = (size_t)(q0 + i) * a.heads + head * a.group + (row - i * a.group);
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+    uint2 w;
+    w.x = bf16x2(v.x * inv, v.y * inv);
+    w.y = bf16x2(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(a.out + at * kDim + d) = w;
+    if (d == 0 && a.lse)
+        a.lse[at] = sum == 0.0f ? -INFINITY
+                                : 0.69314718055994531f * ((top - kBias) + log2f(sum));
+}
+
+__device__ __forceinline__ float weight_of(float top, float all) {
+    return all == -INFINITY ? 0.0f : exp2_fast(top - all);
+}
+
+template <int kDim, int kNT>
+__global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const AttentionArgs a) {
+    using S = Shape<kDim, kNT>;
+    extern __shared__ __align__(128) uint8_t shared[];
+    long long* const prefix = reinterpret_cast<long long*>(shared + S::kPrefixAt);
+    __shared__ long long part[kWarps];
+    __shared__ int joins;
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Worker<kDim, kNT> w(a, smem_addr(shared));
+
+    // prefix sums of the sequences' tiles (each block for itself)
+    long long total = 0;
+    if (tid == 0) prefix[0] = 0;
+    for (int b0 = 0; b0 < a.bt.batch; b0 += kThreads) {
+        const int b = b0 + tid;
+        long long n = 0;
+        if (b < a.bt.batch) {
+            const Kv8Seq s = kv8_seq(a.bt, b);
+            if (s.bad) kv8_report(a.bt);
+            const int rt = row_tiles(a, s.len, S::kRows);
+            for (int r = 0; r < rt; ++r)
+                n += unit_keys<S::kTile, S::kRows>(a, s.kv - s.len, s.len, r).tiles;
+            n *= a.c.kv_heads;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, n, d);
+            if (w.lane >= d) n += v;
+        }
+        if (w.lane == 31) part[w.warp] = n;
+        __syncthreads();
+        long long before = total;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < w.warp) before += part[i];
+            total += part[i];
+        }
+        if (b < a.bt.batch) prefix[b + 1] = before + n;
+        __syncthreads();
+    }
+    if (total == 0) return;
+    const long long most = (total + kMinTiles - 1) / kMinTiles;
+    const long long ranges = most < (long long)gridDim.x ? most : (long long)gridDim.x;
+    if ((long long)blockIdx.x >= ranges) return;
+    const long long begin = total * blockIdx.x / ranges;
+    const long long end = total * (blockIdx.x + 1) / ranges;
+
+    for (long long t = begin; t < end;) {
+        // the unit of tile t
+        int lo = 0, hi = a.bt.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const Kv8Seq seq = kv8_seq(a.bt, lo);
+        w.b = lo;
+        w.q0 = seq.q0;
+        w.len = seq.len;
+        w.first = seq.kv - seq.len;
+        const long long per_head = (prefix[lo + 1] - prefix[lo]) / a.c.kv_heads;
+        long long x = t - prefix[lo];
+        w.head = (int)(x / per_head);
+        x -= w.head * per_head;
+        w.r = 0;
+        for (;;) {
+            w.keys = unit_keys<S::kTile, S::kRows>(a, w.first, w.len, w.r);
+            if (x < w.keys.tiles) break;
+            x -= w.keys.tiles;
+            ++w.r;
+        }
+        const int x0 = (int)x;
+        const int x1 = (int)min((long long)w.keys.tiles, x + (end - t));
+        const long long unit_begin = t - x0;
+
+        // the ring's first copies, then q
+        const int mine = x0 + w.warp;
+        w.find_pages(mine, x1);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) w.issue(mine + s * kWarps, x1, s);
+        if (w.warp < kNT) w.stage_q(w.warp);
+        __syncthreads();
+        w.begin();
+        int stage = 0;
+        for (int i = mine; i < x1; i += kWarps) {
+            const int ahead = stage == 0 ? S::kStages - 1 : stage - 1;
+            w.issue(i + (S::kStages - 1) * kWarps, x1, ahead);
+            cp_async_wait<S::kStages - 1>();
+            __syncwarp();
+            w.consume(i, stage);
+            __syncwarp();
+            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+        }
+        cp_async_wait<0>();
+        w.put_state();
+        __syncthreads();
+
+        // the warps' states joined, 4 values of one row per thread
+        const float* tops = reinterpret_cast<const float*>(shared + S::kMaxAt);
+        const float* sums = reinterpret_cast<const float*>(shared + S::kSumAt);
+        const bool whole = x0 == 0 && x1 == w.keys.tiles;
+        const int slot = 2 * blockIdx.x + (t > begin ? 1 : 0);
+        float* const mine_out = a.partials + (size_t)slot * S::kPartial;
+        for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
+            const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) top = fmaxf(top, tops[i * S::kRows + row]);
+            float sum = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float f = weight_of(tops[i * S::kRows + row], top);
+                const float4 y = *reinterpret_cast<const float4*>(
+                    shared + i * S::kStages * S::kStageBytes + (row * S::kRowFloats + d) * 4);
+                sum = fmaf(sums[i * S::kRows + row], f, sum);
+                v.x = fmaf(y.x, f, v.x);
+                v.y = fmaf(y.y, f, v.y);
+                v.z = fmaf(y.z, f, v.z);
+                v.w = fmaf(y.w, f, v.w);
+            }
+            if (whole) {
+                store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v, top, sum);
+            } else {
+                *reinterpret_cast<float4*>(mine_out + row * kDim + d) = v;
+                if (d == 0) {
+                    mine_out[S::kRows * kDim + row] = top;
+                    mine_out[S::kRows * kDim + S::kRows + row] = sum;
+                }
+            }
+        }
+        if (!whole) {
+            // ranges that hold the unit's first and last tile
+            const long long c0 = ((unit_begin + 1) * ranges + total - 1) / total - 1;
+            const long long c1 =
+                ((unit_begin + w.keys.tiles) * ranges + total - 1) / total - 1;
+            const int n = (int)(c1 - c0) + 1;
+            __syncthreads();
+            if (tid == 0) {
+                const int seen = atom_add_acq_rel_gpu(a.counters + c0, 1);
+                joins = seen == n - 1;
+                if (joins) a.counters[c0] = 0;
+            }
+            __syncthreads();
+            if (joins) {
+                const float* from = a.partials;
+                const int s0 = 2 * (int)c0 + (unit_begin > total * c0 / ranges ? 1 : 0);
+                for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
+                    const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
+                    float top = -INFINITY, sum = 0.0f;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int i = 0; i < n; ++i) {
+                        const float* p =
+                            from + (size_t)(i == 0 ? s0 : 2 * ((int)c0 + i)) * S::kPartial;
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kDim + d));
+                        const float yt = __ldcg(p + S::kRows * kDim + row);
+                        const float ys = __ldcg(p + S::kRows * kDim + S::kRows + row);
+                        const float all = fmaxf(top, yt);
+                        const float f = weight_of(top, all), k = weight_of(yt, all);
+                        top = all;
+                        sum = sum * f + ys * k;
+                        v.x = v.x * f + y.x * k;
+                        v.y = v.y * f + y.y * k;
+                        v.z = v.z * f + y.z * k;
+                        v.w = v.w * f + y.w * k;
+                    }
+                    store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v, top, sum);
+                }
+            }
+        }
+        t += x1 - x0;
+        __syncthreads();  // the states' memory becomes the ring again
+    }
+}
+
+template <int kDim, int kNT>
+cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
+    using S = Shape<kDim, kNT>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv8_attention_kernel<kDim, kNT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<kDim, kNT>, a);
 }
 
 }  // namespace
 
 size_t kv8_attention_data_bytes(int head_dim, int num_sms) {
-    (void)head_dim;
-    (void)num_sms;
-    return 256;
+    // two partial states per block, of 32 rows (16 of 256 values)
+    const size_t rows = head_dim == 256 ? 16 : 32;
+    return (size_t)num_sms * 2 * rows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv8_attention(const void* q, long long q_stride, int heads,
                                  const Kv8CacheArgs& c, const Kv8BatchArgs& bt,
                                  float softmax_scale, int window, int sinks, void* out, float* lse,
                                  int* counters, void* partials, int num_sms, cudaStream_t s) {
-    (void)counters;
-    (void)partials;
-    (void)num_sms;
     AttentionArgs a;
     a.c = c;
     a.bt = bt;
     a.q = reinterpret_cast<const __nv_bfloat16*>(q);
     a.out = reinterpret_cast<__nv_bfloat16*>(out);
     a.lse = lse;
+    a.counters = counters;
+    a.partials = reinterpret_cast<float*>(partials);
     a.q_stride = q_stride;
     a.heads = heads;
     a.group = heads / c.kv_heads;
-    a.scale = softmax_scale;
+    a.scale = softmax_scale * 1.4426950408889634f;
     a.window = window;
     a.sinks = sinks;
-    const dim3 grid(bt.tokens, heads);
+    // rows that share a kv head, per sequence on average: the narrowest tile
+    // that holds them reads the cache once
+    const long long rows = ((long long)bt.tokens * a.group + bt.batch - 1) / bt.batch;
     if (c.head_dim == 64)
-        kv8_attention_kernel<64><<<grid, kWarps * 32, 0, s>>>(a);
-    else if (c.head_dim == 128)
-        kv8_attention_kernel<128><<<grid, kWarps * 32, 0, s>>>(a);
-    else
-        kv8_attention_kernel<256><<<grid, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+        return rows <= 8    ? launch<64, 1>(a, num_sms, s)
+               : rows <= 16 ? launch<64, 2>(a, num_sms, s)
+                            : launch<64, 4>(a, num_sms, s);
+    if (c.head_dim == 128)
+        return rows <= 8    ? launch<128, 1>(a, num_sms, s)
+               : rows <= 16 ? launch<128, 2>(a, num_sms, s)
+                            : launch<128, 4>(a, num_sms, s);
+    return rows <= 8 ? launch<256, 1>(a, num_sms, s) : launch<256, 2>(a, num_sms, s);
 }
 
 }  // namespace nvf
