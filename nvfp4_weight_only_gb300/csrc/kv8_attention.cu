@@ -33,6 +33,8 @@
 // key and l = sum P / v_scale restores the denominator.  P is rounded to f16
 // (11 bits, kept normal down to 2^-28 of the largest); t, maxima, l and O are
 // fp32.
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace nvf {
@@ -42,7 +44,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kBias = 14.0f;  // the largest weight is 2^14 in f16
-constexpr int kMinTiles = 8;    // least tiles per block: one per warp
+constexpr int kTile = 16;       // keys per tile: within one page
+constexpr int kMinTiles = 16;   // least tiles per block: two per warp
+constexpr int kUnitCost = 8;    // what a unit costs beside its tiles, in tiles
 
 struct AttentionArgs {
     Kv8CacheArgs c;
@@ -61,35 +65,41 @@ struct AttentionArgs {
 template <int kDim, int kNT>
 struct Shape {
     static constexpr int kRows = 8 * kNT;
-    static constexpr int kTile = kDim == 256 ? 16 : 32;
-    static constexpr int kStages = kDim == 64 ? 6 : 3;
+    // blocks per SM: two where the state leaves room for 128 registers, so that
+    // one block's unit ends and begins under the other's products
+    static constexpr int kBlocks = kNT == 1 && kDim <= 128 ? 2 : 1;
+    static constexpr int kStages = kDim == 64 ? 6 : 3 * (kBlocks == 1 && kDim == 128 ? 2 : 1);
     static constexpr int kStageBytes = 2 * kTile * kDim;
     static constexpr int kSteps = kDim / 16;  // k16 steps of q . k, m16 tiles of the head
     static constexpr int kRowFloats = kDim + 4;
     // shared memory: ring, page scales of each stage, q fragments, row scales,
-    // warps' maxima and sums, prefix sums of tiles
+    // warps' maxima and sums
     static constexpr int kScalesAt = kWarps * kStages * kStageBytes;
-    static constexpr int kQAt = kScalesAt + kWarps * kStages * 16;
+    static constexpr int kQAt = kScalesAt + kWarps * kStages * 8;
     static constexpr int kRowScaleAt = kQAt + kNT * kSteps * 32 * 8;
     static constexpr int kMaxAt = kRowScaleAt + kRows * 4;
     static constexpr int kSumAt = kMaxAt + kWarps * kRows * 4;
-    static constexpr int kPrefixAt = kSumAt + kWarps * kRows * 4;
-    static constexpr int kBytes = kPrefixAt + (kKv8MaxBatch + 1) * 8;
+    static constexpr int kSeqsAt = kSumAt + kWarps * kRows * 4;
+    // then a Seq per sequence
     // fp32 words of one partial state: O, maxima, sums
     static constexpr int kPartial = kRows * kDim + 2 * kRows;
     static_assert(kRows * kRowFloats * 4 <= kStages * kStageBytes, "states fit a warp's ring");
-    static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(kPrefixAt % 8 == 0, "alignment");
+};
+
+// A sequence in shared memory: its new tokens, length, and the tiles of all
+// sequences before it.
+struct Seq {
+    int q0, len, kv, before;
 };
 
 // The keys of one unit: [lo, hi) and the sinks in front, as tiles.
 struct Keys {
-    int lo, hi;        // hi <= 0: none
+    int lo, hi;          // hi <= 0: none
     int lo_max, hi_min;  // visible to every row of the tile
     int sink_tiles, tiles;
 };
 
-template <int kTile, int kRows>
+template <int kRows>
 __device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int len, int r) {
     Keys k;
     const int i0 = r * kRows / a.group;
@@ -191,9 +201,6 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 template <int kDim, int kNT>
 class Worker {
     using S = Shape<kDim, kNT>;
-    static constexpr int kTile = S::kTile;
-    static constexpr int kMt = kTile / 16;              // m16 tiles of keys
-    static constexpr int kGroupMt = kNT == 4 ? 1 : kMt;  // of them per softmax step
     static constexpr bool kQInRegs = kNT < 4;
     static constexpr int kWords = kDim / 32;  // 32-bit words of a value row that a lane holds
 
@@ -209,7 +216,8 @@ public:
     float top[kNT][2], sum[kNT][2];
     uint2 qf[kQInRegs ? kNT : 1][kQInRegs ? S::kSteps : 1];
     float row_scale[kNT][2];
-    int page[2];  // pages of the next tile to be copied: -1 outside the cache, -2 no key
+    int pages;   // lane l: the page of the warp's tile number (in this segment) pages_at + l
+    int pages_at;
 
     __device__ __forceinline__ Worker(const AttentionArgs& args, uint32_t base)
         : a(args), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), g(lane >> 2), c(lane & 3),
@@ -219,120 +227,153 @@ public:
         return (x < keys.sink_tiles ? x : keys.lo / kTile + x - keys.sink_tiles) * kTile;
     }
 
-    __device__ __forceinline__ void find_pages(int x, int end) {
-#pragma unroll
-        for (int h = 0; h < kMt; ++h) {
-            const int j = tile_start(x) + 16 * h;
-            page[h] = -2;
-            if (x < end && j < keys.hi) {
-                const int p = a.bt.page_table[(size_t)b * a.bt.table_width + (j >> a.bt.page_shift)];
-                page[h] = p >= 0 && p < a.c.pages ? p : -1;
+    // Looks up the pages of the warp's tiles x, x + kWarps, ..: -1 outside the
+    // cache, -2 where there is no key.
+    __device__ __forceinline__ void find_pages(int x, int end, int number) {
+        const int mine = x + lane * kWarps;
+        const int j = tile_start(mine);
+        pages = -2;
+        pages_at = number;
+        if (mine < end && j < keys.hi) {
+            pages = a.bt.page_table[(size_t)b * a.bt.table_width + (j >> a.bt.page_shift)];
+            if (pages < 0 || pages >= a.c.pages) {
+                pages = -1;
+                kv8_report(a.bt);
             }
         }
     }
 
-    // Starts the copy of tile x (pages found before) and finds the pages of the
-    // warp's next one.
-    __device__ __forceinline__ void issue(int x, int end, int stage) {
+    // Starts the copy of tile x, the warp's number-th of the segment.
+    __device__ __forceinline__ void issue(int x, int end, int number, int stage) {
         if (x < end) {
+            if (number - pages_at == 32) find_pages(x, end, number);
+            const int page = __shfl_sync(0xffffffffu, pages, number - pages_at);
             const uint32_t dst = smem + (warp * S::kStages + stage) * S::kStageBytes;
             const int j0 = tile_start(x);
-            const int mask = (1 << a.bt.page_shift) - 1;
-            size_t from[kMt];
-#pragma unroll
-            for (int h = 0; h < kMt; ++h) {
-                const size_t at = (size_t)max(page[h], 0) * a.c.kv_heads + head;
-                from[h] = ((at << a.bt.page_shift) + ((j0 + 16 * h) & mask)) * kDim;
-                if (page[h] == -1 && lane == 0) kv8_report(a.bt);
-            }
+            const size_t at = (size_t)max(page, 0) * a.c.kv_heads + head;
+            const size_t from =
+                ((at << a.bt.page_shift) + (j0 & ((1 << a.bt.page_shift) - 1))) * kDim;
             constexpr int kPieces = kDim / 16;
-            constexpr int kIters = kTile * kPieces / 32;
 #pragma unroll
-            for (int it = 0; it < kIters; ++it) {
+            for (int it = 0; it < kPieces / 2; ++it) {
                 const int row = (it * 32 + lane) / kPieces, piece = (it * 32 + lane) % kPieces;
-                // both halves of an iteration lie in the same 16 rows
-                const int h = (it * 32) / (16 * kPieces);
                 const int j = j0 + row;
-                const bool live =
-                    page[h] >= 0 && j < keys.hi && (j >= keys.lo || j < a.sinks);
-                const size_t off = from[h] + (row - 16 * h) * kDim + piece * 16;
+                // keys that no row sees are copied as zeros
+                const bool live = page >= 0 && j < keys.hi && (j >= keys.lo || j < a.sinks);
+                const size_t off = live ? from + (it * 32 + lane) * 16 : 0;
                 const uint32_t to = dst + piece_at<kDim>(row, piece);
-                cp_async16(to, a.c.k_codes + (live ? off : 0), live);
-                cp_async16(to + kTile * kDim, a.c.v_codes + (live ? off : 0), live);
+                cp_async16(to, a.c.k_codes + off, live);
+                cp_async16(to + kTile * kDim, a.c.v_codes + off, live);
             }
-            if (lane < 2 * kMt) {
-                const int p = kMt == 2 && (lane & 1) ? page[kMt - 1] : page[0];
-                const float* s = lane < kMt ? a.c.k_scales : a.c.v_scales;
+            if (lane < 2) {
                 const uint32_t to =
-                    smem + S::kScalesAt + (warp * S::kStages + stage) * 16 + lane * 4;
-                cp_async4(to, s + (p >= 0 ? (size_t)p * a.c.kv_heads + head : 0), p >= 0);
+                    smem + S::kScalesAt + (warp * S::kStages + stage) * 8 + lane * 4;
+                cp_async4(to, (lane ? a.c.v_scales : a.c.k_scales) + at, page >= 0);
             }
-            find_pages(x + kWarps, end);
         }
         cp_async_commit();
     }
 
-    // q rows of n-tile `nt` as operand fragments, by one warp: lane (g, c) holds
-    // row g's values 16 (c + 4h) + 4j + 0..3 for step 4h + j.
-    __device__ __forceinline__ void stage_q(int nt) {
+    // Lane (g, c)'s share of row g of n-tile nt of q: values 16 (c + 4h) .. + 15.
+    struct QRow {
+        uint4 w[kDim / 64][2];
+    };
+
+    __device__ __forceinline__ QRow load_q(int nt) const {
         const int row = r * S::kRows + nt * 8 + g;
         const int i = row / a.group;
         const bool live = i < len;
         const __nv_bfloat16* src =
             a.q + (long long)(q0 + (live ? i : 0)) * a.q_stride +
             (size_t)(head * a.group + (live ? row - i * a.group : 0)) * kDim;
-        uint32_t w[kDim / 64][8];
-        float big = 0.0f;
-#pragma unroll
-        for (int h = 0; h < kDim / 64; ++h) {
-            const uint4* p = reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h));
-            const uint4 x = live ? p[0] : make_uint4(0, 0, 0, 0);
-            const uint4 y = live ? p[1] : make_uint4(0, 0, 0, 0);
-            w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
-            w[h][4] = y.x, w[h][5] = y.y, w[h][6] = y.z, w[h][7] = y.w;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[h][e])), fabsf(bf16_hi(w[h][e]))));
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // 2^e that brings the row's largest value into [2^14, 2^15)
-        const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 126);
-        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-        const uint32_t at = smem + S::kQAt + nt * S::kSteps * 256 + lane * 8;
+        QRow q;
 #pragma unroll
         for (int h = 0; h < kDim / 64; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t u0 = w[h][2 * j], u1 = w[h][2 * j + 1];
-                asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (4 * h + j) * 256),
-                             "r"(f16x2(bf16_lo(u0) * up, bf16_hi(u0) * up)),
-                             "r"(f16x2(bf16_lo(u1) * up, bf16_hi(u1) * up))
-                             : "memory");
+            for (int e = 0; e < 2; ++e)
+                q.w[h][e] = live ? reinterpret_cast<const uint4*>(src + 16 * (c + 4 * h))[e]
+                                 : make_uint4(0, 0, 0, 0);
+        return q;
+    }
+
+    // Scales the row by a power of two into f16 operand fragments (lane's values
+    // 16 (c + 4h) + 4j + 0..3 for step 4h + j); returns the scale of its scores.
+    __device__ __forceinline__ float make_fragments(const QRow& q, uint2 (&f)[S::kSteps]) const {
+        float big = 0.0f;
+#pragma unroll
+        for (int h = 0; h < kDim / 64; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t w[4] = {q.w[h][e].x, q.w[h][e].y, q.w[h][e].z, q.w[h][e].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
             }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^e brings the row's largest value into [2^14, 2^15)
+        const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 126);
+        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+        for (int h = 0; h < kDim / 64; ++h)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+                const uint32_t w[4] = {q.w[h][e2].x, q.w[h][e2].y, q.w[h][e2].z, q.w[h][e2].w};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    f[4 * h + 2 * e2 + i] =
+                        make_uint2(f16x2(bf16_lo(w[2 * i]) * up, bf16_hi(w[2 * i]) * up),
+                                   f16x2(bf16_lo(w[2 * i + 1]) * up, bf16_hi(w[2 * i + 1]) * up));
+            }
+        return a.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+
+    // Fragments of n-tile nt into shared memory (where registers do not hold
+    // all rows'), by one warp.
+    __device__ __forceinline__ void stage_q(int nt) {
+        uint2 f[S::kSteps];
+        const float scale = make_fragments(load_q(nt), f);
+#pragma unroll
+        for (int k = 0; k < S::kSteps; ++k)
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(
+                             smem + S::kQAt + (nt * S::kSteps + k) * 256 + lane * 8),
+                         "r"(f[k].x), "r"(f[k].y)
+                         : "memory");
         if (c == 0)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + S::kRowScaleAt + (nt * 8 + g) * 4),
-                         "f"(a.scale * __uint_as_float((uint32_t)(127 - e) << 23))
+                         "f"(scale)
                          : "memory");
     }
 
     __device__ __forceinline__ void begin() {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-            for (int m = 0; m < S::kSteps; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.0f;
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 top[nt][e] = -INFINITY;
                 sum[nt][e] = 0.0f;
-                row_scale[nt][e] = lds32(smem + S::kRowScaleAt + (nt * 8 + 2 * c + e) * 4);
-            }
-            if constexpr (kQInRegs)
 #pragma unroll
-                for (int k = 0; k < S::kSteps; ++k)
-                    qf[nt][k] = lds64(smem + S::kQAt + (nt * S::kSteps + k) * 256 + lane * 8);
+                for (int m = 0; m < S::kSteps; ++m) o[nt][m][e] = o[nt][m][e + 2] = 0.0f;
+            }
+    }
+
+    // Rows' scales from the lanes (or shared memory) that hold them to the
+    // column pairs of the scores.
+    __device__ __forceinline__ void take_q(const QRow (&q)[kQInRegs ? kNT : 1]) {
+        if constexpr (kQInRegs) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const float v = make_fragments(q[nt], qf[nt]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    row_scale[nt][e] = __shfl_sync(0xffffffffu, v, 8 * c + 4 * e);
+            }
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    row_scale[nt][e] = lds32(smem + S::kRowScaleAt + (nt * 8 + 2 * c + e) * 4);
         }
     }
 
@@ -364,15 +405,15 @@ public:
         f[3] = e4m3x2_hi_to_f16x2(hi);
     }
 
-    // One m16 tile of keys: O^T += V^T P^T.  guard: some row does not see some
+    // O^T += V^T P^T.  guard: some row does not see some
     // key of the tile; a NaN value then must not reach it through 0 * NaN, so
     // NaNs are taken out of the product and put into the rows that see them.
-    __device__ __forceinline__ void accumulate(uint32_t v_at, int mt, const uint32_t (&p)[kNT][2],
+    __device__ __forceinline__ void accumulate(uint32_t v_at, const uint32_t (&p)[kNT][2],
                                                bool guard, int j0, bool page_ok) {
         uint32_t w[4][kWords];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int row = mt * 16 + 4 * k + c;
+            const int row = 4 * k + c;
             if constexpr (kDim == 64) {
                 const uint2 x = lds64(v_at + piece_at<64>(row, g >> 1) + (g & 1) * 8);
                 w[k][0] = x.x, w[k][1] = x.y;
@@ -398,7 +439,7 @@ public:
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int j = j0 + mt * 16 + tg + 8 * e;
+                        const int j = j0 + tg + 8 * e;
                         see[nt][e] = transpose8x8(f16x2(sees(nt, 0, j, page_ok) ? 1.0f : 0.0f,
                                                         sees(nt, 1, j, page_ok) ? 1.0f : 0.0f));
                     }
@@ -448,115 +489,88 @@ public:
     __device__ __forceinline__ void consume(int x, int stage) {
         const uint32_t k_at = smem + (warp * S::kStages + stage) * S::kStageBytes;
         const uint32_t v_at = k_at + kTile * kDim;
-        const uint32_t scales = smem + S::kScalesAt + (warp * S::kStages + stage) * 16;
+        const uint32_t scales = smem + S::kScalesAt + (warp * S::kStages + stage) * 8;
         const int j0 = tile_start(x);
-        bool page_ok[kMt];
-        float ks[kMt], vs[kMt];
-        bool guard = j0 + kTile > keys.hi_min ||
-                     (j0 < keys.lo_max && j0 + kTile > a.sinks);
+        const float ks = lds32(scales);
+        float vs = lds32(scales + 4);
+        const bool page_ok = vs > 0.0f;  // copied as 0 without a page
+        const bool guard = !page_ok || j0 + kTile > keys.hi_min ||
+                           (j0 < keys.lo_max && j0 + kTile > a.sinks);
+        vs = fmaxf(vs, 1.17549435e-38f);
+        float s[kNT][4];
 #pragma unroll
-        for (int m = 0; m < kMt; ++m) {
-            ks[m] = lds32(scales + m * 4);
-            vs[m] = lds32(scales + (kMt + m) * 4);
-            page_ok[m] = vs[m] > 0.0f;  // copied as 0 without a page
-            guard |= !page_ok[m];
-            vs[m] = fmaxf(vs[m], 1.17549435e-38f);
-        }
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int m0 = 0; m0 < kMt; m0 += kGroupMt) {
-            float s[kGroupMt][kNT][4];
+            for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
 #pragma unroll
-            for (int m = 0; m < kGroupMt; ++m) {
+        for (int h = 0; h < kDim / 64; ++h) {
+            const uint4 x = lds128(k_at + piece_at<kDim>(tg, c + 4 * h));
+            const uint4 y = lds128(k_at + piece_at<kDim>(tg + 8, c + 4 * h));
+            const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = e4m3x2_to_f16x2(wx[j]), a2 = e4m3x2_hi_to_f16x2(wx[j]);
+                const uint32_t a1 = e4m3x2_to_f16x2(wy[j]), a3 = e4m3x2_hi_to_f16x2(wy[j]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[m][nt][e] = 0.0f;
-#pragma unroll
-                for (int h = 0; h < kDim / 64; ++h) {
-                    const int row = (m0 + m) * 16 + tg;
-                    const uint4 x = lds128(k_at + piece_at<kDim>(row, c + 4 * h));
-                    const uint4 y = lds128(k_at + piece_at<kDim>(row + 8, c + 4 * h));
-                    const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a0 = e4m3x2_to_f16x2(wx[j]), a2 = e4m3x2_hi_to_f16x2(wx[j]);
-                        const uint32_t a1 = e4m3x2_to_f16x2(wy[j]), a3 = e4m3x2_hi_to_f16x2(wy[j]);
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) {
-                            const uint2 q = q_fragment(nt, 4 * h + j);
-                            mma_f16_16816(s[m][nt], a0, a1, a2, a3, q.x, q.y);
-                        }
-                    }
+                for (int nt = 0; nt < kNT; ++nt) {
+                    const uint2 q = q_fragment(nt, 4 * h + j);
+                    mma_f16_16816(s[nt], a0, a1, a2, a3, q.x, q.y);
                 }
             }
-            // t = log2(e) s + log2(v_scale), maxima over the keys
-            float most[kNT][2];
+        }
+        // t = log2(e) s + log2(v_scale), maxima over the keys
+        const float lv = __log2f(vs);
+        bool grown = false;
+        float most[kNT][2];
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) most[nt][0] = most[nt][1] = -INFINITY;
+        for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-            for (int m = 0; m < kGroupMt; ++m) {
-                const float lv = __log2f(vs[m0 + m]);
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float t = fmaf(s[m][nt][e], row_scale[nt][e & 1] * ks[m0 + m], lv);
-                        if (guard) {
-                            const int j = j0 + (m0 + m) * 16 + tg + 8 * (e >> 1);
-                            if (!sees(nt, e & 1, j, page_ok[m0 + m])) t = -INFINITY;
-                        }
-                        s[m][nt][e] = t;
-                        most[nt][e & 1] = fmaxf(most[nt][e & 1], t);
-                    }
+            for (int e = 0; e < 4; ++e) {
+                float t = fmaf(s[nt][e], row_scale[nt][e & 1] * ks, lv);
+                if (guard && !sees(nt, e & 1, j0 + tg + 8 * (e >> 1), page_ok)) t = -INFINITY;
+                s[nt][e] = t;
             }
-            bool grown = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                grown |= v > top[nt][e];
+                most[nt][e] = fmaxf(v, top[nt][e]);
+            }
+        }
+        if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float v = most[nt][e];
+                    const float keep =
+                        most[nt][e] == -INFINITY ? 1.0f : exp2_fast(top[nt][e] - most[nt][e]);
+                    top[nt][e] = most[nt][e];
+                    sum[nt][e] *= keep;
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                    most[nt][e] = fmaxf(v, top[nt][e]);
-                    grown |= v > top[nt][e];
-                }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float keep =
-                            most[nt][e] == -INFINITY ? 1.0f : exp2_fast(top[nt][e] - most[nt][e]);
-                        top[nt][e] = most[nt][e];
-                        sum[nt][e] *= keep;
-#pragma unroll
-                        for (int m = 0; m < S::kSteps; ++m) {
-                            o[nt][m][e] *= keep;
-                            o[nt][m][e + 2] *= keep;
-                        }
+                    for (int m = 0; m < S::kSteps; ++m) {
+                        o[nt][m][e] *= keep;
+                        o[nt][m][e + 2] *= keep;
                     }
-            }
-#pragma unroll
-            for (int m = 0; m < kGroupMt; ++m) {
-                const float inv = __fdividef(1.0f, vs[m0 + m]);
-                uint32_t p[kNT][2];
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float base = top[nt][e & 1] == -INFINITY ? 0.0f : top[nt][e & 1];
-                        w[e] = exp2_fast(s[m][nt][e] - (base - kBias));
-                    }
-                    sum[nt][0] = fmaf(w[0] + w[2], inv, sum[nt][0]);
-                    sum[nt][1] = fmaf(w[1] + w[3], inv, sum[nt][1]);
-                    p[nt][0] = transpose8x8(f16x2(w[0], w[1]));
-                    p[nt][1] = transpose8x8(f16x2(w[2], w[3]));
                 }
-                accumulate(v_at, m0 + m, p, guard, j0, page_ok[m0 + m]);
-            }
         }
+        const float inv = __fdividef(1.0f, vs);
+        uint32_t p[kNT][2];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float base = top[nt][e & 1] == -INFINITY ? 0.0f : top[nt][e & 1];
+                w[e] = exp2_fast(s[nt][e] - (base - kBias));
+            }
+            sum[nt][0] = fmaf(w[0] + w[2], inv, sum[nt][0]);
+            sum[nt][1] = fmaf(w[1] + w[3], inv, sum[nt][1]);
+            p[nt][0] = transpose8x8(f16x2(w[0], w[1]));
+            p[nt][1] = transpose8x8(f16x2(w[2], w[3]));
+        }
+        accumulate(v_at, p, guard, j0, page_ok);
     }
 
     // The warp's state into its part of shared memory.
@@ -612,11 +626,27 @@ __device__ __forceinline__ float weight_of(float top, float all) {
     return all == -INFINITY ? 0.0f : exp2_fast(top - all);
 }
 
+// How `total` tiles (virtual ones included) are cut into `ranges` ranges whose
+// sizes differ by at most one.
+struct Cut {
+    unsigned size, longer;  // the first `longer` ranges have one tile more
+    __device__ __forceinline__ Cut(unsigned total, unsigned ranges)
+        : size(total / ranges), longer(total - size * ranges) {}
+    __device__ __forceinline__ unsigned begin(unsigned i) const {
+        return i * size + min(i, longer);
+    }
+    __device__ __forceinline__ unsigned owner(unsigned t) const {
+        const unsigned head = longer * (size + 1);
+        return t < head ? t / (size + 1) : longer + (t - head) / size;
+    }
+};
+
 template <int kDim, int kNT>
-__global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, Shape<kDim, kNT>::kBlocks)
+    kv8_attention_kernel(const AttentionArgs a) {
     using S = Shape<kDim, kNT>;
     extern __shared__ __align__(128) uint8_t shared[];
-    long long* const prefix = reinterpret_cast<long long*>(shared + S::kPrefixAt);
+    Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
     __shared__ long long part[kWarps];
     __shared__ int joins;
     const int tid = threadIdx.x;
@@ -624,20 +654,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Worker<kDim, kNT> w(a, smem_addr(shared));
 
-    // prefix sums of the sequences' tiles (each block for itself)
-    long long total = 0;
-    if (tid == 0) prefix[0] = 0;
+    // the sequences and prefix sums of their tiles (each block for itself);
+    // every unit counts kUnitCost tiles more than it has
+    long long sum = 0;
     for (int b0 = 0; b0 < a.bt.batch; b0 += kThreads) {
         const int b = b0 + tid;
         long long n = 0;
+        Kv8Seq s{0, 0, 0, false};
         if (b < a.bt.batch) {
-            const Kv8Seq s = kv8_seq(a.bt, b);
+            s = kv8_seq(a.bt, b);
             if (s.bad) kv8_report(a.bt);
             const int rt = row_tiles(a, s.len, S::kRows);
             for (int r = 0; r < rt; ++r)
-                n += unit_keys<S::kTile, S::kRows>(a, s.kv - s.len, s.len, r).tiles;
+                n += unit_keys<S::kRows>(a, s.kv - s.len, s.len, r).tiles + kUnitCost;
             n *= a.c.kv_heads;
         }
+        const long long own = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, n, d);
@@ -645,64 +677,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
         }
         if (w.lane == 31) part[w.warp] = n;
         __syncthreads();
-        long long before = total;
+        long long before = sum;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             if (i < w.warp) before += part[i];
-            total += part[i];
+            sum += part[i];
         }
-        if (b < a.bt.batch) prefix[b + 1] = before + n;
+        if (b < a.bt.batch) seqs[b] = Seq{s.q0, s.len, s.kv, (int)(before + n - own)};
         __syncthreads();
     }
-    if (total == 0) return;
-    const long long most = (total + kMinTiles - 1) / kMinTiles;
-    const long long ranges = most < (long long)gridDim.x ? most : (long long)gridDim.x;
-    if ((long long)blockIdx.x >= ranges) return;
-    const long long begin = total * blockIdx.x / ranges;
-    const long long end = total * (blockIdx.x + 1) / ranges;
+    if (sum > 0x7fffffff) {  // over 8e12 bytes of keys and values
+        kv8_report(a.bt);
+        return;
+    }
+    if (sum == 0) return;
+    const unsigned total = (unsigned)sum;
+    const unsigned ranges = min((total + kMinTiles - 1) / kMinTiles, gridDim.x);
+    if (blockIdx.x >= ranges) return;
+    const Cut cut(total, ranges);
+    const unsigned begin = cut.begin(blockIdx.x), end = cut.begin(blockIdx.x + 1);
 
-    for (long long t = begin; t < end;) {
+    for (unsigned t = begin; t < end;) {
         // the unit of tile t
         int lo = 0, hi = a.bt.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= t)
+            if ((unsigned)seqs[mid].before <= t)
                 lo = mid;
             else
                 hi = mid;
         }
-        const Kv8Seq seq = kv8_seq(a.bt, lo);
+        const Seq seq = seqs[lo];
+        const unsigned after = lo + 1 < a.bt.batch ? (unsigned)seqs[lo + 1].before : total;
         w.b = lo;
         w.q0 = seq.q0;
         w.len = seq.len;
         w.first = seq.kv - seq.len;
-        const long long per_head = (prefix[lo + 1] - prefix[lo]) / a.c.kv_heads;
-        long long x = t - prefix[lo];
-        w.head = (int)(x / per_head);
+        const unsigned per_head = (after - seq.before) / a.c.kv_heads;
+        unsigned x = t - seq.before;
+        w.head = x / per_head;
         x -= w.head * per_head;
         w.r = 0;
         for (;;) {
-            w.keys = unit_keys<S::kTile, S::kRows>(a, w.first, w.len, w.r);
-            if (x < w.keys.tiles) break;
-            x -= w.keys.tiles;
+            w.keys = unit_keys<S::kRows>(a, w.first, w.len, w.r);
+            if (x < (unsigned)w.keys.tiles + kUnitCost) break;
+            x -= w.keys.tiles + kUnitCost;
             ++w.r;
         }
-        const int x0 = (int)x;
-        const int x1 = (int)min((long long)w.keys.tiles, x + (end - t));
-        const long long unit_begin = t - x0;
+        const unsigned unit_begin = t - x;
+        const unsigned x_end = min(w.keys.tiles + (unsigned)kUnitCost, x + (end - t));
+        t += x_end - x;
+        if (x_end <= kUnitCost) continue;  // none of its tiles
+        const int x0 = max((int)x - kUnitCost, 0), x1 = (int)x_end - kUnitCost;
 
-        // the ring's first copies, then q
+        // pages, q and the ring's first copies
         const int mine = x0 + w.warp;
-        w.find_pages(mine, x1);
+        w.find_pages(mine, x1, 0);
+        typename Worker<kDim, kNT>::QRow q[kNT < 4 ? kNT : 1];
+        if constexpr (kNT < 4) {
 #pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) w.issue(mine + s * kWarps, x1, s);
-        if (w.warp < kNT) w.stage_q(w.warp);
-        __syncthreads();
+            for (int nt = 0; nt < kNT; ++nt) q[nt] = w.load_q(nt);
+        }
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) w.issue(mine + s * kWarps, x1, s, s);
+        if constexpr (kNT >= 4) {
+            if (w.warp < kNT) w.stage_q(w.warp);
+            __syncthreads();
+        }
         w.begin();
-        int stage = 0;
+        w.take_q(q);
+        int stage = 0, number = S::kStages - 1;
         for (int i = mine; i < x1; i += kWarps) {
             const int ahead = stage == 0 ? S::kStages - 1 : stage - 1;
-            w.issue(i + (S::kStages - 1) * kWarps, x1, ahead);
+            w.issue(i + (S::kStages - 1) * kWarps, x1, number, ahead);
+            ++number;
             cp_async_wait<S::kStages - 1>();
             __syncwarp();
             w.consume(i, stage);
@@ -717,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
         const float* tops = reinterpret_cast<const float*>(shared + S::kMaxAt);
         const float* sums = reinterpret_cast<const float*>(shared + S::kSumAt);
         const bool whole = x0 == 0 && x1 == w.keys.tiles;
-        const int slot = 2 * blockIdx.x + (t > begin ? 1 : 0);
+        const int slot = 2 * blockIdx.x + (unit_begin < begin ? 0 : 1);
         float* const mine_out = a.partials + (size_t)slot * S::kPartial;
         for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
             const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
@@ -749,9 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
         }
         if (!whole) {
             // ranges that hold the unit's first and last tile
-            const long long c0 = ((unit_begin + 1) * ranges + total - 1) / total - 1;
-            const long long c1 =
-                ((unit_begin + w.keys.tiles) * ranges + total - 1) / total - 1;
+            const unsigned c0 = cut.owner(unit_begin + kUnitCost);
+            const unsigned c1 = cut.owner(unit_begin + kUnitCost + w.keys.tiles - 1);
             const int n = (int)(c1 - c0) + 1;
             __syncthreads();
             if (tid == 0) {
@@ -761,33 +808,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
             }
             __syncthreads();
             if (joins) {
-                const float* from = a.partials;
-                const int s0 = 2 * (int)c0 + (unit_begin > total * c0 / ranges ? 1 : 0);
+                // each row's largest maximum and the parts' weights, a warp per row
+                float* const weights = reinterpret_cast<float*>(shared);  // [part][row]
+                float* const all_sums = reinterpret_cast<float*>(shared + S::kSumAt);
+                const float* from = a.partials + (size_t)(2 * c0) * S::kPartial;
+                const int s0 = unit_begin < cut.begin(c0) ? 0 : 1;  // slot of part 0
+                for (int row = w.warp; row < S::kRows; row += kWarps) {
+                    float top = -INFINITY;
+                    for (int i = w.lane; i < n; i += 32) {
+                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial +
+                                         S::kRows * kDim + row;
+                        const float v = __ldcg(p);
+                        weights[i * S::kRows + row] = v;
+                        top = fmaxf(top, v);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    float sum = 0.0f;
+                    for (int i = w.lane; i < n; i += 32) {
+                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial +
+                                         S::kRows * kDim + S::kRows + row;
+                        const float f = weight_of(weights[i * S::kRows + row], top);
+                        weights[i * S::kRows + row] = f;
+                        sum = fmaf(__ldcg(p), f, sum);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    if (w.lane == 0) {
+                        all_sums[row] = sum;
+                        all_sums[S::kRows + row] = top;
+                    }
+                }
+                __syncthreads();
                 for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
                     const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
-                    float top = -INFINITY, sum = 0.0f;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
                     for (int i = 0; i < n; ++i) {
-                        const float* p =
-                            from + (size_t)(i == 0 ? s0 : 2 * ((int)c0 + i)) * S::kPartial;
+                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial;
                         const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kDim + d));
-                        const float yt = __ldcg(p + S::kRows * kDim + row);
-                        const float ys = __ldcg(p + S::kRows * kDim + S::kRows + row);
-                        const float all = fmaxf(top, yt);
-                        const float f = weight_of(top, all), k = weight_of(yt, all);
-                        top = all;
-                        sum = sum * f + ys * k;
-                        v.x = v.x * f + y.x * k;
-                        v.y = v.y * f + y.y * k;
-                        v.z = v.z * f + y.z * k;
-                        v.w = v.w * f + y.w * k;
+                        const float f = weights[i * S::kRows + row];
+                        v.x = fmaf(y.x, f, v.x);
+                        v.y = fmaf(y.y, f, v.y);
+                        v.z = fmaf(y.z, f, v.z);
+                        v.w = fmaf(y.w, f, v.w);
                     }
-                    store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v, top, sum);
+                    store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v,
+                                    all_sums[S::kRows + row], all_sums[row]);
                 }
             }
         }
-        t += x1 - x0;
         __syncthreads();  // the states' memory becomes the ring again
     }
 }
@@ -795,14 +866,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const Attent
 template <int kDim, int kNT>
 cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
     using S = Shape<kDim, kNT>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kv8_attention_kernel<kDim, kNT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !allowed[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kv8_attention_kernel<kDim, kNT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kSeqsAt + kKv8MaxBatch * (int)sizeof(Seq));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(num_sms);
+    cfg.gridDim = dim3(num_sms * S::kBlocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.dynamicSmemBytes = S::kSeqsAt + a.bt.batch * sizeof(Seq);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -815,7 +893,8 @@ cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
 }  // namespace
 
 size_t kv8_attention_data_bytes(int head_dim, int num_sms) {
-    // two partial states per block, of 32 rows (16 of 256 values)
+    // two partial states per block, of 32 rows (16 of 256 values); with two
+    // blocks per SM they have 8 rows
     const size_t rows = head_dim == 256 ? 16 : 32;
     return (size_t)num_sms * 2 * rows * (head_dim + 2) * sizeof(float);
 }

@@ -143,15 +143,6 @@ def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _addr(t):
-    """The address as a plain number: what the newer calls pass (no wrapper object per argument)."""
-    return t.data_ptr() if t is not None else None
-
-
-def _raw_stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
 def _cuda(t, name, dtype=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -466,52 +457,60 @@ def ffn_swiglu_w8a16(x: torch.Tensor, gate_up_packed: torch.Tensor, down_packed:
 
 
 # ------------------------------------------------------------------ attention side of a layer
+#
+# A decode step makes these calls for microseconds of GPU work, so their checks
+# read each tensor attribute once and pass plain numbers.
 
-def _rows(t, name, heads_dim):
-    """A bf16 [tokens, heads, head_dim] view whose rows are contiguous: its token stride."""
-    _on_cuda(t, name, torch.bfloat16)
-    T, heads, dim = t.shape
-    if dim != heads_dim:
-        raise ValueError(f"{name} must have head_dim {heads_dim}, got {dim}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+_BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+# The current stream's handle by device index, without a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _plain(t, name, dtype, shape, device):
+    """Checks a contiguous tensor of `shape` (a tuple) on CUDA device `device`; its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)} on device "
+                         f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, tokens, heads, dim, device):
+    """Checks a bf16 [tokens, heads, head_dim] view with contiguous heads: (address, token
+    stride)."""
+    if t.dtype is not _BF16 or t.shape != (tokens, heads, dim) or t.get_device() != device:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor {[tokens, heads, dim]} on device "
+                         f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    row, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name} must have contiguous heads")
-    return t.stride(0) if T > 1 else heads * dim
+    return t.data_ptr(), (row if tokens > 1 else heads * dim)
 
 
-def _on_cuda(t, name, dtype):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _shaped(t, name, dtype, shape):
-    _cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _norm_args(x, weight, residual, sum_out):
-    _cuda(x, "x", torch.bfloat16)
-    M, H = x.shape
-    _shaped(weight, "weight", torch.bfloat16, (H,))
-    for name, t in (("residual", residual), ("sum_out", sum_out)):
-        if t is not None:
-            _shaped(t, name, torch.bfloat16, (M, H))
-    return M, H
+def _norm_inputs(x, weight, residual, sum_out):
+    """(M, H, device, addresses of residual, weight, sum_out)."""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
+                         f"{list(x.shape)} on {x.device}")
+    shape, device = x.shape, x.get_device()
+    return (shape, device,
+            None if residual is None else _plain(residual, "residual", _BF16, shape, device),
+            _plain(weight, "weight", _BF16, shape[1:], device),
+            None if sum_out is None else _plain(sum_out, "sum_out", _BF16, shape, device))
 
 
 def add_rmsnorm_bf16(x: torch.Tensor, weight: torch.Tensor, eps: float,
                      residual: torch.Tensor = None, sum_out: torch.Tensor = None,
                      weight_bias: float = 0.0, out: torch.Tensor = None) -> torch.Tensor:
     """bf16 norm of x + residual; the sum goes to sum_out (which may be residual) when given."""
-    M, H = _norm_args(x, weight, residual, sum_out)
+    shape, device, res, w, total = _norm_inputs(x, weight, residual, sum_out)
     if out is None:
         out = torch.empty_like(x)
-    _shaped(out, "out", torch.bfloat16, (M, H))
-    _check("add_rmsnorm_bf16",
-           load().add_rmsnorm_bf16(_addr(x), _addr(residual), _addr(weight), M, H, eps,
-                                   weight_bias, _addr(sum_out), _addr(out), _raw_stream(x)))
+    code = (_lib or load()).add_rmsnorm_bf16(
+        x.data_ptr(), res, w, shape[0], shape[1], eps, weight_bias, total,
+        _plain(out, "out", _BF16, shape, device), _raw_stream(device))
+    if code:
+        _check("add_rmsnorm_bf16", code)
     return out
 
 
@@ -520,17 +519,18 @@ def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, eps: float,
                      weight_bias: float = 0.0, codes: torch.Tensor = None,
                      scales: torch.Tensor = None):
     """(codes u8 [M, H], scales fp32 [M, ceil(H/128)]) of the norm of x + residual."""
-    M, H = _norm_args(x, weight, residual, sum_out)
+    shape, device, res, w, total = _norm_inputs(x, weight, residual, sum_out)
+    groups = (shape[0], (shape[1] + 127) // 128)
     if codes is None:
-        codes = torch.empty((M, H), dtype=torch.uint8, device=x.device)
+        codes = torch.empty(shape, dtype=_U8, device=x.device)
     if scales is None:
-        scales = torch.empty((M, (H + 127) // 128), dtype=torch.float32, device=x.device)
-    _shaped(codes, "codes", torch.uint8, (M, H))
-    _shaped(scales, "scales", torch.float32, (M, (H + 127) // 128))
-    _check("add_rmsnorm_e4m3",
-           load().add_rmsnorm_e4m3(_addr(x), _addr(residual), _addr(weight), M, H, eps,
-                                   weight_bias, _addr(sum_out), _addr(codes), _addr(scales),
-                                   _raw_stream(x)))
+        scales = torch.empty(groups, dtype=_F32, device=x.device)
+    code = (_lib or load()).add_rmsnorm_e4m3(
+        x.data_ptr(), res, w, shape[0], shape[1], eps, weight_bias, total,
+        _plain(codes, "codes", _U8, shape, device), _plain(scales, "scales", _F32, groups, device),
+        _raw_stream(device))
+    if code:
+        _check("add_rmsnorm_e4m3", code)
     return codes, scales
 
 
@@ -538,11 +538,12 @@ def rope_table(positions: int, rot_dim: int, base: float, device, scaling: int =
                factor: float = 1.0, context: float = 1.0, slow: float = 1.0, fast: float = 32.0,
                magnitude: float = 1.0) -> torch.Tensor:
     """fp32 [positions, rot_dim/2, 2] rotations (cos, sin) for kv8_append."""
-    table = torch.empty((positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    table = torch.empty((positions, rot_dim // 2, 2), dtype=_F32, device=device)
     if not table.is_cuda:
         raise ValueError("device must be a CUDA device")
     _check("rope_table", load().rope_table(positions, rot_dim, base, scaling, factor, context, slow,
-                                           fast, magnitude, _addr(table), _raw_stream(table)))
+                                           fast, magnitude, table.data_ptr(),
+                                           _raw_stream(table.get_device())))
     return table
 
 
@@ -561,25 +562,25 @@ class Kv8Cache:
     [pages, kv_heads] for k and v.  Holds the tensors and their description."""
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
-        _cuda(k_codes, "k_codes", torch.uint8)
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [pages, kv_heads, page, head_dim]")
-        _shaped(v_codes, "v_codes", torch.uint8, k_codes.shape)
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _shaped(t, name, torch.float32, k_codes.shape[:2])
+        shape, self.device = k_codes.shape, k_codes.get_device()
+        self.struct = _CacheStruct(
+            _plain(k_codes, "k_codes", _U8, shape, self.device),
+            _plain(v_codes, "v_codes", _U8, shape, self.device),
+            _plain(k_scales, "k_scales", _F32, shape[:2], self.device),
+            _plain(v_scales, "v_scales", _F32, shape[:2], self.device), *shape)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = (k_codes, v_codes, k_scales,
                                                                     v_scales)
-        self.pages, self.kv_heads, self.page, self.head_dim = k_codes.shape
-        self.struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
-                                   v_scales.data_ptr(), *k_codes.shape)
+        self.pages, self.kv_heads, self.page, self.head_dim = shape
         self.ref = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, pages, kv_heads, page, head_dim, device):
         """A cache whose pages hold nothing yet."""
-        codes = [torch.empty((pages, kv_heads, page, head_dim), dtype=torch.uint8, device=device)
+        codes = [torch.empty((pages, kv_heads, page, head_dim), dtype=_U8, device=device)
                  for _ in "kv"]
-        scales = [torch.ones((pages, kv_heads), dtype=torch.float32, device=device) for _ in "kv"]
+        scales = [torch.ones((pages, kv_heads), dtype=_F32, device=device) for _ in "kv"]
         return cls(*codes, *scales)
 
 
@@ -589,23 +590,28 @@ class Kv8Batch:
     may advance them in place.  Owns a status word, which kv8_batch_status reads."""
 
     def __init__(self, q_start, kv_len, page_table):
-        _cuda(kv_len, "kv_len", torch.int32)
-        batch = kv_len.numel()
-        _shaped(kv_len, "kv_len", torch.int32, (batch,))
-        _shaped(q_start, "q_start", torch.int32, (batch + 1,))
-        _cuda(page_table, "page_table", torch.int32)
-        if page_table.dim() != 2 or page_table.shape[0] != batch:
+        if page_table.dim() != 2:
             raise ValueError("page_table must be [batch, table_width]")
+        batch, width = page_table.shape
+        self.device = kv_len.get_device()
+        addresses = (_plain(q_start, "q_start", _I32, (batch + 1,), self.device),
+                     _plain(kv_len, "kv_len", _I32, (batch,), self.device),
+                     _plain(page_table, "page_table", _I32, (batch, width), self.device))
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
-        self.status = torch.zeros(1, dtype=torch.int32, device=kv_len.device)
-        self.struct = _BatchStruct(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
-                                   self.status.data_ptr(), batch, page_table.shape[1])
+        self.status = torch.zeros(1, dtype=_I32, device=kv_len.device)
+        self.struct = _BatchStruct(*addresses, self.status.data_ptr(), batch, width)
         self.ref = ctypes.addressof(self.struct)
+
+
+def _same_device(cache, batch):
+    if cache.device != batch.device:
+        raise ValueError("cache and batch must be on the same device")
+    return cache.device
 
 
 def kv8_batch_status(batch: Kv8Batch) -> int:
     """Synchronise, read and clear the batch's status word (0 = OK, 4 = an index out of range)."""
-    return load().kv8_batch_status(batch.ref, _raw_stream(batch.status))
+    return load().kv8_batch_status(batch.ref, _raw_stream(batch.device))
 
 
 def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tensor,
@@ -613,39 +619,46 @@ def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tenso
                interleaved: bool = False):
     """Write k, v [tokens, kv_heads, head_dim] into the cache, k rotated by the rope table; with
     q [tokens, heads, head_dim] given, return it rotated (contiguous, in q_out when given)."""
-    k_stride = _rows(k, "k", cache.head_dim)
-    v_stride = _rows(v, "v", cache.head_dim)
-    T = k.shape[0]
-    if k.shape[1] != cache.kv_heads or v.shape[:2] != k.shape[:2]:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim]")
+    device, dim = _same_device(cache, batch), cache.head_dim
+    T = len(k)
+    k_at, k_stride = _rows(k, "k", T, cache.kv_heads, dim, device)
+    v_at, v_stride = _rows(v, "v", T, cache.kv_heads, dim, device)
+    q_at = out_at = rope_at = None
     heads = q_stride = positions = rot = 0
     if q is not None:
-        q_stride = _rows(q, "q", cache.head_dim)
-        heads = q.shape[1]
-        if q.shape[0] != T:
-            raise ValueError("q must have the tokens of k")
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, head_dim]")
+        shape = q.shape
+        heads = shape[1]
+        q_at, q_stride = _rows(q, "q", T, heads, dim, device)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _shaped(q_out, "q_out", torch.bfloat16, q.shape)
+            q_out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out_at = _plain(q_out, "q_out", _BF16, shape, device)
     if rope is not None:
-        _cuda(rope, "rope", torch.float32)
-        if rope.dim() != 3 or rope.shape[2] != 2:
+        shape = rope.shape
+        if len(shape) != 3 or shape[2] != 2:
             raise ValueError("rope must be [positions, rot_dim/2, 2]")
-        positions, rot = rope.shape[0], 2 * rope.shape[1]
-    _check("kv8_append",
-           load().kv8_append(cache.ref, batch.ref, T, _addr(k), k_stride, _addr(v), v_stride,
-                             _addr(q), q_stride, heads, _addr(q_out), _addr(rope), positions, rot,
-                             1 if interleaved else 0, _raw_stream(k)))
+        rope_at = _plain(rope, "rope", _F32, shape, device)
+        positions, rot = shape[0], 2 * shape[1]
+    code = (_lib or load()).kv8_append(
+        cache.ref, batch.ref, T, k_at, k_stride, v_at, v_stride, q_at, q_stride, heads, out_at,
+        rope_at, positions, rot, 1 if interleaved else 0, _raw_stream(device))
+    if code:
+        _check("kv8_append", code)
     return q_out
 
 
 def kv8_read(cache: Kv8Cache, batch: Kv8Batch, k_out: torch.Tensor, v_out: torch.Tensor):
     """Read the batch's tokens back: k_out, v_out bf16 [tokens, kv_heads, head_dim]."""
-    T = k_out.shape[0]
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _shaped(t, name, torch.bfloat16, (T, cache.kv_heads, cache.head_dim))
-    _check("kv8_read", load().kv8_read(cache.ref, batch.ref, T, _addr(k_out), _addr(v_out),
-                                       _raw_stream(k_out)))
+    device = _same_device(cache, batch)
+    T = len(k_out)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    code = (_lib or load()).kv8_read(cache.ref, batch.ref, T,
+                                     _plain(k_out, "k_out", _BF16, shape, device),
+                                     _plain(v_out, "v_out", _BF16, shape, device),
+                                     _raw_stream(device))
+    if code:
+        _check("kv8_read", code)
     return k_out, v_out
 
 
@@ -658,17 +671,20 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, softmax_sca
                   out: torch.Tensor = None, lse: torch.Tensor = None) -> torch.Tensor:
     """out bf16 [tokens, heads, head_dim]: attention of q over the cache, which already holds the
     batch's tokens; log-sum-exps go to lse fp32 [tokens, heads] when given."""
-    q_stride = _rows(q, "q", cache.head_dim)
-    T, heads = q.shape[:2]
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    device, shape = _same_device(cache, batch), q.shape
+    T, heads, _ = shape
+    q_at, q_stride = _rows(q, "q", T, heads, cache.head_dim, device)
     if ws is None:
         ws = workspace(kv8_attention_workspace_bytes(cache, batch, T, heads), q.device)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    _shaped(out, "out", torch.bfloat16, q.shape)
-    if lse is not None:
-        _shaped(lse, "lse", torch.float32, (T, heads))
-    _check("kv8_attention",
-           load().kv8_attention(_addr(q), q_stride, T, heads, cache.ref, batch.ref, softmax_scale,
-                                window, sinks, _addr(out), _addr(lse), _addr(ws), ws.numel(),
-                                _raw_stream(q)))
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    code = (_lib or load()).kv8_attention(
+        q_at, q_stride, T, heads, cache.ref, batch.ref, softmax_scale, window, sinks,
+        _plain(out, "out", _BF16, shape, device),
+        None if lse is None else _plain(lse, "lse", _F32, (T, heads), device),
+        _plain(ws, "ws", _U8, ws.shape, device), ws.numel(), _raw_stream(device))
+    if code:
+        _check("kv8_attention", code)
     return out
