@@ -525,8 +525,10 @@ size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* ba
  *   ws (device) >= kv8_attention_workspace_bytes.
  * A query that sees nothing gets 0 and -infinity.  Masked keys and values do
  * not enter the result, whatever they hold.  Scores, maxima and sums are fp32.
- * heads a multiple of kv_heads; window, sinks >= 0 (sinks without a window
- * have no effect).
+ * heads a multiple of kv_heads, tokens * heads / kv_heads at most 2^30;
+ * window, sinks >= 0 (sinks without a window have no effect).  Within a
+ * sequence the pages' v_scales may differ by up to 2^100 (a smaller one's
+ * weights may be lost beyond that).
  */
 nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int heads,
                            const kv8_cache* cache, const kv8_batch* batch, float softmax_scale,

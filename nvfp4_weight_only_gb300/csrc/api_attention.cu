@@ -216,6 +216,7 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
     const int dim = cache->head_dim;
     if (heads < 1 || heads % cache->kv_heads != 0) return NVFP4_ERR_SHAPE;
     if (window < 0 || sinks < 0 || !std::isfinite(softmax_scale)) return NVFP4_ERR_RANGE;
+    if ((long long)tokens * (heads / cache->kv_heads) > (1LL << 30)) return NVFP4_ERR_RANGE;
     e = check_rows(q, heads, q_stride, dim);
     if (e != NVFP4_OK) return e;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 16)) return NVFP4_ERR_ALIGN;

@@ -41,12 +41,11 @@ namespace nvf {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr float kBias = 14.0f;  // the largest weight is 2^14 in f16
 constexpr int kTile = 16;       // keys per tile: within one page
-constexpr int kMinTiles = 16;   // least tiles per block: two per warp
-constexpr int kUnitCost = 8;    // what a unit costs beside its tiles, in tiles
+constexpr int kMinTiles = 16;   // least tiles per block
+constexpr int kMostBlocks = 320;
+constexpr int kUnitCost = 24;   // what a unit, or a piece of one, costs beside its tiles, in tiles
 
 struct AttentionArgs {
     Kv8CacheArgs c;
@@ -58,20 +57,30 @@ struct AttentionArgs {
     float* partials;
     long long q_stride;
     int heads, group;
+    unsigned group_inverse;  // floor(2^32 / group), at most 2^32 - 1
     float scale;  // softmax_scale * log2(e)
     int window, sinks;
 };
 
-template <int kDim, int kNT>
+// row / group: the product with the inverse is the quotient or one less.
+__device__ __forceinline__ int token_of(const AttentionArgs& a, int row) {
+    const unsigned q = __umulhi((unsigned)row, a.group_inverse);
+    return (int)(q + ((unsigned)row - q * a.group >= (unsigned)a.group ? 1 : 0));
+}
+
+template <int kDim, int kNT, bool kFew>
 struct Shape {
     static constexpr int kRows = 8 * kNT;
-    // blocks per SM: two where the state leaves room for 128 registers, so that
-    // one block's unit ends and begins under the other's products
-    static constexpr int kBlocks = kNT == 1 && kDim <= 128 ? 2 : 1;
-    static constexpr int kStages = kDim == 64 ? 6 : 3 * (kBlocks == 1 && kDim == 128 ? 2 : 1);
+    // 16 warps per SM where the state leaves room for 128 registers: two blocks,
+    // so that one's unit ends and begins under the other's products, or, when
+    // few units are cut into many parts, one block, which halves the parts
+    static constexpr bool kNarrow = kNT == 1 && kDim <= 128;
+    static constexpr int kBlocks = kNarrow && !kFew ? 2 : 1;
+    static constexpr int kWarps = kNarrow && kFew ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kStages = kDim == 64 || (kDim == 128 && !kNarrow) ? 6 : 3;
     static constexpr int kStageBytes = 2 * kTile * kDim;
     static constexpr int kSteps = kDim / 16;  // k16 steps of q . k, m16 tiles of the head
-    static constexpr int kRowFloats = kDim + 4;
     // shared memory: ring, page scales of each stage, q fragments, row scales,
     // warps' maxima and sums
     static constexpr int kScalesAt = kWarps * kStages * kStageBytes;
@@ -83,13 +92,20 @@ struct Shape {
     // then a Seq per sequence
     // fp32 words of one partial state: O, maxima, sums
     static constexpr int kPartial = kRows * kDim + 2 * kRows;
-    static_assert(kRows * kRowFloats * 4 <= kStages * kStageBytes, "states fit a warp's ring");
+    // a warp's state takes the first kNT stages of its ring
+    static_assert(kRows * kDim * 4 == kNT * kStageBytes && kNT < kStages, "state and ring");
+    // float index of value d of a state's row: the XOR spreads the rows that one
+    // store touches over the banks and keeps 8 values together
+    static __device__ __forceinline__ int state_at(int row, int d) {
+        return row * kDim + (d ^ ((row & 6) << 2));
+    }
 };
 
 // A sequence in shared memory: its new tokens, length, and the tiles of all
 // sequences before it.
 struct Seq {
-    int q0, len, kv, before;
+    int q0, len, kv;
+    unsigned before;
 };
 
 // The keys of one unit: [lo, hi) and the sinks in front, as tiles.
@@ -102,8 +118,8 @@ struct Keys {
 template <int kRows>
 __device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int len, int r) {
     Keys k;
-    const int i0 = r * kRows / a.group;
-    const int i1 = min((r * kRows + kRows - 1) / a.group, len - 1);
+    const int i0 = token_of(a, r * kRows);
+    const int i1 = min(token_of(a, r * kRows + kRows - 1), len - 1);
     k.hi_min = first + i0 + 1;
     k.hi = first + i1 + 1;
     k.lo = a.window > 0 ? max(k.hi_min - a.window, 0) : 0;
@@ -115,8 +131,20 @@ __device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int
     return k;
 }
 
+// A piece of one unit that a block takes, and how its state is joined.
+struct Segment {
+    int b, q0, len, first, head, r;
+    Keys keys;
+    int x0, x1;            // its tiles
+    unsigned slot;         // of its partial state
+    unsigned counter;      // of the unit's finished parts
+    unsigned slot0, slot1;  // of part 0, of part 1 (then every second one)
+    int parts;
+    int last;              // the block's last segment
+};
+
 __device__ __forceinline__ int row_tiles(const AttentionArgs& a, int len, int rows) {
-    return (int)(((long long)len * a.group + rows - 1) / rows);
+    return (len * a.group + rows - 1) / rows;  // at most 2^30 rows, `rows` a constant
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
@@ -129,6 +157,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool fu
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                  "r"(full ? 4 : 0)
                  : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ void cp_async_commit() {
@@ -198,9 +230,10 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-template <int kDim, int kNT>
+template <int kDim, int kNT, bool kFew>
 class Worker {
-    using S = Shape<kDim, kNT>;
+    using S = Shape<kDim, kNT, kFew>;
+    static constexpr int kWarps = S::kWarps;
     static constexpr bool kQInRegs = kNT < 4;
     static constexpr int kWords = kDim / 32;  // 32-bit words of a value row that a lane holds
 
@@ -208,49 +241,44 @@ public:
     const AttentionArgs& a;
     const int lane, warp, g, c, tg;
     const uint32_t smem;
-    // the unit
-    int b, head, first, len, q0, r;
-    Keys keys;
+    const Segment* seg;  // in shared memory: read there, not held in registers
     // the state: column pairs (2c, 2c + 1) of each n8 tile
     float o[kNT][S::kSteps][4];
     float top[kNT][2], sum[kNT][2];
     uint2 qf[kQInRegs ? kNT : 1][kQInRegs ? S::kSteps : 1];
     float row_scale[kNT][2];
-    int pages;   // lane l: the page of the warp's tile number (in this segment) pages_at + l
+    int pages;   // lane l: the page (not yet checked) of the segment's tile number pages_at + l
     int pages_at;
 
     __device__ __forceinline__ Worker(const AttentionArgs& args, uint32_t base)
         : a(args), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), g(lane >> 2), c(lane & 3),
           tg(((lane >> 2) & 1) << 2 | (lane >> 3)), smem(base) {}
 
-    __device__ __forceinline__ int tile_start(int x) const {
-        return (x < keys.sink_tiles ? x : keys.lo / kTile + x - keys.sink_tiles) * kTile;
+    __device__ __forceinline__ static int tile_start(const Keys& k, int x) {
+        return (x < k.sink_tiles ? x : k.lo / kTile + x - k.sink_tiles) * kTile;
     }
 
-    // Looks up the pages of the warp's tiles x, x + kWarps, ..: -1 outside the
-    // cache, -2 where there is no key.
-    __device__ __forceinline__ void find_pages(int x, int end, int number) {
-        const int mine = x + lane * kWarps;
-        const int j = tile_start(mine);
-        pages = -2;
-        pages_at = number;
-        if (mine < end && j < keys.hi) {
-            pages = a.bt.page_table[(size_t)b * a.bt.table_width + (j >> a.bt.page_shift)];
-            if (pages < 0 || pages >= a.c.pages) {
-                pages = -1;
-                kv8_report(a.bt);
-            }
-        }
+    // The table's entry for tile x; -2 where there is no key.
+    __device__ __forceinline__ int page_of(const Segment& s, int x) const {
+        const int j = tile_start(s.keys, x);
+        if (x >= s.x1 || j >= s.keys.hi) return -2;
+        return a.bt.page_table[(size_t)s.b * a.bt.table_width + (j >> a.bt.page_shift)];
     }
 
     // Starts the copy of tile x, the warp's number-th of the segment.
-    __device__ __forceinline__ void issue(int x, int end, int number, int stage) {
-        if (x < end) {
-            if (number - pages_at == 32) find_pages(x, end, number);
-            const int page = __shfl_sync(0xffffffffu, pages, number - pages_at);
+    __device__ __forceinline__ void issue(int x, int number, int stage) {
+        if (x < seg->x1) {
+            if (number - pages_at == 32) {
+                pages = page_of(*seg, x + lane * kWarps);
+                pages_at = number;
+            }
+            const int entry = __shfl_sync(0xffffffffu, pages, number - pages_at);
+            const bool ok = entry >= 0 && entry < a.c.pages;
+            if (!ok && entry != -2) kv8_report(a.bt);
             const uint32_t dst = smem + (warp * S::kStages + stage) * S::kStageBytes;
-            const int j0 = tile_start(x);
-            const size_t at = (size_t)max(page, 0) * a.c.kv_heads + head;
+            const int j0 = tile_start(seg->keys, x);
+            const int lo = seg->keys.lo, hi = seg->keys.hi;
+            const size_t at = (size_t)(ok ? entry : 0) * a.c.kv_heads + seg->head;
             const size_t from =
                 ((at << a.bt.page_shift) + (j0 & ((1 << a.bt.page_shift) - 1))) * kDim;
             constexpr int kPieces = kDim / 16;
@@ -259,7 +287,7 @@ public:
                 const int row = (it * 32 + lane) / kPieces, piece = (it * 32 + lane) % kPieces;
                 const int j = j0 + row;
                 // keys that no row sees are copied as zeros
-                const bool live = page >= 0 && j < keys.hi && (j >= keys.lo || j < a.sinks);
+                const bool live = ok && j < hi && (j >= lo || j < a.sinks);
                 const size_t off = live ? from + (it * 32 + lane) * 16 : 0;
                 const uint32_t to = dst + piece_at<kDim>(row, piece);
                 cp_async16(to, a.c.k_codes + off, live);
@@ -268,7 +296,7 @@ public:
             if (lane < 2) {
                 const uint32_t to =
                     smem + S::kScalesAt + (warp * S::kStages + stage) * 8 + lane * 4;
-                cp_async4(to, (lane ? a.c.v_scales : a.c.k_scales) + at, page >= 0);
+                cp_async4(to, (lane ? a.c.v_scales : a.c.k_scales) + at, ok);
             }
         }
         cp_async_commit();
@@ -280,12 +308,12 @@ public:
     };
 
     __device__ __forceinline__ QRow load_q(int nt) const {
-        const int row = r * S::kRows + nt * 8 + g;
-        const int i = row / a.group;
-        const bool live = i < len;
+        const int row = seg->r * S::kRows + nt * 8 + g;
+        const int i = token_of(a, row);
+        const bool live = i < seg->len;
         const __nv_bfloat16* src =
-            a.q + (long long)(q0 + (live ? i : 0)) * a.q_stride +
-            (size_t)(head * a.group + (live ? row - i * a.group : 0)) * kDim;
+            a.q + (long long)(seg->q0 + (live ? i : 0)) * a.q_stride +
+            (size_t)(seg->head * a.group + (live ? row - i * a.group : 0)) * kDim;
         QRow q;
 #pragma unroll
         for (int h = 0; h < kDim / 64; ++h)
@@ -386,10 +414,10 @@ public:
 
     // Whether row column e of n-tile nt sees key j.
     __device__ __forceinline__ bool sees(int nt, int e, int j, bool page_ok) const {
-        const int i = (r * S::kRows + nt * 8 + 2 * c + e) / a.group;
-        const int hi = first + i + 1;
+        const int i = token_of(a, seg->r * S::kRows + nt * 8 + 2 * c + e);
+        const int hi = seg->first + i + 1;
         const int lo = a.window > 0 ? hi - a.window : 0;
-        return page_ok && i < len && j < hi && (j >= lo || j < a.sinks);
+        return page_ok && i < seg->len && j < hi && (j >= lo || j < a.sinks);
     }
 
     // V^T fragments (values g and g + 8 of m16 tiles 2i and 2i + 1) of four keys'
@@ -490,7 +518,8 @@ public:
         const uint32_t k_at = smem + (warp * S::kStages + stage) * S::kStageBytes;
         const uint32_t v_at = k_at + kTile * kDim;
         const uint32_t scales = smem + S::kScalesAt + (warp * S::kStages + stage) * 8;
-        const int j0 = tile_start(x);
+        const Keys& keys = seg->keys;
+        const int j0 = tile_start(keys, x);
         const float ks = lds32(scales);
         float vs = lds32(scales + 4);
         const bool page_ok = vs > 0.0f;  // copied as 0 without a page
@@ -597,7 +626,7 @@ public:
                     const int d = kDim == 64 ? 8 * g + 2 * m
                                              : 16 * (tg + 8 * (m / 8)) + 2 * (m % 8);
                     asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(
-                                     mine + (row * S::kRowFloats + d) * 4),
+                                     mine + S::state_at(row, d) * 4),
                                  "f"(o[nt][m][e]), "f"(o[nt][m][e + 2])
                                  : "memory");
                 }
@@ -609,7 +638,7 @@ public:
 template <int kDim>
 __device__ __forceinline__ void store_row(const AttentionArgs& a, int q0, int len, int head,
                                           int row, int d, float4 v, float top, float sum) {
-    const int i = row / a.group;
+    const int i = token_of(a, row);
     if (i >= len) return;
     const size_t at = (size_t)(q0 + i) * a.heads + head * a.group + (row - i * a.group);
     const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
@@ -626,12 +655,24 @@ __device__ __forceinline__ float weight_of(float top, float all) {
     return all == -INFINITY ? 0.0f : exp2_fast(top - all);
 }
 
-// How `total` tiles (virtual ones included) are cut into `ranges` ranges whose
-// sizes differ by at most one.
-struct Cut {
-    unsigned size, longer;  // the first `longer` ranges have one tile more
-    __device__ __forceinline__ Cut(unsigned total, unsigned ranges)
-        : size(total / ranges), longer(total - size * ranges) {}
+// The blocks' shares of the work.  Kept in shared memory and advanced by one
+// warp while the others join states, two segments ahead, so that it takes no
+// registers from the products and every warp can begin the next segment's
+// copies before the current one's states are joined.
+//
+// Many units: all units' tiles, kUnitCost more for each, in one line that is
+// cut into equal ranges, one per block.  Few units (a single sequence, say):
+// each is cut evenly into parts of at most `most` tiles, one per block; with U
+// units, total / (blocks - U) tiles per part give at most `blocks` parts.  About as
+// many units as blocks, none much longer than the others: one block each.
+struct Plan {
+    unsigned total, ranges;
+    unsigned most;          // units cut into equal parts: tiles per part; else 0
+    unsigned size, longer;  // a range has `size` tiles, the first `longer` one more
+    unsigned t, x, end;     // next tile in the line and in its unit; the range's end
+    int b, head, r;
+    int number;             // segments so far
+
     __device__ __forceinline__ unsigned begin(unsigned i) const {
         return i * size + min(i, longer);
     }
@@ -639,117 +680,407 @@ struct Cut {
         const unsigned head = longer * (size + 1);
         return t < head ? t / (size + 1) : longer + (t - head) / size;
     }
+    // what a unit of n tiles takes in the line
+    __device__ __forceinline__ unsigned weight(int n) const {
+        return most ? (n + most - 1) / most : n + (unsigned)kUnitCost;
+    }
 };
 
-template <int kDim, int kNT>
-__global__ void __launch_bounds__(kThreads, Shape<kDim, kNT>::kBlocks)
-    kv8_attention_kernel(const AttentionArgs a) {
-    using S = Shape<kDim, kNT>;
-    extern __shared__ __align__(128) uint8_t shared[];
-    Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
-    __shared__ long long part[kWarps];
-    __shared__ int joins;
-    const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    Worker<kDim, kNT> w(a, smem_addr(shared));
+constexpr unsigned kMostTiles = 0x7fffffff;
 
-    // the sequences and prefix sums of their tiles (each block for itself);
-    // every unit counts kUnitCost tiles more than it has
-    long long sum = 0;
-    for (int b0 = 0; b0 < a.bt.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long n = 0;
-        Kv8Seq s{0, 0, 0, false};
-        if (b < a.bt.batch) {
-            s = kv8_seq(a.bt, b);
-            if (s.bad) kv8_report(a.bt);
-            const int rt = row_tiles(a, s.len, S::kRows);
-            for (int r = 0; r < rt; ++r)
-                n += unit_keys<S::kRows>(a, s.kv - s.len, s.len, r).tiles + kUnitCost;
-            n *= a.c.kv_heads;
-        }
-        const long long own = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, n, d);
-            if (w.lane >= d) n += v;
-        }
-        if (w.lane == 31) part[w.warp] = n;
-        __syncthreads();
-        long long before = sum;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < w.warp) before += part[i];
-            sum += part[i];
-        }
-        if (b < a.bt.batch) seqs[b] = Seq{s.q0, s.len, s.kv, (int)(before + n - own)};
-        __syncthreads();
+__device__ __forceinline__ unsigned times(unsigned a, unsigned b) {
+    return (unsigned)min((unsigned long long)a * b, (unsigned long long)kMostTiles);
+}
+
+__device__ __forceinline__ unsigned add_tiles(unsigned a, unsigned b) {
+    return min(a + b, kMostTiles);  // both at most kMostTiles
+}
+
+template <int kRows, bool kFew>
+class Scheduler {
+    const AttentionArgs& a;
+    Plan* const plan;
+    Seq* const seqs;
+    Segment* const segments;  // three: the current, the next and the one after
+    const int lane;
+
+    __device__ __forceinline__ Keys keys_of(const Seq& s, int r) const {
+        return unit_keys<kRows>(a, s.kv - s.len, s.len, r);
     }
-    if (sum > 0x7fffffff) {  // over 8e12 bytes of keys and values
-        kv8_report(a.bt);
+
+    // What a sequence's units take in the line.
+    __device__ __forceinline__ unsigned weight_of_units(const Plan& p, const Seq& s,
+                                                        int& longest) const {
+        const int rt = row_tiles(a, s.len, kRows);
+        unsigned n = 0;
+#pragma unroll 1
+        for (int r = 0; r < rt; ++r) {
+            const int tiles = keys_of(s, r).tiles;
+            longest = max(longest, tiles);
+            n = add_tiles(n, p.weight(tiles));
+        }
+        return times(n, a.c.kv_heads);
+    }
+
+public:
+    __device__ __forceinline__ Scheduler(const AttentionArgs& args, Plan* p, Seq* s, Segment* out)
+        : a(args), plan(p), seqs(s), segments(out), lane(threadIdx.x & 31) {}
+
+    // Reads the sequences and cuts the work (one warp); the block's first segment
+    // when there is one.  One warp's latency, so the fewest dependent steps.
+    __device__ __forceinline__ bool start() {
+        const int batch = a.bt.batch;
+        Plan p;
+        p.most = kFew ? 1 : 0;  // first pass: tiles
+        unsigned sum = 0, units = 0;
+        int longest = 0;
+#pragma unroll 1
+        for (int b = lane; b < batch; b += 32) {
+            const Kv8Seq k = kv8_seq(a.bt, b);
+            if (k.bad) kv8_report(a.bt);
+            const Seq s{k.q0, k.len, k.kv, 0};
+            seqs[b] = s;
+            sum = add_tiles(sum, weight_of_units(p, s, longest));
+            units = add_tiles(units, times(row_tiles(a, s.len, kRows), a.c.kv_heads));
+        }
+        __syncwarp();
+        // lanes' sums below 2^26 each cannot overflow the warp's
+        if (__any_sync(0xffffffffu, sum >= 1u << 26 || units >= 1u << 26)) {
+#pragma unroll 1
+            for (int d = 16; d > 0; d >>= 1) {
+                sum = add_tiles(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+                units = add_tiles(units, __shfl_xor_sync(0xffffffffu, units, d));
+            }
+        } else {
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            units = __reduce_add_sync(0xffffffffu, units);
+        }
+        if (sum == kMostTiles) kv8_report(a.bt);  // over 8e12 bytes of keys and values
+        if (sum == 0 || sum == kMostTiles) return false;
+        // at most half of the blocks go to rounding (the host has bounded the units)
+        if (kFew)
+            p.most = max((unsigned)kMinTiles, sum / (gridDim.x - min(units, gridDim.x / 2)) + 1);
+        // a block per unit, where cutting the longest would cost more than it saves
+        if (!kFew && units <= gridDim.x) {
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            if ((unsigned)longest <= sum / gridDim.x) p.most = longest;
+        }
+        if (batch > 1 || p.most) {
+            sum = 0;
+#pragma unroll 1
+            for (int b0 = 0; b0 < batch; b0 += 32) {
+                const int b = b0 + lane;
+                const unsigned n = b < batch ? weight_of_units(p, seqs[b], longest) : 0;
+                unsigned upto = n;
+                if (batch > 1)
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const unsigned v = __shfl_up_sync(0xffffffffu, upto, d);
+                        if (lane >= d) upto += v;
+                    }
+                if (b < batch) seqs[b].before = sum + upto - n;
+                sum += __shfl_sync(0xffffffffu, upto, batch > 1 ? 31 : 0);
+            }
+        }
+        __syncwarp();
+        p.total = sum;
+        p.ranges = p.most ? sum : min((sum + kMinTiles - 1) / kMinTiles, gridDim.x);
+        if (blockIdx.x >= p.ranges) return false;
+        p.size = p.total / p.ranges;
+        p.longer = p.total - p.size * p.ranges;
+        p.t = p.begin(blockIdx.x);
+        p.end = p.begin(blockIdx.x + 1);
+        // the sequence, row tile and head of tile t: the last sequence that
+        // begins at or before it
+        p.b = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < batch; b0 += 32) {
+            const unsigned m = __ballot_sync(0xffffffffu,
+                                             b0 + lane < batch && seqs[b0 + lane].before <= p.t);
+            if (m) p.b = b0 + 31 - __clz(m);
+        }
+        const Seq s = seqs[p.b];
+        p.x = p.t - s.before;
+        p.r = 0;
+        unsigned one;
+#pragma unroll 1
+        for (;;) {  // a row tile's heads lie side by side in the line
+            one = p.weight(keys_of(s, p.r).tiles);
+            if (p.x < one * a.c.kv_heads) break;
+            p.x -= one * a.c.kv_heads;
+            ++p.r;
+        }
+        p.head = p.x / one;
+        p.x -= p.head * one;
+        p.number = 0;
+        if (lane == 0) *plan = p;
+        __syncwarp();
+        next();
+        return true;
+    }
+
+    // Writes the next segment, if there is one, and advances.
+    __device__ __forceinline__ void next() {
+        Plan p = *plan;
+        if (p.t >= p.end) return;
+        Seq s = seqs[p.b];
+        Segment g;
+#pragma unroll 1
+        do {
+            g.keys = keys_of(s, p.r);
+            g.b = p.b;
+            g.q0 = s.q0;
+            g.len = s.len;
+            g.first = s.kv - s.len;
+            g.head = p.head;
+            g.r = p.r;
+            const unsigned tiles = g.keys.tiles;
+            const unsigned unit = p.t - p.x, all = p.weight(tiles);
+            const unsigned take = min(all - p.x, p.end - p.t);
+            unsigned c0, c1;
+            if (p.most) {  // part x of `all` equal ones (take is 1)
+                c0 = unit;
+                c1 = c0 + all - 1;
+                g.slot0 = 2 * c0;
+                const unsigned each = tiles / all, more = tiles - each * all;
+                g.x0 = p.x * each + min(p.x, more);
+                g.x1 = g.x0 + each + (p.x < more ? 1 : 0);
+            } else {
+                g.x0 = max((int)p.x - kUnitCost, 0);
+                g.x1 = (int)(p.x + take) - kUnitCost;
+                // ranges that hold the unit's first and last tile
+                const unsigned u0 = unit + kUnitCost, u1 = u0 + tiles - 1;
+                c0 = u0 >= p.begin(blockIdx.x) ? blockIdx.x : p.owner(u0);
+                c1 = u1 < p.end ? blockIdx.x : p.owner(u1);
+                // a range's slots: of the unit it begins in, of the unit it ends in
+                g.slot0 = 2 * c0 + (unit < p.begin(c0) ? 0 : 1);
+            }
+            g.slot = c0 == blockIdx.x ? g.slot0 : 2 * blockIdx.x;
+            g.slot1 = 2 * c0 + 2;
+            g.counter = c0;
+            g.parts = (int)(c1 - c0) + 1;
+            p.t += take;
+            g.last = p.t >= p.end;
+            p.x = 0;
+            if (!g.last && ++p.head == a.c.kv_heads) {
+                p.head = 0;
+                if (++p.r >= row_tiles(a, s.len, kRows)) {
+                    p.r = 0;
+                    do s = seqs[++p.b];
+                    while (s.len == 0);
+                }
+            }
+            // a range may hold only the cost, not the tiles, of its last unit
+        } while (g.x1 <= g.x0 && !g.last);
+        const int at = p.number % 3;
+        ++p.number;
+        __syncwarp();
+        if (lane == 0) {
+            *plan = p;
+            segments[at] = g;
+        }
+        __syncwarp();
+    }
+};
+
+// Joins the partial states of the segment's unit, by a whole block.  Many
+// parts' weights (one per part and row) and the thread groups' sums go to the
+// rings' first stages, which hold nothing any more.
+template <int kDim, int kNT, bool kFew>
+__device__ __forceinline__ void join_parts(const AttentionArgs& a, const Segment& g,
+                                           uint8_t* shared) {
+    using S = Shape<kDim, kNT, kFew>;
+    constexpr int kItems = S::kRows * kDim / 4;
+    const int parts = g.parts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned slot0 = g.slot0, slot1 = g.slot1;
+    auto part = [&](int i) {
+        return a.partials + (size_t)(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * S::kPartial;
+    };
+    constexpr int kFewParts = 8;
+    if (parts <= kFewParts) {
+        // everything in one round of loads
+        for (int item = threadIdx.x; item < kItems; item += S::kThreads) {
+            const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
+            float4 y[kFewParts];
+            float tops[kFewParts], sums[kFewParts];
+#pragma unroll
+            for (int i = 0; i < kFewParts; ++i) {
+                tops[i] = -INFINITY;
+                sums[i] = 0.0f;
+                y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < parts) {
+                    const float* p = part(i);
+                    y[i] = __ldcg(reinterpret_cast<const float4*>(p + row * kDim + d));
+                    tops[i] = __ldcg(p + S::kRows * kDim + row);
+                    sums[i] = __ldcg(p + S::kRows * kDim + S::kRows + row);
+                }
+            }
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kFewParts; ++i) top = fmaxf(top, tops[i]);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kFewParts; ++i) {
+                const float f = weight_of(tops[i], top);
+                sum = fmaf(sums[i], f, sum);
+                v.x = fmaf(y[i].x, f, v.x);
+                v.y = fmaf(y[i].y, f, v.y);
+                v.z = fmaf(y[i].z, f, v.z);
+                v.w = fmaf(y[i].w, f, v.w);
+            }
+            store_row<kDim>(a, g.q0, g.len, g.head, g.r * S::kRows + row, d, v, top, sum);
+        }
         return;
     }
-    if (sum == 0) return;
-    const unsigned total = (unsigned)sum;
-    const unsigned ranges = min((total + kMinTiles - 1) / kMinTiles, gridDim.x);
-    if (blockIdx.x >= ranges) return;
-    const Cut cut(total, ranges);
-    const unsigned begin = cut.begin(blockIdx.x), end = cut.begin(blockIdx.x + 1);
-
-    for (unsigned t = begin; t < end;) {
-        // the unit of tile t
-        int lo = 0, hi = a.bt.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((unsigned)seqs[mid].before <= t)
-                lo = mid;
-            else
-                hi = mid;
+    // each row's largest maximum and the parts' weights, a warp per row:
+    // [part][row], in pieces of one warp's free stages
+    constexpr int kPiece = kNT * S::kStageBytes / 4 / S::kRows;
+    static_assert(kPiece * S::kWarps >= kMostBlocks, "a weight for every part");
+    auto weight = [&](int i, int row) -> float& {
+        return reinterpret_cast<float*>(shared + (i / kPiece) * S::kStages * S::kStageBytes)
+            [(i % kPiece) * S::kRows + row];
+    };
+    float* const all = reinterpret_cast<float*>(shared + S::kSumAt);
+    for (int row = warp; row < S::kRows; row += S::kWarps) {
+        float top = -INFINITY;
+        for (int i = lane; i < parts; i += 32) {
+            const float v = __ldcg(part(i) + S::kRows * kDim + row);
+            weight(i, row) = v;
+            top = fmaxf(top, v);
         }
-        const Seq seq = seqs[lo];
-        const unsigned after = lo + 1 < a.bt.batch ? (unsigned)seqs[lo + 1].before : total;
-        w.b = lo;
-        w.q0 = seq.q0;
-        w.len = seq.len;
-        w.first = seq.kv - seq.len;
-        const unsigned per_head = (after - seq.before) / a.c.kv_heads;
-        unsigned x = t - seq.before;
-        w.head = x / per_head;
-        x -= w.head * per_head;
-        w.r = 0;
-        for (;;) {
-            w.keys = unit_keys<S::kRows>(a, w.first, w.len, w.r);
-            if (x < (unsigned)w.keys.tiles + kUnitCost) break;
-            x -= w.keys.tiles + kUnitCost;
-            ++w.r;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float sum = 0.0f;
+        for (int i = lane; i < parts; i += 32) {
+            const float f = weight_of(weight(i, row), top);
+            weight(i, row) = f;
+            sum = fmaf(__ldcg(part(i) + S::kRows * kDim + S::kRows + row), f, sum);
         }
-        const unsigned unit_begin = t - x;
-        const unsigned x_end = min(w.keys.tiles + (unsigned)kUnitCost, x + (end - t));
-        t += x_end - x;
-        if (x_end <= kUnitCost) continue;  // none of its tiles
-        const int x0 = max((int)x - kUnitCost, 0), x1 = (int)x_end - kUnitCost;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) {
+            all[row] = sum;
+            all[S::kRows + row] = top;
+        }
+    }
+    __syncthreads();
+    // groups of threads take every kGroups-th part
+    constexpr int kGroups = S::kThreads > kItems ? S::kThreads / kItems : 1;
+    const int group = kGroups > 1 ? threadIdx.x / kItems : 0;
+    for (int item = kGroups > 1 ? threadIdx.x % kItems : threadIdx.x; item < kItems;
+         item += S::kThreads) {
+        const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int i = group; i < parts; i += kGroups) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(part(i) + row * kDim + d));
+            const float f = weight(i, row);
+            v.x = fmaf(y.x, f, v.x);
+            v.y = fmaf(y.y, f, v.y);
+            v.z = fmaf(y.z, f, v.z);
+            v.w = fmaf(y.w, f, v.w);
+        }
+        if constexpr (kGroups > 1) {
+            // the groups' sums, in order, through the last warps' free stages
+            float4* const mine = reinterpret_cast<float4*>(
+                shared + (S::kWarps - kGroups + group) * S::kStages * S::kStageBytes);
+            static_assert(kItems * 16 <= kNT * S::kStageBytes &&
+                              kPiece * (S::kWarps - kGroups) >= kMostBlocks, "room for both");
+            mine[item] = v;
+            __syncthreads();
+            if (group > 0) break;
+            v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const float4 y = reinterpret_cast<const float4*>(
+                    shared + (S::kWarps - kGroups + i) * S::kStages * S::kStageBytes)[item];
+                v.x += y.x;
+                v.y += y.y;
+                v.z += y.z;
+                v.w += y.w;
+            }
+        }
+        store_row<kDim>(a, g.q0, g.len, g.head, g.r * S::kRows + row, d, v, all[S::kRows + row],
+                        all[row]);
+    }
+}
 
-        // pages, q and the ring's first copies
-        const int mine = x0 + w.warp;
-        w.find_pages(mine, x1, 0);
-        typename Worker<kDim, kNT>::QRow q[kNT < 4 ? kNT : 1];
+template <int kDim, int kNT, bool kFew>
+__global__ void __launch_bounds__(Shape<kDim, kNT, kFew>::kThreads,
+                                  Shape<kDim, kNT, kFew>::kBlocks)
+    kv8_attention_kernel(const AttentionArgs a) {
+    using S = Shape<kDim, kNT, kFew>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+    extern __shared__ __align__(128) uint8_t shared[];
+    __shared__ Plan plan;
+    __shared__ Segment segments[3];
+    __shared__ int work, joins;
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the lists' first lines into L2 while the preceding kernel ends
+    if (blockIdx.x == 0) {
+        const int* const lists[2] = {a.bt.kv_len, a.bt.q_start};
+        if (tid < 2) prefetch_l2(lists[tid]);
+        const size_t entries = (size_t)a.bt.batch * a.bt.table_width;
+        if ((size_t)tid * 32 < entries) prefetch_l2(a.bt.page_table + tid * 32);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Worker<kDim, kNT, kFew> w(a, smem_addr(shared));
+    Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
+    Scheduler<S::kRows, kFew> scheduler(a, &plan, seqs, segments);
+    if (w.warp == kWarps - 1) {
+        const bool some = scheduler.start();
+        if (w.lane == 0) work = some;
+    }
+    __syncthreads();
+    if (!work) return;
+
+    // the first copies of a segment go to the stages behind the state of the one
+    // before it, which may still be waiting to be joined
+    constexpr int kEarly = S::kStages - kNT < S::kStages - 1 ? S::kStages - kNT : S::kStages - 1;
+    typename Worker<kDim, kNT, kFew>::QRow q[kNT < 4 ? kNT : 1];
+    int ahead_pages = -2;  // of the next segment's first tiles
+    auto look_ahead = [&](const Segment& g) {
+        ahead_pages = w.page_of(g, g.x0 + w.warp + w.lane * kWarps);
+    };
+    auto enter = [&](const Segment& g) {
+        w.seg = &g;
+        const int mine = g.x0 + w.warp;
+        w.pages = ahead_pages;
+        w.pages_at = 0;
         if constexpr (kNT < 4) {
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) q[nt] = w.load_q(nt);
         }
 #pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) w.issue(mine + s * kWarps, x1, s, s);
+        for (int i = 0; i < kEarly; ++i) w.issue(mine + i * kWarps, i, kNT + i);
+    };
+    look_ahead(segments[0]);
+    enter(segments[0]);
+    // the second segment, while the first one's copies are under way
+    if (!segments[0].last) {
+        if (w.warp == kWarps - 1) scheduler.next();
+        __syncthreads();
+    }
+    for (int at = 0;; at = at == 2 ? 0 : at + 1) {
+        const Segment& g = segments[at];
+        const int x1 = g.x1, mine = g.x0 + w.warp;
+        if (x1 <= g.x0) break;
+        if (!g.last) look_ahead(segments[at == 2 ? 0 : at + 1]);
+#pragma unroll
+        for (int i = kEarly; i < S::kStages - 1; ++i)
+            w.issue(mine + i * kWarps, i, (kNT + i) % S::kStages);
         if constexpr (kNT >= 4) {
             if (w.warp < kNT) w.stage_q(w.warp);
             __syncthreads();
         }
         w.begin();
         w.take_q(q);
-        int stage = 0, number = S::kStages - 1;
+        int stage = kNT, number = S::kStages - 1;
+#pragma unroll 1
         for (int i = mine; i < x1; i += kWarps) {
             const int ahead = stage == 0 ? S::kStages - 1 : stage - 1;
-            w.issue(i + (S::kStages - 1) * kWarps, x1, number, ahead);
+            w.issue(i + (S::kStages - 1) * kWarps, number, ahead);
             ++number;
             cp_async_wait<S::kStages - 1>();
             __syncwarp();
@@ -759,14 +1090,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kDim, kNT>::kBlocks)
         }
         cp_async_wait<0>();
         w.put_state();
+        const bool last = g.last;
+        if (!last) enter(segments[at == 2 ? 0 : at + 1]);
         __syncthreads();
+        if (!last && w.warp == kWarps - 1) scheduler.next();
 
         // the warps' states joined, 4 values of one row per thread
+        const int parts = g.parts;
         const float* tops = reinterpret_cast<const float*>(shared + S::kMaxAt);
         const float* sums = reinterpret_cast<const float*>(shared + S::kSumAt);
-        const bool whole = x0 == 0 && x1 == w.keys.tiles;
-        const int slot = 2 * blockIdx.x + (unit_begin < begin ? 0 : 1);
-        float* const mine_out = a.partials + (size_t)slot * S::kPartial;
+        float* const mine_out = a.partials + (size_t)g.slot * S::kPartial;
         for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
             const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
             float top = -INFINITY;
@@ -778,15 +1111,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kDim, kNT>::kBlocks)
             for (int i = 0; i < kWarps; ++i) {
                 const float f = weight_of(tops[i * S::kRows + row], top);
                 const float4 y = *reinterpret_cast<const float4*>(
-                    shared + i * S::kStages * S::kStageBytes + (row * S::kRowFloats + d) * 4);
+                    shared + i * S::kStages * S::kStageBytes + S::state_at(row, d) * 4);
                 sum = fmaf(sums[i * S::kRows + row], f, sum);
                 v.x = fmaf(y.x, f, v.x);
                 v.y = fmaf(y.y, f, v.y);
                 v.z = fmaf(y.z, f, v.z);
                 v.w = fmaf(y.w, f, v.w);
             }
-            if (whole) {
-                store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v, top, sum);
+            if (parts == 1) {
+                store_row<kDim>(a, g.q0, g.len, g.head, g.r * S::kRows + row, d, v, top, sum);
             } else {
                 *reinterpret_cast<float4*>(mine_out + row * kDim + d) = v;
                 if (d == 0) {
@@ -795,91 +1128,39 @@ __global__ void __launch_bounds__(kThreads, Shape<kDim, kNT>::kBlocks)
                 }
             }
         }
-        if (!whole) {
-            // ranges that hold the unit's first and last tile
-            const unsigned c0 = cut.owner(unit_begin + kUnitCost);
-            const unsigned c1 = cut.owner(unit_begin + kUnitCost + w.keys.tiles - 1);
-            const int n = (int)(c1 - c0) + 1;
+        if (parts > 1) {
             __syncthreads();
             if (tid == 0) {
-                const int seen = atom_add_acq_rel_gpu(a.counters + c0, 1);
-                joins = seen == n - 1;
-                if (joins) a.counters[c0] = 0;
+                const int seen = atom_add_acq_rel_gpu(a.counters + g.counter, 1);
+                joins = seen == parts - 1;
+                if (joins) a.counters[g.counter] = 0;
             }
             __syncthreads();
-            if (joins) {
-                // each row's largest maximum and the parts' weights, a warp per row
-                float* const weights = reinterpret_cast<float*>(shared);  // [part][row]
-                float* const all_sums = reinterpret_cast<float*>(shared + S::kSumAt);
-                const float* from = a.partials + (size_t)(2 * c0) * S::kPartial;
-                const int s0 = unit_begin < cut.begin(c0) ? 0 : 1;  // slot of part 0
-                for (int row = w.warp; row < S::kRows; row += kWarps) {
-                    float top = -INFINITY;
-                    for (int i = w.lane; i < n; i += 32) {
-                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial +
-                                         S::kRows * kDim + row;
-                        const float v = __ldcg(p);
-                        weights[i * S::kRows + row] = v;
-                        top = fmaxf(top, v);
-                    }
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    float sum = 0.0f;
-                    for (int i = w.lane; i < n; i += 32) {
-                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial +
-                                         S::kRows * kDim + S::kRows + row;
-                        const float f = weight_of(weights[i * S::kRows + row], top);
-                        weights[i * S::kRows + row] = f;
-                        sum = fmaf(__ldcg(p), f, sum);
-                    }
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    if (w.lane == 0) {
-                        all_sums[row] = sum;
-                        all_sums[S::kRows + row] = top;
-                    }
-                }
-                __syncthreads();
-                for (int item = tid; item < S::kRows * kDim / 4; item += kThreads) {
-                    const int row = item / (kDim / 4), d = item % (kDim / 4) * 4;
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int i = 0; i < n; ++i) {
-                        const float* p = from + (size_t)(2 * i + (i == 0 ? s0 : 0)) * S::kPartial;
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kDim + d));
-                        const float f = weights[i * S::kRows + row];
-                        v.x = fmaf(y.x, f, v.x);
-                        v.y = fmaf(y.y, f, v.y);
-                        v.z = fmaf(y.z, f, v.z);
-                        v.w = fmaf(y.w, f, v.w);
-                    }
-                    store_row<kDim>(a, w.q0, w.len, w.head, w.r * S::kRows + row, d, v,
-                                    all_sums[S::kRows + row], all_sums[row]);
-                }
-            }
+            if (joins) join_parts<kDim, kNT, kFew>(a, g, shared);
         }
+        if (last) break;
         __syncthreads();  // the states' memory becomes the ring again
     }
+    cp_async_wait<0>();
 }
 
-template <int kDim, int kNT>
-cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
-    using S = Shape<kDim, kNT>;
+template <int kDim, int kNT, bool kFew>
+cudaError_t launch_as(const AttentionArgs& a, int num_sms, cudaStream_t s) {
+    using S = Shape<kDim, kNT, kFew>;
     static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !allowed[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kv8_attention_kernel<kDim, kNT>,
+        e = cudaFuncSetAttribute(kv8_attention_kernel<kDim, kNT, kFew>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  S::kSeqsAt + kKv8MaxBatch * (int)sizeof(Seq));
         if (e != cudaSuccess) return e;
         if (dev < 64) allowed[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(num_sms * S::kBlocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(min(num_sms * S::kBlocks, kMostBlocks));
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSeqsAt + a.bt.batch * sizeof(Seq);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -887,7 +1168,17 @@ cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<kDim, kNT>, a);
+    return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<kDim, kNT, kFew>, a);
+}
+
+// At most this many units (row tiles times kv heads of all sequences) leave
+// blocks to cut them up.
+template <int kDim, int kNT>
+cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
+    const long long rows = (long long)a.bt.tokens * a.group;
+    const long long units = (rows / (8 * kNT) + a.bt.batch) * a.c.kv_heads;
+    return units <= num_sms / 4 ? launch_as<kDim, kNT, true>(a, num_sms, s)
+                                : launch_as<kDim, kNT, false>(a, num_sms, s);
 }
 
 }  // namespace
@@ -914,6 +1205,7 @@ cudaError_t launch_kv8_attention(const void* q, long long q_stride, int heads,
     a.q_stride = q_stride;
     a.heads = heads;
     a.group = heads / c.kv_heads;
+    a.group_inverse = a.group == 1 ? 0xffffffffu : (unsigned)((1ull << 32) / a.group);
     a.scale = softmax_scale * 1.4426950408889634f;
     a.window = window;
     a.sinks = sinks;

@@ -75,6 +75,7 @@ def test_batches(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL), (dict(tokens=0), RANGE),
     (dict(heads=3), SHAPE), (dict(heads=0), SHAPE), (dict(q_stride=504), SHAPE),
+    (dict(tokens=2 ** 30), RANGE),
     (dict(q_stride=516), SHAPE), (dict(window=-1), RANGE), (dict(sinks=-1), RANGE),
     (dict(scale=float("nan")), RANGE), (dict(scale=float("inf")), RANGE),
     (dict(q=P(10) + 2), ALIGN), (dict(out=P(11) + 8), ALIGN), (dict(lse=P(12) + 2), ALIGN),

@@ -142,9 +142,11 @@ def test_attention(dev, case):
 
 
 @pytest.mark.parametrize("q_lens,kv_lens,group,dim,window", [
-    ([1], [9000], 8, 128, 0), ([1] * 9, [700, 3, 1500, 90, 64, 65, 2048, 31, 1000], 4, 128, 0),
+    ([1], [9000], 8, 128, 0), ([1], [90001], 8, 128, 0), ([1, 2], [70000, 20011], 2, 64, 0),
+    ([3], [70003], 1, 128, 30000), ([1] * 9, [700, 3, 1500, 90, 64, 65, 2048, 31, 1000], 4, 128, 0),
     ([40], [1400], 8, 128, 0), ([130], [600], 1, 64, 100), ([64, 7], [900, 1100], 16, 64, 0),
-    ([35], [1000], 4, 256, 0)])
+    ([35], [1000], 4, 256, 0), ([1] * 40, [64 * i + 1 for i in range(40)], 3, 128, 0),
+    ([5], [40000], 8, 256, 0)])
 def test_attention_on_longer_rows(dev, q_lens, kv_lens, group, dim, window):
     """Longer sequences than the loops of the plain statement serve, in fp64 tensor form."""
     s = Setup(dev, q_lens, kv_lens, 2, dim, 64, seed=11)
