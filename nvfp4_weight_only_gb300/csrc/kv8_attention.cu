@@ -147,7 +147,11 @@ __device__ __forceinline__ int row_tiles(const AttentionArgs& a, int len, int ro
     return (len * a.group + rows - 1) / rows;  // at most 2^30 rows, `rows` a constant
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(full ? 16 : 0)
                  : "memory");
@@ -265,6 +269,14 @@ public:
         return a.bt.page_table[(size_t)s.b * a.bt.table_width + (j >> a.bt.page_shift)];
     }
 
+    // Where the lane's 16 bytes of a tile's it-th 512 bytes go: 8 rows of 128
+    // bytes on the swizzle is the same again.
+    __device__ __forceinline__ uint32_t copy_at(int it) const {
+        constexpr int kPieces = kDim / 16, kPeriod = 8 * kDim / 512;
+        const int piece = (it % kPeriod) * 32 + lane;
+        return piece_at<kDim>(piece / kPieces, piece % kPieces) + it / kPeriod * kPeriod * 512;
+    }
+
     // Starts the copy of tile x, the warp's number-th of the segment.
     __device__ __forceinline__ void issue(int x, int number, int stage) {
         if (x < seg->x1) {
@@ -276,22 +288,32 @@ public:
             const bool ok = entry >= 0 && entry < a.c.pages;
             if (!ok && entry != -2) kv8_report(a.bt);
             const uint32_t dst = smem + (warp * S::kStages + stage) * S::kStageBytes;
-            const int j0 = tile_start(seg->keys, x);
-            const int lo = seg->keys.lo, hi = seg->keys.hi;
+            const Keys& keys = seg->keys;
+            const int j0 = tile_start(keys, x);
             const size_t at = (size_t)(ok ? entry : 0) * a.c.kv_heads + seg->head;
             const size_t from =
-                ((at << a.bt.page_shift) + (j0 & ((1 << a.bt.page_shift) - 1))) * kDim;
+                ((at << a.bt.page_shift) + (j0 & ((1 << a.bt.page_shift) - 1))) * kDim + lane * 16;
+            const uint8_t* const k = a.c.k_codes + from;
+            const uint8_t* const v = a.c.v_codes + from;
             constexpr int kPieces = kDim / 16;
+            if (ok && j0 + kTile <= keys.hi && (j0 >= keys.lo || j0 + kTile <= a.sinks)) {
 #pragma unroll
-            for (int it = 0; it < kPieces / 2; ++it) {
-                const int row = (it * 32 + lane) / kPieces, piece = (it * 32 + lane) % kPieces;
-                const int j = j0 + row;
-                // keys that no row sees are copied as zeros
-                const bool live = ok && j < hi && (j >= lo || j < a.sinks);
-                const size_t off = live ? from + (it * 32 + lane) * 16 : 0;
-                const uint32_t to = dst + piece_at<kDim>(row, piece);
-                cp_async16(to, a.c.k_codes + off, live);
-                cp_async16(to + kTile * kDim, a.c.v_codes + off, live);
+                for (int it = 0; it < kPieces / 2; ++it) {
+                    const uint32_t to = dst + copy_at(it);
+                    cp_async16(to, k + it * 512);
+                    cp_async16(to + kTile * kDim, v + it * 512);
+                }
+            } else {
+                // keys that no row sees are filled with zeros
+#pragma unroll
+                for (int it = 0; it < kPieces / 2; ++it) {
+                    const int j = j0 + (it * 32 + lane) / kPieces;
+                    const bool live =
+                        ok && j < keys.hi && (j >= keys.lo || j < a.sinks);
+                    const uint32_t to = dst + copy_at(it);
+                    cp_async16_or_zero(to, live ? k + it * 512 : a.c.k_codes, live);
+                    cp_async16_or_zero(to + kTile * kDim, live ? v + it * 512 : a.c.v_codes, live);
+                }
             }
             if (lane < 2) {
                 const uint32_t to =
