@@ -200,9 +200,13 @@ nvfp4_status kv8_read(const kv8_cache* cache, const kv8_batch* batch, int tokens
 
 size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* batch, int tokens,
                                      int heads) {
-    if (!cache || !batch || tokens < 1 || heads < 1) return 0;
+    if (!cache || !batch || tokens < 1 || cache->kv_heads < 1 || heads < cache->kv_heads ||
+        batch->batch < 1)
+        return 0;
     const int sms = nvf::device_sm_count();
-    return nvf::kDataOffset + nvf::kv8_attention_data_bytes(cache->head_dim, sms > 0 ? sms : 160);
+    return nvf::kDataOffset +
+           nvf::kv8_attention_data_bytes(cache->head_dim, tokens, heads / cache->kv_heads,
+                                         batch->batch, sms > 0 ? sms : 160);
 }
 
 nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int heads,
@@ -226,13 +230,14 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
         return NVFP4_ERR_ALIAS;
     const int sms = nvf::device_sm_count();
     if (sms <= 0) return NVFP4_ERR_CUDA;
-    if (ws_bytes < nvf::kDataOffset + nvf::kv8_attention_data_bytes(dim, sms))
+    if (ws_bytes < nvf::kDataOffset + nvf::kv8_attention_data_bytes(
+                                          dim, tokens, heads / cache->kv_heads, batch->batch, sms))
         return NVFP4_ERR_WORKSPACE;
     char* w = reinterpret_cast<char*>(ws);
     return cuda_status(nvf::launch_kv8_attention(
         q, q_stride, heads, cache_args(cache), batch_args(batch, cache, tokens), softmax_scale,
-        window, sinks, out, lse, reinterpret_cast<int*>(w + nvf::kStatusBytes),
-        w + nvf::kDataOffset, sms, stream));
+        window, sinks, out, lse, reinterpret_cast<int*>(w),
+        reinterpret_cast<int*>(w + nvf::kStatusBytes), w + nvf::kDataOffset, sms, stream));
 }
 
 nvfp4_status kv8_batch_status(const kv8_batch* batch, cudaStream_t stream) {

@@ -10,6 +10,8 @@ namespace nvf {
 // Written to a batch's status word for an index outside its buffers (the
 // value of NVFP4_ERR_RANGE).
 constexpr int kKv8BadIndex = 4;
+// Written to a workspace's status word by an abandoned wait (NVFP4_ERR_TIMEOUT).
+constexpr int kKv8Timeout = 7;
 constexpr int kKv8MaxBatch = 1024;
 
 struct Kv8CacheArgs {
@@ -55,11 +57,13 @@ cudaError_t launch_kv8_read(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, void*
                             void* v_out, cudaStream_t s);
 
 // kv8_attention.cu
-size_t kv8_attention_data_bytes(int head_dim, int num_sms);
+size_t kv8_attention_data_bytes(int head_dim, long long tokens, int group, int batch,
+                                int num_sms);
 cudaError_t launch_kv8_attention(const void* q, long long q_stride, int heads,
                                  const Kv8CacheArgs& c, const Kv8BatchArgs& bt,
                                  float softmax_scale, int window, int sinks, void* out, float* lse,
-                                 int* counters, void* partials, int num_sms, cudaStream_t s);
+                                 int* status, int* counters, void* partials, int num_sms,
+                                 cudaStream_t s);
 
 // rmsnorm.cu: codes null for the bf16 output, else out null; H a multiple of
 // 8, at most kNormMaxWidth.

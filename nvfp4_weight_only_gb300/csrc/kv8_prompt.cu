@@ -1,0 +1,791 @@
+// kv8_prompt.cu -- attention of many rows per kv head (a prompt's tokens, or
+// a chunk of one) over the paged E4M3 cache: the same operator as
+// kv8_attention.cu, on tcgen05.
+//
+// What bounds it: the products, 4 * head_dim flops per row and key.  A block
+// takes 256 rows of one kv head as two 128-row tiles and goes through its keys
+// 128 at a time:
+//   S = q K^T      128 x 128, both operands in shared memory, f16 -> fp32 in TMEM
+//   P = 2^(t - m)  t = log2(e) s + log2(v_scale), one row per thread, f16 in TMEM
+//   O += P V       128 x head_dim, P from TMEM, V from shared memory
+// The two tiles alternate: while one's softmax runs, the tensor cores work on
+// the other's products.  8 warps do the softmax, 4 warps turn E4M3 pages into
+// f16 tiles (exactly) in the 128-byte swizzle that the tensor cores read, one
+// thread issues the products.  TMEM holds S (then P in its place) and O of both
+// tiles, all 512 columns.  K, V and q tiles are rows of 128 bytes (64 values),
+// 16-byte pieces XORed with the row; V is the transposed operand of the second
+// product, so both tiles are written alike.
+//
+// Softmax with a scale per page, as in kv8_attention.cu: O = sum P v_code,
+// l = sum P / v_scale.  m is the largest t when the row's O was last rescaled;
+// O is rescaled only when a tile's largest t exceeds it by kSlack, so P stays
+// below 2^(kPromptBias + kSlack) and most tiles read S twice and O never.  t,
+// m, l and O are fp32, P is f16.
+//
+// Blocks that share a unit leave partial states, which a second kernel joins
+// in the order of their ranges.  Every wait is bounded.
+#include <atomic>
+
+#include "kv8_schedule.cuh"
+
+namespace nvf {
+
+namespace {
+
+constexpr int kPromptKeys = 128;
+constexpr int kPromptRows = 256;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kConvertWarps = 4;
+constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 1) * 32;
+constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
+// Least rows per sequence and kv head, on average, for these kernels.
+constexpr int kPromptLeastRows = 96;
+constexpr float kPromptBias = 6.0f;
+constexpr float kSlack = 8.0f;
+
+using PromptTiling = TilingOf<kPromptRows, kPromptKeys, 2, 4>;
+
+// One block's note for the join: the unit whose first part it has, if that
+// unit has several.
+struct JoinNote {
+    int parts, q0, len, head, r;
+    unsigned slot0, slot1;
+    int pad;
+};
+
+template <int kDim>
+struct PromptShape {
+    static constexpr int kTileBytes = 128 * kDim * 2;  // of q, K or V
+    static constexpr int kQAt = 0;
+    static constexpr int kKAt = kQAt + 2 * kTileBytes;
+    static constexpr int kVAt = kKAt + 2 * kTileBytes;
+    // per buffer and group of 16 keys: k_scale, log2(v_scale), 1 / v_scale
+    static constexpr int kScalesAt = kVAt + 2 * kTileBytes;
+    // per buffer and key: which of its values are NaN (filled where rows are masked)
+    static constexpr int kNansAt = kScalesAt + 2 * kGroups * 16;
+    static constexpr int kRowScaleAt = kNansAt + 2 * kPromptKeys * kDim / 8;
+    static constexpr int kSeqsAt = kRowScaleAt + kPromptRows * 4;
+    static constexpr int kPartial = kPromptRows * (kDim + 2);  // fp32 words
+    // TMEM columns
+    static constexpr int kO = 256;  // S of tile w at 128 w, O of tile w at kO + kDim w
+};
+
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+          "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
+        "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
+        "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
+        "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+
+// The values pass through the wait, so that no use of them moves in front of it.
+__device__ __forceinline__ void tmem_wait_load(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                   "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
+                   "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                   "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Generic writes to shared memory before the tensor cores' reads.
+__device__ __forceinline__ void fence_shared_to_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle, 8 rows of 128 bytes per
+// 1024; `leading` is the distance of 64-value blocks (transposed operand).
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t leading) {
+    return (uint64_t)((at & 0x3ffffu) >> 4) | (uint64_t)(leading >> 4) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// Instruction descriptor: f16 operands, fp32 sums, 128 rows, n columns; the
+// second operand transposed or not.
+__device__ __forceinline__ constexpr uint32_t instruction(int n, bool transposed) {
+    return 1u << 4 | (transposed ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 |
+           (uint32_t)(128 / 16) << 24;
+}
+
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                         bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0)
+        : "memory");
+}
+
+// `bar` completes when all products issued so far have.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bar)
+                 : "memory");
+}
+
+// fp32 pairs.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The block's barriers, each completed once per use.
+struct Barriers {
+    uint64_t q_full;       // q tiles of a segment written
+    uint64_t k_full[2], k_empty[2];
+    uint64_t v_full[2], v_empty[2];  // and the page scales
+    uint64_t s_full[2];    // tile w: scores of a key tile; after the last key tile, O
+    uint64_t p_full[2];    // tile w: P written
+};
+
+template <int kDim, bool kFew>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    kv8_prompt_kernel(const AttentionArgs a, JoinNote* const notes, int* const status) {
+    using S = PromptShape<kDim>;
+    extern __shared__ __align__(1024) uint8_t dynamic[];
+    // the swizzle goes by address: tiles begin on multiples of 1024
+    uint8_t* const shared = dynamic + (-smem_addr(dynamic) & 1023u);
+    __shared__ Barriers bars;
+    __shared__ Plan<PromptTiling> plan;
+    __shared__ Segment segments[3];
+    __shared__ int work;
+    __shared__ volatile int abort;
+    __shared__ int nan_tile[2];  // per buffer: the last key tile in which a NaN was found
+    __shared__ uint32_t tmem_at;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t smem = smem_addr(shared);
+    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps;
+    Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_addr(&tmem_at))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        mbar_init(smem_addr(&bars.q_full), kSoftmaxWarps * 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&bars.k_full[i]), kConvertWarps * 32);
+            mbar_init(smem_addr(&bars.v_full[i]), kConvertWarps * 32);
+            mbar_init(smem_addr(&bars.k_empty[i]), 1);
+            mbar_init(smem_addr(&bars.v_empty[i]), 1);
+            mbar_init(smem_addr(&bars.s_full[i]), 1);
+            mbar_init(smem_addr(&bars.p_full[i]), 128);
+            nan_tile[i] = -1;
+        }
+        abort = 0;
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Scheduler<PromptTiling, kFew> scheduler(a, &plan, seqs, segments);
+    if (warp == kIssueWarp) {
+        const bool some = scheduler.start();
+        if (lane == 0) {
+            work = some;
+            notes[blockIdx.x].parts = 0;
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    // Waits for a barrier's completion number `uses` (from 0); false, with the
+    // status set, when it does not come in time.
+    auto wait_lane = [&](uint64_t& bar, unsigned uses) {
+        if (mbar_wait_bounded(smem_addr(&bar), uses & 1, &abort)) return true;
+        abort = 1;
+        *status = kKv8Timeout;
+        return false;
+    };
+    auto wait = [&](uint64_t& bar, unsigned uses) {  // the same answer for a whole warp
+        return __all_sync(0xffffffffu, wait_lane(bar, uses)) != 0;
+    };
+
+    // of the segments before this one: key tiles, and the completions of the
+    // two row tiles' barriers (a unit may lack the second)
+    unsigned done = 0, s_done[2] = {0, 0}, p_done[2] = {0, 0};
+    for (int number = 0; work; ++number) {
+        const Segment& g = segments[number % 3];
+        const int n = g.x1 - g.x0;
+        const bool last = g.last;
+        const int rows = min(g.len * a.group - g.r * kPromptRows, kPromptRows);
+        const int tiles = rows > 128 ? 2 : 1;  // 128-row tiles that hold rows
+        const Keys keys = g.keys;
+        auto tile_start = [&](int x) {
+            return (x < keys.sink_tiles ? x : keys.lo / kPromptKeys + x - keys.sink_tiles) *
+                   kPromptKeys;
+        };
+        auto masked = [&](int j0) {  // some row does not see some key of the tile
+            return j0 + kPromptKeys > keys.hi_min ||
+                   (j0 < keys.lo_max && j0 + kPromptKeys > a.sinks);
+        };
+        if (n <= 0) break;
+
+        if (warp < kSoftmaxWarps) {
+            // ---- q, then the softmax of tile w, a row per thread
+            const int w = warp >> 2;
+            {
+                constexpr int kLanes = kDim / 8;  // lanes per row
+                const int sub = lane / kLanes, d = lane % kLanes;
+#pragma unroll 4
+                for (int i = 0; i < kLanes; ++i) {
+                    const int row = warp * 32 + i * (32 / kLanes) + sub;
+                    const int unit_row = g.r * kPromptRows + row;
+                    const int token = token_of(a, unit_row);
+                    const bool live = token < g.len;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (live)
+                        x = reinterpret_cast<const uint4*>(
+                            a.q + (long long)(g.q0 + token) * a.q_stride +
+                            (size_t)(g.head * a.group + unit_row - token * a.group) * kDim)[d];
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                    float big = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        big = fmaxf(big, fmaxf(fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e]))));
+#pragma unroll
+                    for (int m = kLanes / 2; m > 0; m >>= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+                    // 2^e brings the row's largest value into [2^14, 2^15); a negative
+                    // softmax_scale goes into the sign of q, so larger scores stay larger
+                    const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 126);
+                    float up = __uint_as_float((uint32_t)(e + 127) << 23);
+                    if (a.scale < 0.0f) up = -up;
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = f16x2(bf16_lo(u[k]) * up, bf16_hi(u[k]) * up);
+                    uint8_t* const to = shared + S::kQAt + (row >> 7) * S::kTileBytes +
+                                        (d >> 3) * 128 * 128 + (row & 127) * 128 +
+                                        ((d ^ row) & 7) * 16;
+                    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (d == 0)
+                        reinterpret_cast<float*>(shared + S::kRowScaleAt)[row] =
+                            fabsf(a.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
+                }
+                fence_shared_to_async();
+                mbar_arrive(smem_addr(&bars.q_full));
+            }
+            if (w < tiles) {
+                bool ok = wait(bars.q_full, number);  // and the row scales
+                const int row = tid & 127;
+                const int unit_row = g.r * kPromptRows + w * 128 + row;
+                const int token = token_of(a, unit_row);
+                const int hi = token < g.len ? g.first + token + 1 : 0;
+                const int lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+                const float row_scale =
+                    reinterpret_cast<const float*>(shared + S::kRowScaleAt)[w * 128 + row];
+                const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+                const uint32_t s_at = lanes + w * 128, o_at = lanes + S::kO + w * kDim;
+                float top = -INFINITY, sum = 0.0f;
+                uint32_t nans[kDim / 32];
+#pragma unroll
+                for (int i = 0; i < kDim / 32; ++i) nans[i] = 0;
+                const unsigned s_uses = w ? s_done[1] : s_done[0];
+                for (int i = 0; i < n && ok; ++i) {
+                    const unsigned at = done + i;
+                    const int buf = at & 1;
+                    const int j0 = tile_start(g.x0 + i);
+                    const bool guard = masked(j0);
+                    ok = wait(bars.v_full[buf], at >> 1) && wait(bars.s_full[w], s_uses + i);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    const float4* const scales =
+                        reinterpret_cast<const float4*>(shared + S::kScalesAt) + buf * kGroups;
+                    auto seen = [&](int j) { return j < hi && (j >= lo || j < a.sinks); };
+                    // the tile's largest t
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kPromptKeys / 32; ++c) {
+                        float s[32];
+                        tmem_load32(s_at + 32 * c, s);
+                        tmem_wait_load(s);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (guard) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (!seen(j0 + 32 * c + 16 * h + e)) s[16 * h + e] = -INFINITY;
+                            }
+                            float m = s[16 * h];
+#pragma unroll
+                            for (int e = 1; e < 16; ++e) m = fmaxf(m, s[16 * h + e]);
+                            const float4 sc = scales[2 * c + h];
+                            most = fmaxf(most, fmaf(m, row_scale * sc.x, sc.y));
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, most > top + kSlack)) {
+                        const float now = fmaxf(most, top);
+                        const float keep = now == -INFINITY ? 1.0f : exp2_fast(top - now);
+                        top = now;
+                        sum *= keep;
+                        // the scores' completion follows that of the product before
+                        if (i > 0) {
+#pragma unroll
+                            for (int c = 0; c < kDim / 32; ++c) {
+                                float v[32];
+                                tmem_load32(o_at + 32 * c, v);
+                                tmem_wait_load(v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] *= keep;
+                                tmem_store32(o_at + 32 * c, v);
+                            }
+                        }
+                    }
+                    const float shift = kPromptBias - (top == -INFINITY ? 0.0f : top);
+#pragma unroll
+                    for (int c = 0; c < kPromptKeys / 32; ++c) {
+                        float s[32];
+                        tmem_load32(s_at + 32 * c, s);
+                        tmem_wait_load(s);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 sc = scales[2 * c + h];
+                            const float by = row_scale * sc.x, off = sc.y + shift;
+                            const uint64_t by2 = pair(by, by), off2 = pair(off, off);
+                            uint64_t total = pair(0.0f, 0.0f);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float2 t = unpair(fma2(
+                                    pair(s[16 * h + 2 * e], s[16 * h + 2 * e + 1]), by2, off2));
+                                if (guard) {
+                                    const int j = j0 + 32 * c + 16 * h + 2 * e;
+                                    if (!seen(j)) t.x = -INFINITY;
+                                    if (!seen(j + 1)) t.y = -INFINITY;
+                                }
+                                t.x = exp2_fast(t.x);
+                                t.y = exp2_fast(t.y);
+                                total = add2(total, pair(t.x, t.y));
+                                p[8 * h + e] = f16x2(t.x, t.y);
+                            }
+                            const float2 two = unpair(total);
+                            sum = fmaf(two.x + two.y, sc.z, sum);
+                        }
+                        tmem_store16(s_at + 16 * c, p);
+                    }
+                    if (guard && nan_tile[buf] == (int)at) {
+                        const uint32_t* const bits = reinterpret_cast<const uint32_t*>(
+                            shared + S::kNansAt + buf * kPromptKeys * kDim / 8);
+                        for (int j = 0; j < kPromptKeys; ++j)
+                            if (seen(j0 + j)) {
+#pragma unroll
+                                for (int k = 0; k < kDim / 32; ++k) nans[k] |= bits[j * kDim / 32 + k];
+                            }
+                    }
+                    __syncwarp();
+                    tmem_wait_store();
+                    tmem_fence_before();
+                    mbar_arrive(smem_addr(&bars.p_full[w]));
+                }
+                if (ok && wait(bars.s_full[w], s_uses + n)) {
+                    tmem_fence_after();
+                    const bool live = token < g.len;
+                    const bool whole = g.parts == 1;
+                    const size_t out_row = (size_t)(g.q0 + (live ? token : 0)) * a.heads +
+                                           g.head * a.group +
+                                           (live ? unit_row - token * a.group : 0);
+                    float* const part = a.partials + (size_t)g.slot * S::kPartial;
+                    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+#pragma unroll
+                    for (int c = 0; c < kDim / 32; ++c) {
+                        float v[32];
+                        __syncwarp();
+                        tmem_load32(o_at + 32 * c, v);
+                        tmem_wait_load(v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (nans[c] >> e & 1) v[e] = NAN;
+                        if (live && whole) {
+                            uint4* const to =
+                                reinterpret_cast<uint4*>(a.out + out_row * kDim + 32 * c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                to[e] = make_uint4(bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                   bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                   bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                   bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                        } else if (live) {
+                            float4* const to = reinterpret_cast<float4*>(
+                                part + (w * 128 + row) * kDim + 32 * c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2],
+                                                    v[4 * e + 3]);
+                        }
+                    }
+                    if (live && whole && a.lse)
+                        a.lse[out_row] = sum == 0.0f ? -INFINITY
+                                                     : 0.69314718055994531f *
+                                                           ((top - kPromptBias) + log2f(sum));
+                    if (live && !whole) {
+                        part[kPromptRows * kDim + w * 128 + row] = top;
+                        part[kPromptRows * (kDim + 1) + w * 128 + row] = sum;
+                    }
+                    tmem_fence_before();
+                }
+            }
+        } else if (warp < kIssueWarp) {
+            // ---- pages to f16 tiles: a lane has 16 values of one key at a time
+            const int t = warp - kSoftmaxWarps, q = lane >> 2;
+            constexpr int kItems = kDim / 16;
+            // lanes 0..3 and 4..7 write pieces of an even and an odd row, which the
+            // swizzle puts on different banks
+            const int piece = kDim == 128 ? (lane & 3) + 4 * (t >> 1) : lane & 3;
+            const int row0 = kDim == 128 ? 8 * (t & 1) + q : 8 * t + q;
+            constexpr int kRowStep = kDim == 128 ? 16 : 32;
+            const int page_mask = (1 << a.bt.page_shift) - 1;
+            uint4 k[kItems], v[kItems];
+            // lane l < 8: the table's entry for keys 16 l .. of tile x, -2 without keys
+            auto find_pages = [&](int x) {
+                const int j = tile_start(x) + 16 * lane;
+                int e = -2;
+                if (lane < kGroups && x < g.x1 && j < keys.hi)
+                    e = a.bt.page_table[(size_t)g.b * a.bt.table_width + (j >> a.bt.page_shift)];
+                return e;
+            };
+            auto load = [&](uint4 (&to)[kItems], const uint8_t* codes, int entries, int x) {
+                const int j0 = tile_start(x);
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int row = row0 + i * kRowStep, j = j0 + row;
+                    const int e = __shfl_sync(0xffffffffu, entries, row >> 4);
+                    const bool live = x < g.x1 && e >= 0 && e < a.c.pages && j < keys.hi &&
+                                      (j >= keys.lo || j < a.sinks);
+                    to[i] = make_uint4(0, 0, 0, 0);
+                    if (live)
+                        to[i] = __ldg(reinterpret_cast<const uint4*>(
+                            codes +
+                            ((((size_t)e * a.c.kv_heads + g.head) << a.bt.page_shift) +
+                             (j & page_mask)) *
+                                kDim +
+                            piece * 16));
+                }
+            };
+            auto store = [&](const uint4& x, uint32_t tile, int row) {
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                uint32_t h[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[2 * e] = e4m3x2_to_f16x2(u[e]);
+                    h[2 * e + 1] = e4m3x2_hi_to_f16x2(u[e]);
+                }
+                uint8_t* const to = shared + tile + (piece >> 2) * 128 * 128 + row * 128;
+                const int c = 2 * (piece & 3);
+                *reinterpret_cast<uint4*>(to + ((c ^ row) & 7) * 16) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + (((c + 1) ^ row) & 7) * 16) =
+                    make_uint4(h[4], h[5], h[6], h[7]);
+            };
+            // the scales of keys 16 l .. in lane l of the first of these warps
+            auto load_scales = [&](int entry) {
+                float2 s = make_float2(0.0f, 0.0f);  // no page: every key is masked
+                if (t == 0 && entry != -2) {
+                    if (entry >= 0 && entry < a.c.pages) {
+                        const size_t i = (size_t)entry * a.c.kv_heads + g.head;
+                        s = make_float2(a.c.k_scales[i], fmaxf(a.c.v_scales[i], 1.17549435e-38f));
+                    } else {
+                        kv8_report(a.bt);
+                    }
+                }
+                return s;
+            };
+            int entries = find_pages(g.x0);
+            float2 page_scales = load_scales(entries);
+            load(k, a.c.k_codes, entries, g.x0);
+            load(v, a.c.v_codes, entries, g.x0);
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const unsigned at = done + i;
+                const int buf = at & 1;
+                const int x = g.x0 + i;
+                const int next = find_pages(x + 1);
+                // k_empty and v_empty complete once per use of the buffer
+                if (at >= 2) ok = wait(bars.k_empty[buf], (at >> 1) - 1);
+                if (!ok) break;
+#pragma unroll
+                for (int m = 0; m < kItems; ++m)
+                    store(k[m], S::kKAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                fence_shared_to_async();
+                mbar_arrive(smem_addr(&bars.k_full[buf]));
+                const float2 next_scales = load_scales(next);
+                load(k, a.c.k_codes, next, x + 1);
+                if (at >= 2) ok = wait(bars.v_empty[buf], (at >> 1) - 1);
+                if (!ok) break;
+                if (t == 0 && lane < kGroups) {
+                    const float vs = page_scales.y;
+                    const float4 sc =
+                        vs > 0.0f ? make_float4(page_scales.x, __log2f(vs), __fdividef(1.0f, vs), 0.0f)
+                                  : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                    reinterpret_cast<float4*>(shared + S::kScalesAt)[buf * kGroups + lane] = sc;
+                }
+                if (masked(tile_start(x))) {
+                    // NaNs out of the product, and where they were
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int m = 0; m < kItems; ++m) {
+                        uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t bad = nan_bytes(u[e]) >> 7;
+                            u[e] &= ~(bad * 0xffu);
+                            bits |= ((bad * 0x00204081u) >> 21 & 0xfu) << (4 * e);
+                        }
+                        v[m] = make_uint4(u[0], u[1], u[2], u[3]);
+                        any |= bits;
+                        reinterpret_cast<uint16_t*>(
+                            shared + S::kNansAt +
+                            buf * kPromptKeys * kDim / 8)[(row0 + m * kRowStep) * kDim / 16 + piece] =
+                            (uint16_t)bits;
+                    }
+                    if (any) nan_tile[buf] = (int)at;
+                }
+#pragma unroll
+                for (int m = 0; m < kItems; ++m)
+                    store(v[m], S::kVAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                fence_shared_to_async();
+                mbar_arrive(smem_addr(&bars.v_full[buf]));
+                load(v, a.c.v_codes, next, x + 1);
+                page_scales = next_scales;
+            }
+        } else if (lane == 0) {
+            // ---- the products
+            const uint64_t q_op = operand(smem + S::kQAt, 16);
+            const uint64_t k_op = operand(smem + S::kKAt, 16);
+            const uint64_t v_op = operand(smem + S::kVAt, 128 * 128);
+            constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBlockUnits = 128 * 128 >> 4;
+            auto scores = [&](int w, int buf) {
+#pragma unroll
+                for (int k = 0; k < kDim / 16; ++k) {
+                    const uint32_t off = (k / 4) * kBlockUnits + (k % 4) * 2;
+                    mma_shared(tmem + w * 128, q_op + w * kTileUnits + off,
+                               k_op + buf * kTileUnits + off, instruction(kPromptKeys, false),
+                               k > 0);
+                }
+                mma_commit(smem_addr(&bars.s_full[w]));
+            };
+            bool ok =
+                wait_lane(bars.q_full, number) && wait_lane(bars.k_full[done & 1], done >> 1);
+            if (ok) {
+                tmem_fence_after();
+                for (int w = 0; w < tiles; ++w) scores(w, done & 1);
+                mma_commit(smem_addr(&bars.k_empty[done & 1]));
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                const unsigned at = done + i;
+                const int buf = at & 1;
+                const bool more = i + 1 < n;
+                ok = wait_lane(bars.v_full[buf], at >> 1);
+                for (int w = 0; w < tiles && ok; ++w) {
+                    ok = wait_lane(bars.p_full[w], (w ? p_done[1] : p_done[0]) + i);
+                    if (ok && more && w == 0) ok = wait_lane(bars.k_full[buf ^ 1], (at + 1) >> 1);
+                    if (!ok) break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kPromptKeys / 16; ++k)
+                        mma_tmem(tmem + S::kO + w * kDim, tmem + w * 128 + 8 * k,
+                                 v_op + buf * kTileUnits + k * (2048 >> 4),
+                                 instruction(kDim, true), i > 0 || k > 0);
+                    if (more)
+                        scores(w, buf ^ 1);
+                    else
+                        mma_commit(smem_addr(&bars.s_full[w]));
+                }
+                if (ok) {
+                    mma_commit(smem_addr(&bars.v_empty[buf]));
+                    if (more) mma_commit(smem_addr(&bars.k_empty[buf ^ 1]));
+                }
+            }
+            if (!ok) {
+                // products under way end before the memory they use is given back
+                mma_commit(smem_addr(&bars.q_full));
+                __nanosleep(100000);
+            }
+        }
+        __syncwarp();
+        if (warp == kIssueWarp) {
+            if (lane == 0 && g.parts > 1 && g.counter == blockIdx.x)
+                notes[blockIdx.x] =
+                    JoinNote{g.parts, g.q0, g.len, g.head, g.r, g.slot0, g.slot1, 0};
+            if (!last) scheduler.next();
+        }
+        done += n;
+        for (int w = 0; w < tiles; ++w) {
+            s_done[w] += n + 1;  // the last one is for O
+            p_done[w] += n;
+        }
+        tmem_fence_before();
+        __syncthreads();
+        tmem_fence_after();
+        if (last || abort) break;
+    }
+    __syncthreads();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+                     : "memory");
+}
+
+// Joins the parts of the unit whose first part block blockIdx.x had, for 16 of
+// its rows.
+template <int kDim>
+__global__ void __launch_bounds__(128) kv8_prompt_join_kernel(const AttentionArgs a,
+                                                              const JoinNote* const notes) {
+    using S = PromptShape<kDim>;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const JoinNote g = notes[blockIdx.x];
+    if (g.parts < 2) return;
+    auto part = [&](int i) {
+        return a.partials + (size_t)(i == 0 ? g.slot0 : g.slot1 + 2 * (i - 1)) * S::kPartial;
+    };
+    for (int item = threadIdx.x; item < 16 * kDim / 4; item += 128) {
+        const int row = blockIdx.y * 16 + item / (kDim / 4), d = item % (kDim / 4) * 4;
+        const int unit_row = g.r * kPromptRows + row;
+        if (token_of(a, unit_row) >= g.len) continue;
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int i = 0; i < g.parts; ++i) top = fmaxf(top, part(i)[kPromptRows * kDim + row]);
+        float sum = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i < g.parts; ++i) {
+            const float* p = part(i);
+            const float4 y = *reinterpret_cast<const float4*>(p + row * kDim + d);
+            const float f = weight_of(p[kPromptRows * kDim + row], top);
+            sum = fmaf(p[kPromptRows * (kDim + 1) + row], f, sum);
+            v.x = fmaf(y.x, f, v.x);
+            v.y = fmaf(y.y, f, v.y);
+            v.z = fmaf(y.z, f, v.z);
+            v.w = fmaf(y.w, f, v.w);
+        }
+        store_row<kDim>(a, g.q0, g.len, g.head, unit_row, d, v, top - kPromptBias, sum);
+    }
+}
+
+template <int kDim, bool kFew>
+cudaError_t launch(const AttentionArgs& a, JoinNote* notes, int* status, int num_sms,
+                   cudaStream_t s) {
+    using S = PromptShape<kDim>;
+    static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !allowed[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kv8_prompt_kernel<kDim, kFew>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + S::kSeqsAt + kKv8MaxBatch * (int)sizeof(Seq));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kPromptThreads);
+    cfg.dynamicSmemBytes = 1024 + S::kSeqsAt + a.bt.batch * sizeof(Seq);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<kDim, kFew>, a, notes, status);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(num_sms, kPromptRows / 16);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv8_prompt_join_kernel<kDim>, a, (const JoinNote*)notes);
+}
+
+}  // namespace
+
+bool kv8_prompt_applies(int head_dim, long long tokens, int group, int batch) {
+    return head_dim <= 128 && tokens * group >= (long long)kPromptLeastRows * batch;
+}
+
+size_t kv8_prompt_data_bytes(int head_dim, int num_sms) {
+    const size_t notes = ((size_t)num_sms * sizeof(JoinNote) + 255) / 256 * 256;
+    return notes + (size_t)num_sms * 2 * kPromptRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv8_prompt(AttentionArgs a, void* data, int* status, int num_sms,
+                              cudaStream_t s) {
+    JoinNote* const notes = reinterpret_cast<JoinNote*>(data);
+    a.partials = reinterpret_cast<float*>(reinterpret_cast<char*>(data) +
+                                          ((size_t)num_sms * sizeof(JoinNote) + 255) / 256 * 256);
+    const long long rows = (long long)a.bt.tokens * a.group;
+    const bool few = (rows / kPromptRows + a.bt.batch) * a.c.kv_heads <= num_sms / 2;
+    if (a.c.head_dim == 64)
+        return few ? launch<64, true>(a, notes, status, num_sms, s)
+                   : launch<64, false>(a, notes, status, num_sms, s);
+    return few ? launch<128, true>(a, notes, status, num_sms, s)
+               : launch<128, false>(a, notes, status, num_sms, s);
+}
+
+}  // namespace nvf

@@ -146,7 +146,9 @@ def test_attention(dev, case):
     ([3], [70003], 1, 128, 30000), ([1] * 9, [700, 3, 1500, 90, 64, 65, 2048, 31, 1000], 4, 128, 0),
     ([40], [1400], 8, 128, 0), ([130], [600], 1, 64, 100), ([64, 7], [900, 1100], 16, 64, 0),
     ([35], [1000], 4, 256, 0), ([1] * 40, [64 * i + 1 for i in range(40)], 3, 128, 0),
-    ([5], [40000], 8, 256, 0)])
+    ([5], [40000], 8, 256, 0), ([64], [3000], 8, 128, 0), ([100, 3, 130], [700, 1200, 130], 4, 64, 0),
+    ([300], [900], 2, 128, 77), ([16, 90], [2000, 95], 16, 64, 500), ([256], [257], 5, 128, 0),
+    ([97], [4001], 1, 128, 0)])
 def test_attention_on_longer_rows(dev, q_lens, kv_lens, group, dim, window):
     """Longer sequences than the loops of the plain statement serve, in fp64 tensor form."""
     s = Setup(dev, q_lens, kv_lens, 2, dim, 64, seed=11)
@@ -224,12 +226,14 @@ def test_workspace_serves_any_sequence_of_shapes(dev):
         assert torch.equal(ffi.kv8_attention(qs, small.cache, small.batch, 0.1, ws=ws), want_s)
 
 
-def test_masked_values_do_not_enter(dev):
+@pytest.mark.parametrize("n,kv,window,dim", [(9, 60, 11, 128), (9, 60, 11, 64), (9, 60, 11, 256),
+                                             (40, 300, 90, 128), (64, 200, 100, 64)])
+def test_masked_values_do_not_enter(dev, n, kv, window, dim):
     """NaN in a later token's k and v, and in tokens that the window has left behind, changes no
     query that does not see them (stale rows hold NaN in every test here)."""
-    page, n, kv, window = 16, 9, 60, 11
-    s = Setup(dev, [n], [kv], 2, 128, page)
-    q = draw_q(n, 8, 128, 4)
+    page = 16
+    s = Setup(dev, [n], [kv], 2, dim, page)
+    q = draw_q(n, 8, dim, 4)
     for name in "kv":
         for j in list(range(0, kv - n + 1 - window)) + [kv - 1, kv - 4]:
             s.codes[name][int(s.table[0, j // page]), :, j % page] = NAN_CODE
@@ -246,14 +250,18 @@ def test_masked_values_do_not_enter(dev):
     s.codes = clean
 
 
-def test_one_value_code_nan_spoils_only_its_column(dev):
-    s = Setup(dev, [2], [30], 1, 64, 16)
-    j = 29
-    s.codes["v"][int(s.table[0, j // 16]), 0, j % 16, 5] = NAN_CODE
+@pytest.mark.parametrize("n,dim", [(2, 64), (2, 128), (60, 64), (60, 128)])
+def test_one_value_code_nan_spoils_only_its_column(dev, n, dim):
+    kv = n + 28
+    s = Setup(dev, [n], [kv], 1, dim, 16)
+    for j, d in ((kv - 1, 5), (kv - 2, 33)):
+        s.codes["v"][int(s.table[0, j // 16]), 0, j % 16, d] = NAN_CODE
     s.upload()
-    out, _ = run_attention(s, draw_q(2, 4, 64, 9), 0.1)
+    out, _ = run_attention(s, draw_q(n, 4, dim, 9), 0.1)
     bad = torch.isnan(out.float())
-    assert not bad[0].any() and bad[1, :, 5].all() and bad[1].sum() == 4
+    assert not bad[:n - 2].any()
+    assert bad[n - 2, :, 33].all() and bad[n - 2].sum() == 4
+    assert bad[n - 1, :, [5, 33]].all() and bad[n - 1].sum() == 8
 
 
 def test_large_scores_and_values(dev):
