@@ -9,7 +9,8 @@
 //   P = 2^(t - m)  t = log2(e) s + log2(v_scale), one row per thread, f16 in TMEM
 //   O += P V       128 x head_dim, P from TMEM, V from shared memory
 // The two tiles alternate: while one's softmax runs, the tensor cores work on
-// the other's products.  8 warps do the softmax, 4 warps turn E4M3 pages into
+// the other's products.  8 warps do the softmax, one copies pages into shared
+// memory (the bulk-copy engine, 16 keys at a time), 4 turn their E4M3 bytes into
 // f16 tiles (exactly) in the 128-byte swizzle that the tensor cores read, one
 // thread issues the products.  TMEM holds S (then P in its place) and O of both
 // tiles, all 512 columns.  K, V and q tiles are rows of 128 bytes (64 values),
@@ -36,7 +37,7 @@ constexpr int kPromptKeys = 128;
 constexpr int kPromptRows = 256;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
-constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 1) * 32;
+constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
 // Least rows per sequence and kv head, on average, for these kernels.
 constexpr int kPromptLeastRows = 96;
@@ -59,10 +60,15 @@ struct PromptShape {
     static constexpr int kQAt = 0;
     static constexpr int kKAt = kQAt + 2 * kTileBytes;
     static constexpr int kVAt = kKAt + 2 * kTileBytes;
-    // per buffer and group of 16 keys: k_scale, log2(v_scale), 1 / v_scale
-    static constexpr int kScalesAt = kVAt + 2 * kTileBytes;
+    // E4M3 bytes of the next K and V tile, as they come
+    static constexpr int kRawAt = kVAt + kTileBytes;
+    static constexpr int kRawBytes = kPromptKeys * kDim;
+    // for each of 4 key tiles in turn and group of 16 keys: k_scale,
+    // log2(v_scale), 1 / v_scale (the copies are at most 3 tiles ahead of the
+    // softmax)
+    static constexpr int kScalesAt = kRawAt + 2 * kRawBytes;
     // per buffer and key: which of its values are NaN (filled where rows are masked)
-    static constexpr int kNansAt = kScalesAt + 2 * kGroups * 16;
+    static constexpr int kNansAt = kScalesAt + 4 * kGroups * 16;
     static constexpr int kRowScaleAt = kNansAt + 2 * kPromptKeys * kDim / 8;
     static constexpr int kSeqsAt = kRowScaleAt + kPromptRows * 4;
     static constexpr int kPartial = kPromptRows * (kDim + 2);  // fp32 words
@@ -193,11 +199,90 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// One row of a tile of scores, from TMEM at s_at.
+struct ScoreRow {
+    uint32_t s_at;
+    float row_scale;
+    const float4* scales;  // per 16 keys: k_scale, log2(v_scale), 1 / v_scale
+    int hi, lo, sinks;     // keys that the row sees, from the tile's first
+};
+
+template <bool kGuard>
+__device__ __forceinline__ bool sees(const ScoreRow& r, int j) {
+    return !kGuard || (j < r.hi && (j >= r.lo || j < r.sinks));
+}
+
+// The largest t of the row.  The next 32 scores are on their way while 32 are
+// used.
+template <bool kGuard>
+__device__ __forceinline__ float largest(const ScoreRow& r) {
+    float most = -INFINITY;
+    float s[2][32];
+    tmem_load32(r.s_at, s[0]);
+#pragma unroll
+    for (int c = 0; c < kPromptKeys / 32; ++c) {
+        float(&x)[32] = s[c & 1];
+        tmem_wait_load(x);
+        if (c + 1 < kPromptKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (sees<kGuard>(r, 32 * c + 16 * h + e)) m[e & 3] = fmaxf(m[e & 3], x[16 * h + e]);
+            const float4 sc = r.scales[2 * c + h];
+            most = fmaxf(most, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])),
+                                    r.row_scale * sc.x, sc.y));
+        }
+    }
+    return most;
+}
+
+// P = 2^(t + shift) over the scores' place, as f16; returns sum P / v_scale.
+template <bool kGuard>
+__device__ __forceinline__ float weights(const ScoreRow& r, float shift) {
+    float sum = 0.0f;
+    float s[2][32];
+    tmem_load32(r.s_at, s[0]);
+#pragma unroll
+    for (int c = 0; c < kPromptKeys / 32; ++c) {
+        float(&x)[32] = s[c & 1];
+        tmem_wait_load(x);
+        if (c + 1 < kPromptKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 sc = r.scales[2 * c + h];
+            const float by = r.row_scale * sc.x, off = sc.y + shift;
+            const uint64_t by2 = pair(by, by), off2 = pair(off, off);
+            uint64_t total[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float2 t = unpair(fma2(pair(x[16 * h + 2 * e], x[16 * h + 2 * e + 1]), by2, off2));
+                if (kGuard) {
+                    const int j = 32 * c + 16 * h + 2 * e;
+                    if (!sees<kGuard>(r, j)) t.x = -INFINITY;
+                    if (!sees<kGuard>(r, j + 1)) t.y = -INFINITY;
+                }
+                t.x = exp2_fast(t.x);
+                t.y = exp2_fast(t.y);
+                total[e & 1] = add2(total[e & 1], pair(t.x, t.y));
+                p[8 * h + e] = f16x2(t.x, t.y);
+            }
+            const float2 two = unpair(add2(total[0], total[1]));
+            sum = fmaf(two.x + two.y, sc.z, sum);
+        }
+        tmem_store16(r.s_at + 16 * c, p);
+    }
+    return sum;
+}
+
 // The block's barriers, each completed once per use.
 struct Barriers {
     uint64_t q_full;       // q tiles of a segment written
     uint64_t k_full[2], k_empty[2];
-    uint64_t v_full[2], v_empty[2];  // and the page scales
+    uint64_t v_full, v_empty;
+    uint64_t raw_full[2], raw_empty[2];  // E4M3 bytes of K (and the page scales), of V
     uint64_t s_full[2];    // tile w: scores of a key tile; after the last key tile, O
     uint64_t p_full[2];    // tile w: P written
 };
@@ -215,10 +300,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ int work;
     __shared__ volatile int abort;
     __shared__ int nan_tile[2];  // per buffer: the last key tile in which a NaN was found
+    __shared__ unsigned paged[4];  // of 4 key tiles in turn: which groups of keys have a page
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_addr(shared);
-    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps;
+    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps, kCopyWarp = kIssueWarp + 1;
     Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -230,13 +316,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (tid == 32) {
         mbar_init(smem_addr(&bars.q_full), kSoftmaxWarps * 32);
+        mbar_init(smem_addr(&bars.v_full), kConvertWarps * 32);
+        mbar_init(smem_addr(&bars.v_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.k_full[i]), kConvertWarps * 32);
-            mbar_init(smem_addr(&bars.v_full[i]), kConvertWarps * 32);
             mbar_init(smem_addr(&bars.k_empty[i]), 1);
-            mbar_init(smem_addr(&bars.v_empty[i]), 1);
             mbar_init(smem_addr(&bars.s_full[i]), 1);
             mbar_init(smem_addr(&bars.p_full[i]), 128);
+            mbar_init(smem_addr(&bars.raw_full[i]), 1);
+            mbar_init(smem_addr(&bars.raw_empty[i]), kConvertWarps);
             nan_tile[i] = -1;
         }
         abort = 0;
@@ -354,33 +442,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const int buf = at & 1;
                     const int j0 = tile_start(g.x0 + i);
                     const bool guard = masked(j0);
-                    ok = wait(bars.v_full[buf], at >> 1) && wait(bars.s_full[w], s_uses + i);
+                    ok = wait(bars.k_full[buf], at >> 1) && wait(bars.s_full[w], s_uses + i);
                     if (!ok) break;
                     tmem_fence_after();
-                    const float4* const scales =
-                        reinterpret_cast<const float4*>(shared + S::kScalesAt) + buf * kGroups;
-                    auto seen = [&](int j) { return j < hi && (j >= lo || j < a.sinks); };
-                    // the tile's largest t
-                    float most = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kPromptKeys / 32; ++c) {
-                        float s[32];
-                        tmem_load32(s_at + 32 * c, s);
-                        tmem_wait_load(s);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (guard) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (!seen(j0 + 32 * c + 16 * h + e)) s[16 * h + e] = -INFINITY;
-                            }
-                            float m = s[16 * h];
-#pragma unroll
-                            for (int e = 1; e < 16; ++e) m = fmaxf(m, s[16 * h + e]);
-                            const float4 sc = scales[2 * c + h];
-                            most = fmaxf(most, fmaf(m, row_scale * sc.x, sc.y));
-                        }
-                    }
+                    const ScoreRow scores{
+                        s_at, row_scale,
+                        reinterpret_cast<const float4*>(shared + S::kScalesAt) + (at & 3) * kGroups,
+                        hi - j0, lo - j0, a.sinks - j0};
+                    const float most = guard ? largest<true>(scores) : largest<false>(scores);
                     if (__any_sync(0xffffffffu, most > top + kSlack)) {
                         const float now = fmaxf(most, top);
                         const float keep = now == -INFINITY ? 1.0f : exp2_fast(top - now);
@@ -400,42 +469,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         }
                     }
                     const float shift = kPromptBias - (top == -INFINITY ? 0.0f : top);
-#pragma unroll
-                    for (int c = 0; c < kPromptKeys / 32; ++c) {
-                        float s[32];
-                        tmem_load32(s_at + 32 * c, s);
-                        tmem_wait_load(s);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float4 sc = scales[2 * c + h];
-                            const float by = row_scale * sc.x, off = sc.y + shift;
-                            const uint64_t by2 = pair(by, by), off2 = pair(off, off);
-                            uint64_t total = pair(0.0f, 0.0f);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float2 t = unpair(fma2(
-                                    pair(s[16 * h + 2 * e], s[16 * h + 2 * e + 1]), by2, off2));
-                                if (guard) {
-                                    const int j = j0 + 32 * c + 16 * h + 2 * e;
-                                    if (!seen(j)) t.x = -INFINITY;
-                                    if (!seen(j + 1)) t.y = -INFINITY;
-                                }
-                                t.x = exp2_fast(t.x);
-                                t.y = exp2_fast(t.y);
-                                total = add2(total, pair(t.x, t.y));
-                                p[8 * h + e] = f16x2(t.x, t.y);
-                            }
-                            const float2 two = unpair(total);
-                            sum = fmaf(two.x + two.y, sc.z, sum);
-                        }
-                        tmem_store16(s_at + 16 * c, p);
-                    }
+                    sum += guard ? weights<true>(scores, shift) : weights<false>(scores, shift);
+                    if (guard) ok = wait(bars.v_full, at);
                     if (guard && nan_tile[buf] == (int)at) {
                         const uint32_t* const bits = reinterpret_cast<const uint32_t*>(
                             shared + S::kNansAt + buf * kPromptKeys * kDim / 8);
                         for (int j = 0; j < kPromptKeys; ++j)
-                            if (seen(j0 + j)) {
+                            if (sees<true>(scores, j)) {
 #pragma unroll
                                 for (int k = 0; k < kDim / 32; ++k) nans[k] |= bits[j * kDim / 32 + k];
                             }
@@ -493,42 +533,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
         } else if (warp < kIssueWarp) {
-            // ---- pages to f16 tiles: a lane has 16 values of one key at a time
+            // ---- E4M3 bytes to f16 tiles: a lane has 16 values of one key at a time
             const int t = warp - kSoftmaxWarps, q = lane >> 2;
             constexpr int kItems = kDim / 16;
-            // lanes 0..3 and 4..7 write pieces of an even and an odd row, which the
-            // swizzle puts on different banks
-            const int piece = kDim == 128 ? (lane & 3) + 4 * (t >> 1) : lane & 3;
+            // neighbouring rows read and write different halves of a line: no two of
+            // 8 lanes meet on a bank, neither in the bytes nor in the swizzled tile
+            const int piece = kDim == 128 ? (lane & 3) + 4 * ((q & 1) ^ (t >> 1)) : lane & 3;
             const int row0 = kDim == 128 ? 8 * (t & 1) + q : 8 * t + q;
             constexpr int kRowStep = kDim == 128 ? 16 : 32;
-            const int page_mask = (1 << a.bt.page_shift) - 1;
-            uint4 k[kItems], v[kItems];
-            // lane l < 8: the table's entry for keys 16 l .. of tile x, -2 without keys
-            auto find_pages = [&](int x) {
-                const int j = tile_start(x) + 16 * lane;
-                int e = -2;
-                if (lane < kGroups && x < g.x1 && j < keys.hi)
-                    e = a.bt.page_table[(size_t)g.b * a.bt.table_width + (j >> a.bt.page_shift)];
-                return e;
-            };
-            auto load = [&](uint4 (&to)[kItems], const uint8_t* codes, int entries, int x) {
-                const int j0 = tile_start(x);
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const int row = row0 + i * kRowStep, j = j0 + row;
-                    const int e = __shfl_sync(0xffffffffu, entries, row >> 4);
-                    const bool live = x < g.x1 && e >= 0 && e < a.c.pages && j < keys.hi &&
-                                      (j >= keys.lo || j < a.sinks);
-                    to[i] = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        to[i] = __ldg(reinterpret_cast<const uint4*>(
-                            codes +
-                            ((((size_t)e * a.c.kv_heads + g.head) << a.bt.page_shift) +
-                             (j & page_mask)) *
-                                kDim +
-                            piece * 16));
-                }
-            };
+            const uint32_t raw = smem + S::kRawAt + row0 * kDim + piece * 16;
             auto store = [&](const uint4& x, uint32_t tile, int row) {
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                 uint32_t h[8];
@@ -544,62 +557,61 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 *reinterpret_cast<uint4*>(to + (((c + 1) ^ row) & 7) * 16) =
                     make_uint4(h[4], h[5], h[6], h[7]);
             };
-            // the scales of keys 16 l .. in lane l of the first of these warps
-            auto load_scales = [&](int entry) {
-                float2 s = make_float2(0.0f, 0.0f);  // no page: every key is masked
-                if (t == 0 && entry != -2) {
-                    if (entry >= 0 && entry < a.c.pages) {
-                        const size_t i = (size_t)entry * a.c.kv_heads + g.head;
-                        s = make_float2(a.c.k_scales[i], fmaxf(a.c.v_scales[i], 1.17549435e-38f));
-                    } else {
-                        kv8_report(a.bt);
-                    }
-                }
-                return s;
-            };
-            int entries = find_pages(g.x0);
-            float2 page_scales = load_scales(entries);
-            load(k, a.c.k_codes, entries, g.x0);
-            load(v, a.c.v_codes, entries, g.x0);
             bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
                 const unsigned at = done + i;
                 const int buf = at & 1;
-                const int x = g.x0 + i;
-                const int next = find_pages(x + 1);
-                // k_empty and v_empty complete once per use of the buffer
-                if (at >= 2) ok = wait(bars.k_empty[buf], (at >> 1) - 1);
+                const int j0 = tile_start(g.x0 + i);
+                const bool guard = masked(j0);
+                ok = wait(bars.raw_full[0], at);
+                // the barriers of empty buffers complete once per use
+                if (ok && at >= 2) ok = wait(bars.k_empty[buf], (at >> 1) - 1);
                 if (!ok) break;
+                const unsigned pages = paged[at & 3];
+                const bool partly = pages != (1u << kGroups) - 1 || j0 + kPromptKeys > keys.hi ||
+                                    (j0 < keys.lo && j0 + kPromptKeys > a.sinks);
+                // all of a tile's bytes first: their latency is paid once
+                uint4 x[kItems];
+                auto read = [&](int which) {
+#pragma unroll
+                    for (int m = 0; m < kItems; ++m)
+                        x[m] = lds128(raw + which * S::kRawBytes + m * kRowStep * kDim);
+                    if (!partly) return;
+                    // keys that no row sees, and those without a page, become zeros
+#pragma unroll
+                    for (int m = 0; m < kItems; ++m) {
+                        const int row = row0 + m * kRowStep, j = j0 + row;
+                        if (!(pages >> (row >> 4) & 1) || j >= keys.hi ||
+                            (j < keys.lo && j >= a.sinks))
+                            x[m] = make_uint4(0, 0, 0, 0);
+                    }
+                };
+                read(0);
 #pragma unroll
                 for (int m = 0; m < kItems; ++m)
-                    store(k[m], S::kKAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                    store(x[m], S::kKAt + buf * S::kTileBytes, row0 + m * kRowStep);
                 fence_shared_to_async();
                 mbar_arrive(smem_addr(&bars.k_full[buf]));
-                const float2 next_scales = load_scales(next);
-                load(k, a.c.k_codes, next, x + 1);
-                if (at >= 2) ok = wait(bars.v_empty[buf], (at >> 1) - 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[0]));
+                ok = wait(bars.raw_full[1], at);
                 if (!ok) break;
-                if (t == 0 && lane < kGroups) {
-                    const float vs = page_scales.y;
-                    const float4 sc =
-                        vs > 0.0f ? make_float4(page_scales.x, __log2f(vs), __fdividef(1.0f, vs), 0.0f)
-                                  : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
-                    reinterpret_cast<float4*>(shared + S::kScalesAt)[buf * kGroups + lane] = sc;
-                }
-                if (masked(tile_start(x))) {
+                read(1);
+                if (at >= 1) ok = wait(bars.v_empty, at - 1);
+                if (!ok) break;
+                if (guard) {
                     // NaNs out of the product, and where they were
                     uint32_t any = 0;
 #pragma unroll
                     for (int m = 0; m < kItems; ++m) {
-                        uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-                        uint32_t bits = 0;
+                        uint32_t u[4] = {x[m].x, x[m].y, x[m].z, x[m].w}, bits = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t bad = nan_bytes(u[e]) >> 7;
                             u[e] &= ~(bad * 0xffu);
                             bits |= ((bad * 0x00204081u) >> 21 & 0xfu) << (4 * e);
                         }
-                        v[m] = make_uint4(u[0], u[1], u[2], u[3]);
+                        x[m] = make_uint4(u[0], u[1], u[2], u[3]);
                         any |= bits;
                         reinterpret_cast<uint16_t*>(
                             shared + S::kNansAt +
@@ -609,14 +621,72 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (any) nan_tile[buf] = (int)at;
                 }
 #pragma unroll
-                for (int m = 0; m < kItems; ++m)
-                    store(v[m], S::kVAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                for (int m = 0; m < kItems; ++m) store(x[m], S::kVAt, row0 + m * kRowStep);
                 fence_shared_to_async();
-                mbar_arrive(smem_addr(&bars.v_full[buf]));
-                load(v, a.c.v_codes, next, x + 1);
-                page_scales = next_scales;
+                mbar_arrive(smem_addr(&bars.v_full));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[1]));
             }
-        } else if (lane == 0) {
+        } else if (warp == kCopyWarp) {
+            // ---- pages into shared memory as they are: a group of 16 keys is one
+            // piece of a page, copied by lane l < 8
+            const int page_mask = (1 << a.bt.page_shift) - 1;
+            // the table's entry for the lane's keys of tile x, -2 without keys
+            auto find_page = [&](int x) {
+                const int j = tile_start(x) + 16 * lane;
+                if (lane >= kGroups || x >= g.x1 || j >= keys.hi) return -2;
+                return a.bt.page_table[(size_t)g.b * a.bt.table_width + (j >> a.bt.page_shift)];
+            };
+            auto exists = [&](int page) { return page >= 0 && page < a.c.pages; };
+            auto scale_of = [&](const float* scales, int page) {
+                return exists(page) ? scales[(size_t)page * a.c.kv_heads + g.head] : 0.0f;
+            };
+            int page = find_page(g.x0), next = find_page(g.x0 + 1);
+            float ks = scale_of(a.c.k_scales, page), vs = scale_of(a.c.v_scales, page);
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const unsigned at = done + i;
+                const int x = g.x0 + i;
+                const bool have = exists(page);
+                if (!have && page != -2) kv8_report(a.bt);
+                const unsigned groups = __ballot_sync(0xffffffffu, have);
+                const uint32_t bytes = __popc(groups) * 16 * kDim;
+                const int j = tile_start(x) + 16 * lane;
+                const size_t from =
+                    ((((size_t)(have ? page : 0) * a.c.kv_heads + g.head) << a.bt.page_shift) +
+                     (j & page_mask)) *
+                    kDim;
+                const int after = find_page(x + 2);
+                const float ks1 = scale_of(a.c.k_scales, next), vs1 = scale_of(a.c.v_scales, next);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    if (ok && at >= 1) ok = wait(bars.raw_empty[which], at - 1);
+                    if (!ok) break;
+                    if (which == 0) {
+                        if (lane < kGroups) {
+                            const float v = fmaxf(vs, 1.17549435e-38f);
+                            reinterpret_cast<float4*>(shared +
+                                                      S::kScalesAt)[(at & 3) * kGroups + lane] =
+                                have ? make_float4(ks, __log2f(v), __fdividef(1.0f, v), 0.0f)
+                                     : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                        }
+                        if (lane == 0) paged[at & 3] = groups;
+                        __syncwarp();
+                    }
+                    const uint32_t bar = smem_addr(&bars.raw_full[which]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (have)
+                        bulk_copy_g2s(smem + S::kRawAt + which * S::kRawBytes + lane * 16 * kDim,
+                                      (which ? a.c.v_codes : a.c.k_codes) + from, 16 * kDim, bar);
+                }
+                page = next;
+                next = after;
+                ks = ks1;
+                vs = vs1;
+            }
+            if (!ok) __nanosleep(100000);  // copies under way end before their memory is left
+        } else if (warp == kIssueWarp && lane == 0) {
             // ---- the products
             const uint64_t q_op = operand(smem + S::kQAt, 16);
             const uint64_t k_op = operand(smem + S::kKAt, 16);
@@ -643,26 +713,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const unsigned at = done + i;
                 const int buf = at & 1;
                 const bool more = i + 1 < n;
-                ok = wait_lane(bars.v_full[buf], at >> 1);
+                ok = wait_lane(bars.v_full, at);
                 for (int w = 0; w < tiles && ok; ++w) {
                     ok = wait_lane(bars.p_full[w], (w ? p_done[1] : p_done[0]) + i);
-                    if (ok && more && w == 0) ok = wait_lane(bars.k_full[buf ^ 1], (at + 1) >> 1);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
                     for (int k = 0; k < kPromptKeys / 16; ++k)
                         mma_tmem(tmem + S::kO + w * kDim, tmem + w * 128 + 8 * k,
-                                 v_op + buf * kTileUnits + k * (2048 >> 4),
+                                 v_op + k * (2048 >> 4),
                                  instruction(kDim, true), i > 0 || k > 0);
+                    if (w == tiles - 1) mma_commit(smem_addr(&bars.v_empty));
+                    if (more && w == 0) {
+                        ok = wait_lane(bars.k_full[buf ^ 1], (at + 1) >> 1);
+                        if (!ok) break;
+                        tmem_fence_after();
+                    }
                     if (more)
                         scores(w, buf ^ 1);
                     else
                         mma_commit(smem_addr(&bars.s_full[w]));
                 }
-                if (ok) {
-                    mma_commit(smem_addr(&bars.v_empty[buf]));
-                    if (more) mma_commit(smem_addr(&bars.k_empty[buf ^ 1]));
-                }
+                if (ok && more) mma_commit(smem_addr(&bars.k_empty[buf ^ 1]));
             }
             if (!ok) {
                 // products under way end before the memory they use is given back
