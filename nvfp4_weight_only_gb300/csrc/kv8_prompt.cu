@@ -8,11 +8,11 @@
 //   S = q K^T      128 x 128, both operands in shared memory, f16 -> fp32 in TMEM
 //   P = 2^(t - m)  t = log2(e) s + log2(v_scale), one row per thread, f16 in TMEM
 //   O += P V       128 x head_dim, P from TMEM, V from shared memory
-// The two tiles alternate: while one's softmax runs, the tensor cores work on
-// the other's products.  8 warps do the softmax, one copies pages into shared
+// While the softmax of one row tile runs, the tensor cores work on the other's
+// products; P is handed on in halves, so that O begins under the second half.  8 warps do the softmax, one copies pages into shared
 // memory (the bulk-copy engine, 16 keys at a time), 4 turn their E4M3 bytes into
 // f16 tiles (exactly) in the 128-byte swizzle that the tensor cores read, one
-// thread issues the products.  TMEM holds S (then P in its place) and O of both
+// thread per row tile issues its products.  TMEM holds S (then P in its place) and O of both
 // tiles, all 512 columns.  K, V and q tiles are rows of 128 bytes (64 values),
 // 16-byte pieces XORed with the row; V is the transposed operand of the second
 // product, so both tiles are written alike.
@@ -35,9 +35,10 @@ namespace {
 
 constexpr int kPromptKeys = 128;
 constexpr int kPromptRows = 256;
+constexpr int kHalfKeys = 64;  // keys of one product and one softmax step
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
-constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
+constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 3) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
 // Least rows per sequence and kv head, on average, for these kernels.
 constexpr int kPromptLeastRows = 96;
@@ -59,9 +60,9 @@ struct PromptShape {
     static constexpr int kTileBytes = 128 * kDim * 2;  // of q, K or V
     static constexpr int kQAt = 0;
     static constexpr int kKAt = kQAt + 2 * kTileBytes;
-    static constexpr int kVAt = kKAt + 2 * kTileBytes;
+    static constexpr int kVAt = kKAt + kTileBytes;
     // E4M3 bytes of the next K and V tile, as they come
-    static constexpr int kRawAt = kVAt + kTileBytes;
+    static constexpr int kRawAt = kVAt + 2 * kTileBytes;
     static constexpr int kRawBytes = kPromptKeys * kDim;
     // for each of 4 key tiles in turn and group of 16 keys: k_scale,
     // log2(v_scale), 1 / v_scale (the copies are at most 3 tiles ahead of the
@@ -71,7 +72,9 @@ struct PromptShape {
     static constexpr int kNansAt = kScalesAt + 4 * kGroups * 16;
     static constexpr int kRowScaleAt = kNansAt + 2 * kPromptKeys * kDim / 8;
     static constexpr int kSeqsAt = kRowScaleAt + kPromptRows * 4;
-    static constexpr int kPartial = kPromptRows * (kDim + 2);  // fp32 words
+    // A partial state, in fp32 words: O as [kDim / 4][row][4] (neighbouring rows,
+    // a row per thread, side by side), maxima [row], sums [row].
+    static constexpr int kPartial = kPromptRows * (kDim + 2);
     // TMEM columns
     static constexpr int kO = 256;  // S of tile w at 128 w, O of tile w at kO + kDim w
 };
@@ -199,12 +202,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// One row of a tile of scores, from TMEM at s_at.
+// One row of half a tile of scores, from TMEM at s_at.
 struct ScoreRow {
     uint32_t s_at;
     float row_scale;
     const float4* scales;  // per 16 keys: k_scale, log2(v_scale), 1 / v_scale
-    int hi, lo, sinks;     // keys that the row sees, from the tile's first
+    int hi, lo, sinks;     // keys that the row sees, from the half's first
 };
 
 template <bool kGuard>
@@ -220,10 +223,10 @@ __device__ __forceinline__ float largest(const ScoreRow& r) {
     float s[2][32];
     tmem_load32(r.s_at, s[0]);
 #pragma unroll
-    for (int c = 0; c < kPromptKeys / 32; ++c) {
+    for (int c = 0; c < kHalfKeys / 32; ++c) {
         float(&x)[32] = s[c & 1];
         tmem_wait_load(x);
-        if (c + 1 < kPromptKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
+        if (c + 1 < kHalfKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -238,17 +241,18 @@ __device__ __forceinline__ float largest(const ScoreRow& r) {
     return most;
 }
 
-// P = 2^(t + shift) over the scores' place, as f16; returns sum P / v_scale.
+// P = 2^(t + shift), as f16 in the first columns of the scores' place (the
+// scores there have been used); returns sum P / v_scale.
 template <bool kGuard>
 __device__ __forceinline__ float weights(const ScoreRow& r, float shift) {
     float sum = 0.0f;
     float s[2][32];
     tmem_load32(r.s_at, s[0]);
 #pragma unroll
-    for (int c = 0; c < kPromptKeys / 32; ++c) {
+    for (int c = 0; c < kHalfKeys / 32; ++c) {
         float(&x)[32] = s[c & 1];
         tmem_wait_load(x);
-        if (c + 1 < kPromptKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
+        if (c + 1 < kHalfKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
         uint32_t p[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -280,11 +284,12 @@ __device__ __forceinline__ float weights(const ScoreRow& r, float shift) {
 // The block's barriers, each completed once per use.
 struct Barriers {
     uint64_t q_full;       // q tiles of a segment written
-    uint64_t k_full[2], k_empty[2];
-    uint64_t v_full, v_empty;
-    uint64_t raw_full[2], raw_empty[2];  // E4M3 bytes of K (and the page scales), of V
-    uint64_t s_full[2];    // tile w: scores of a key tile; after the last key tile, O
-    uint64_t p_full[2];    // tile w: P written
+    uint64_t k_full, k_empty;        // one K tile: its products run a tile ahead
+    uint64_t v_full[2], v_empty[2];  // two V tiles
+    uint64_t raw_full[2], raw_empty[2];  // E4M3 bytes of K, of V
+    uint64_t scales_full[4];             // page scales of 4 key tiles in turn
+    // row tile w, half h of a key tile: scores, P in their place, O with it added
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2];
 };
 
 template <int kDim, bool kFew>
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_addr(shared);
-    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps, kCopyWarp = kIssueWarp + 1;
+    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps, kCopyWarp = kIssueWarp + 2;
     Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -316,13 +321,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (tid == 32) {
         mbar_init(smem_addr(&bars.q_full), kSoftmaxWarps * 32);
-        mbar_init(smem_addr(&bars.v_full), kConvertWarps * 32);
-        mbar_init(smem_addr(&bars.v_empty), 1);
+        mbar_init(smem_addr(&bars.k_full), kConvertWarps * 32);
+        mbar_init(smem_addr(&bars.k_empty), 2);  // both row tiles' products
+        for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars.scales_full[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&bars.k_full[i]), kConvertWarps * 32);
-            mbar_init(smem_addr(&bars.k_empty[i]), 1);
-            mbar_init(smem_addr(&bars.s_full[i]), 1);
-            mbar_init(smem_addr(&bars.p_full[i]), 128);
+            mbar_init(smem_addr(&bars.v_full[i]), kConvertWarps * 32);
+            mbar_init(smem_addr(&bars.v_empty[i]), 2);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_addr(&bars.s_full[i][h]), 1);
+                mbar_init(smem_addr(&bars.p_full[i][h]), 128);
+                mbar_init(smem_addr(&bars.o_full[i][h]), 1);
+            }
             mbar_init(smem_addr(&bars.raw_full[i]), 1);
             mbar_init(smem_addr(&bars.raw_empty[i]), kConvertWarps);
             nan_tile[i] = -1;
@@ -356,9 +365,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         return __all_sync(0xffffffffu, wait_lane(bar, uses)) != 0;
     };
 
-    // of the segments before this one: key tiles, and the completions of the
-    // two row tiles' barriers (a unit may lack the second)
-    unsigned done = 0, s_done[2] = {0, 0}, p_done[2] = {0, 0};
+    // of the segments before this one: key tiles, and those of the two row tiles
+    // (a unit may lack the second)
+    unsigned done = 0, row_done[2] = {0, 0};
     for (int number = 0; work; ++number) {
         const Segment& g = segments[number % 3];
         const int n = g.x1 - g.x0;
@@ -382,18 +391,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             {
                 constexpr int kLanes = kDim / 8;  // lanes per row
                 const int sub = lane / kLanes, d = lane % kLanes;
-#pragma unroll 4
+                uint4 x[kLanes];
+#pragma unroll
                 for (int i = 0; i < kLanes; ++i) {
-                    const int row = warp * 32 + i * (32 / kLanes) + sub;
-                    const int unit_row = g.r * kPromptRows + row;
+                    const int unit_row =
+                        g.r * kPromptRows + warp * 32 + i * (32 / kLanes) + sub;
                     const int token = token_of(a, unit_row);
                     const bool live = token < g.len;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        x = reinterpret_cast<const uint4*>(
-                            a.q + (long long)(g.q0 + token) * a.q_stride +
-                            (size_t)(g.head * a.group + unit_row - token * a.group) * kDim)[d];
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                    const __nv_bfloat16* const from =
+                        a.q + (long long)(g.q0 + (live ? token : 0)) * a.q_stride +
+                        (size_t)(g.head * a.group + (live ? unit_row - token * a.group : 0)) * kDim;
+                    x[i] = reinterpret_cast<const uint4*>(from)[d];
+                }
+#pragma unroll
+                for (int i = 0; i < kLanes; ++i) {
+                    const int row = warp * 32 + i * (32 / kLanes) + sub;
+                    // rows beyond the last are zeros
+                    if (token_of(a, g.r * kPromptRows + row) >= g.len)
+                        x[i] = make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                     float big = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -436,27 +452,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 uint32_t nans[kDim / 32];
 #pragma unroll
                 for (int i = 0; i < kDim / 32; ++i) nans[i] = 0;
-                const unsigned s_uses = w ? s_done[1] : s_done[0];
-                for (int i = 0; i < n && ok; ++i) {
-                    const unsigned at = done + i;
+                const unsigned before = w ? row_done[1] : row_done[0];
+                for (int i = 0; i < 2 * n && ok; ++i) {
+                    const int h = i & 1;
+                    const unsigned at = done + (i >> 1);
                     const int buf = at & 1;
-                    const int j0 = tile_start(g.x0 + i);
+                    const int j0 = tile_start(g.x0 + (i >> 1));
                     const bool guard = masked(j0);
-                    ok = wait(bars.k_full[buf], at >> 1) && wait(bars.s_full[w], s_uses + i);
+                    ok = wait(bars.scales_full[at & 3], at >> 2) &&
+                         wait(bars.s_full[w][h], before + (i >> 1));
                     if (!ok) break;
                     tmem_fence_after();
-                    const ScoreRow scores{
-                        s_at, row_scale,
-                        reinterpret_cast<const float4*>(shared + S::kScalesAt) + (at & 3) * kGroups,
-                        hi - j0, lo - j0, a.sinks - j0};
+                    const int from = j0 + h * kHalfKeys;
+                    const ScoreRow scores{s_at + h * kHalfKeys, row_scale,
+                                          reinterpret_cast<const float4*>(shared + S::kScalesAt) +
+                                              (at & 3) * kGroups + h * (kGroups / 2),
+                                          hi - from, lo - from, a.sinks - from};
                     const float most = guard ? largest<true>(scores) : largest<false>(scores);
                     if (__any_sync(0xffffffffu, most > top + kSlack)) {
                         const float now = fmaxf(most, top);
                         const float keep = now == -INFINITY ? 1.0f : exp2_fast(top - now);
                         top = now;
                         sum *= keep;
-                        // the scores' completion follows that of the product before
-                        if (i > 0) {
+                        if (i > 0) {  // all of O so far: these scores came after all but one half
+                            ok = wait(bars.o_full[w][h ^ 1], before + ((i - 1) >> 1));
+                            if (!ok) break;
+                            tmem_fence_after();
 #pragma unroll
                             for (int c = 0; c < kDim / 32; ++c) {
                                 float v[32];
@@ -470,22 +491,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     const float shift = kPromptBias - (top == -INFINITY ? 0.0f : top);
                     sum += guard ? weights<true>(scores, shift) : weights<false>(scores, shift);
-                    if (guard) ok = wait(bars.v_full, at);
-                    if (guard && nan_tile[buf] == (int)at) {
-                        const uint32_t* const bits = reinterpret_cast<const uint32_t*>(
-                            shared + S::kNansAt + buf * kPromptKeys * kDim / 8);
-                        for (int j = 0; j < kPromptKeys; ++j)
-                            if (sees<true>(scores, j)) {
+                    if (guard) {
+                        ok = wait(bars.v_full[buf], at >> 1);
+                        if (!ok) break;
+                        if (nan_tile[buf] == (int)at) {
+                            const uint32_t* const bits = reinterpret_cast<const uint32_t*>(
+                                shared + S::kNansAt + buf * kPromptKeys * kDim / 8 +
+                                h * kHalfKeys * kDim / 8);
+                            for (int j = 0; j < kHalfKeys; ++j)
+                                if (sees<true>(scores, j)) {
 #pragma unroll
-                                for (int k = 0; k < kDim / 32; ++k) nans[k] |= bits[j * kDim / 32 + k];
-                            }
+                                    for (int k = 0; k < kDim / 32; ++k)
+                                        nans[k] |= bits[j * kDim / 32 + k];
+                                }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     tmem_wait_store();
                     tmem_fence_before();
-                    mbar_arrive(smem_addr(&bars.p_full[w]));
+                    mbar_arrive(smem_addr(&bars.p_full[w][h]));
                 }
-                if (ok && wait(bars.s_full[w], s_uses + n)) {
+                if (ok && wait(bars.o_full[w][0], before + n - 1) &&
+                    wait(bars.o_full[w][1], before + n - 1)) {
                     tmem_fence_after();
                     const bool live = token < g.len;
                     const bool whole = g.parts == 1;
@@ -513,11 +540,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                                    bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
                                                    bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
                         } else if (live) {
-                            float4* const to = reinterpret_cast<float4*>(
-                                part + (w * 128 + row) * kDim + 32 * c);
+                            float4* const to = reinterpret_cast<float4*>(part) +
+                                               8 * c * kPromptRows + w * 128 + row;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2],
+                                to[e * kPromptRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2],
                                                     v[4 * e + 3]);
                         }
                     }
@@ -565,7 +592,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const bool guard = masked(j0);
                 ok = wait(bars.raw_full[0], at);
                 // the barriers of empty buffers complete once per use
-                if (ok && at >= 2) ok = wait(bars.k_empty[buf], (at >> 1) - 1);
+                if (ok && at >= 1) ok = wait(bars.k_empty, at - 1);
                 if (!ok) break;
                 const unsigned pages = paged[at & 3];
                 const bool partly = pages != (1u << kGroups) - 1 || j0 + kPromptKeys > keys.hi ||
@@ -589,15 +616,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 read(0);
 #pragma unroll
                 for (int m = 0; m < kItems; ++m)
-                    store(x[m], S::kKAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                    store(x[m], S::kKAt, row0 + m * kRowStep);
                 fence_shared_to_async();
-                mbar_arrive(smem_addr(&bars.k_full[buf]));
+                mbar_arrive(smem_addr(&bars.k_full));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[0]));
                 ok = wait(bars.raw_full[1], at);
                 if (!ok) break;
                 read(1);
-                if (at >= 1) ok = wait(bars.v_empty, at - 1);
+                if (at >= 2) ok = wait(bars.v_empty[buf], (at >> 1) - 1);
                 if (!ok) break;
                 if (guard) {
                     // NaNs out of the product, and where they were
@@ -621,9 +648,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (any) nan_tile[buf] = (int)at;
                 }
 #pragma unroll
-                for (int m = 0; m < kItems; ++m) store(x[m], S::kVAt, row0 + m * kRowStep);
+                for (int m = 0; m < kItems; ++m) store(x[m], S::kVAt + buf * S::kTileBytes, row0 + m * kRowStep);
                 fence_shared_to_async();
-                mbar_arrive(smem_addr(&bars.v_full));
+                mbar_arrive(smem_addr(&bars.v_full[buf]));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[1]));
             }
@@ -672,6 +699,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         }
                         if (lane == 0) paged[at & 3] = groups;
                         __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&bars.scales_full[at & 3]));
                     }
                     const uint32_t bar = smem_addr(&bars.raw_full[which]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
@@ -686,55 +714,63 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 vs = vs1;
             }
             if (!ok) __nanosleep(100000);  // copies under way end before their memory is left
-        } else if (warp == kIssueWarp && lane == 0) {
-            // ---- the products
-            const uint64_t q_op = operand(smem + S::kQAt, 16);
+        } else if (lane == 0 && warp - kIssueWarp < tiles) {
+            // ---- the products of row tile w
+            const int w = warp - kIssueWarp;
+            const uint64_t q_op = operand(smem + S::kQAt + w * S::kTileBytes, 16);
             const uint64_t k_op = operand(smem + S::kKAt, 16);
             const uint64_t v_op = operand(smem + S::kVAt, 128 * 128);
             constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBlockUnits = 128 * 128 >> 4;
-            auto scores = [&](int w, int buf) {
+            constexpr uint32_t kHalfUnits = kHalfKeys * 128 >> 4;
+            const uint32_t s_at = tmem + w * 128, o_at = tmem + S::kO + w * kDim;
+            const unsigned before = w ? row_done[1] : row_done[0];
+            // A buffer is empty when both row tiles are done with it; a single one
+            // answers for both.
+            auto release = [&](uint64_t& bar) {
+                mma_commit(smem_addr(&bar));
+                if (tiles == 1) mma_commit(smem_addr(&bar));
+            };
+            auto scores = [&](int h) {
 #pragma unroll
                 for (int k = 0; k < kDim / 16; ++k) {
                     const uint32_t off = (k / 4) * kBlockUnits + (k % 4) * 2;
-                    mma_shared(tmem + w * 128, q_op + w * kTileUnits + off,
-                               k_op + buf * kTileUnits + off, instruction(kPromptKeys, false),
-                               k > 0);
+                    mma_shared(s_at + h * kHalfKeys, q_op + off, k_op + h * kHalfUnits + off,
+                               instruction(kHalfKeys, false), k > 0);
                 }
-                mma_commit(smem_addr(&bars.s_full[w]));
+                mma_commit(smem_addr(&bars.s_full[w][h]));
             };
-            bool ok =
-                wait_lane(bars.q_full, number) && wait_lane(bars.k_full[done & 1], done >> 1);
+            bool ok = wait_lane(bars.q_full, number) && wait_lane(bars.k_full, done);
             if (ok) {
                 tmem_fence_after();
-                for (int w = 0; w < tiles; ++w) scores(w, done & 1);
-                mma_commit(smem_addr(&bars.k_empty[done & 1]));
+                scores(0);
+                scores(1);
+                release(bars.k_empty);
             }
             for (int i = 0; i < n && ok; ++i) {
                 const unsigned at = done + i;
                 const int buf = at & 1;
-                const bool more = i + 1 < n;
-                ok = wait_lane(bars.v_full, at);
-                for (int w = 0; w < tiles && ok; ++w) {
-                    ok = wait_lane(bars.p_full[w], (w ? p_done[1] : p_done[0]) + i);
+                ok = wait_lane(bars.v_full[buf], at >> 1);
+                for (int h = 0; h < 2 && ok; ++h) {
+                    ok = wait_lane(bars.p_full[w][h], before + i);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kPromptKeys / 16; ++k)
-                        mma_tmem(tmem + S::kO + w * kDim, tmem + w * 128 + 8 * k,
-                                 v_op + k * (2048 >> 4),
-                                 instruction(kDim, true), i > 0 || k > 0);
-                    if (w == tiles - 1) mma_commit(smem_addr(&bars.v_empty));
-                    if (more && w == 0) {
-                        ok = wait_lane(bars.k_full[buf ^ 1], (at + 1) >> 1);
-                        if (!ok) break;
-                        tmem_fence_after();
-                    }
-                    if (more)
-                        scores(w, buf ^ 1);
-                    else
-                        mma_commit(smem_addr(&bars.s_full[w]));
+                    for (int k = 0; k < kHalfKeys / 16; ++k)
+                        mma_tmem(o_at, s_at + h * kHalfKeys + 8 * k,
+                                 v_op + buf * kTileUnits + h * kHalfUnits + k * (2048 >> 4),
+                                 instruction(kDim, true), i > 0 || h > 0 || k > 0);
+                    mma_commit(smem_addr(&bars.o_full[w][h]));
+                    if (h == 1) release(bars.v_empty[buf]);
+                    if (i + 1 == n) continue;
+                    // The next scores take the place of this P: products on different
+                    // sums are not ordered, so this one has to be complete.
+                    ok = (h == 1 || wait_lane(bars.k_full, at + 1)) &&
+                         wait_lane(bars.o_full[w][h], before + i);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    scores(h);
+                    if (h == 1) release(bars.k_empty);
                 }
-                if (ok && more) mma_commit(smem_addr(&bars.k_empty[buf ^ 1]));
             }
             if (!ok) {
                 // products under way end before the memory they use is given back
@@ -750,10 +786,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!last) scheduler.next();
         }
         done += n;
-        for (int w = 0; w < tiles; ++w) {
-            s_done[w] += n + 1;  // the last one is for O
-            p_done[w] += n;
-        }
+        row_done[0] += n;
+        if (tiles == 2) row_done[1] += n;
         tmem_fence_before();
         __syncthreads();
         tmem_fence_after();
@@ -765,41 +799,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                      : "memory");
 }
 
-// Joins the parts of the unit whose first part block blockIdx.x had, for 16 of
-// its rows.
+// Joins the parts of the unit whose first part block blockIdx.x had, for
+// kJoinValues of each row's values: a row per thread.
+constexpr int kJoinValues = 8;
+
 template <int kDim>
-__global__ void __launch_bounds__(128) kv8_prompt_join_kernel(const AttentionArgs a,
-                                                              const JoinNote* const notes) {
+__global__ void __launch_bounds__(kPromptRows) kv8_prompt_join_kernel(const AttentionArgs a,
+                                                                      const JoinNote* const notes) {
     using S = PromptShape<kDim>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const JoinNote g = notes[blockIdx.x];
-    if (g.parts < 2) return;
+    const int row = threadIdx.x, unit_row = g.r * kPromptRows + row;
+    if (g.parts < 2 || token_of(a, unit_row) >= g.len) return;
     auto part = [&](int i) {
         return a.partials + (size_t)(i == 0 ? g.slot0 : g.slot1 + 2 * (i - 1)) * S::kPartial;
     };
-    for (int item = threadIdx.x; item < 16 * kDim / 4; item += 128) {
-        const int row = blockIdx.y * 16 + item / (kDim / 4), d = item % (kDim / 4) * 4;
-        const int unit_row = g.r * kPromptRows + row;
-        if (token_of(a, unit_row) >= g.len) continue;
-        float top = -INFINITY;
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < g.parts; ++i) top = fmaxf(top, part(i)[kPromptRows * kDim + row]);
+    constexpr int kVectors = kJoinValues / 4;
+    float sum = 0.0f;
+    float4 v[kVectors];
+#pragma unroll
+    for (int k = 0; k < kVectors; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int i = 0; i < g.parts; ++i) top = fmaxf(top, part(i)[kPromptRows * kDim + row]);
-        float sum = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = 0; i < g.parts; ++i) {
-            const float* p = part(i);
-            const float4 y = *reinterpret_cast<const float4*>(p + row * kDim + d);
-            const float f = weight_of(p[kPromptRows * kDim + row], top);
-            sum = fmaf(p[kPromptRows * (kDim + 1) + row], f, sum);
-            v.x = fmaf(y.x, f, v.x);
-            v.y = fmaf(y.y, f, v.y);
-            v.z = fmaf(y.z, f, v.z);
-            v.w = fmaf(y.w, f, v.w);
+    for (int i = 0; i < g.parts; ++i) {
+        const float* p = part(i);
+        const float f = weight_of(p[kPromptRows * kDim + row], top);
+        sum = fmaf(p[kPromptRows * (kDim + 1) + row], f, sum);
+#pragma unroll
+        for (int k = 0; k < kVectors; ++k) {
+            const float4 y = reinterpret_cast<const float4*>(
+                p)[(blockIdx.y * kVectors + k) * kPromptRows + row];
+            v[k].x = fmaf(y.x, f, v[k].x);
+            v[k].y = fmaf(y.y, f, v[k].y);
+            v[k].z = fmaf(y.z, f, v[k].z);
+            v[k].w = fmaf(y.w, f, v[k].w);
         }
-        store_row<kDim>(a, g.q0, g.len, g.head, unit_row, d, v, top - kPromptBias, sum);
     }
+#pragma unroll
+    for (int k = 0; k < kVectors; ++k)
+        store_row<kDim>(a, g.q0, g.len, g.head, unit_row, (blockIdx.y * kVectors + k) * 4, v[k],
+                        top - kPromptBias, sum);
 }
 
 template <int kDim, bool kFew>
@@ -829,8 +871,8 @@ cudaError_t launch(const AttentionArgs& a, JoinNote* notes, int* status, int num
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<kDim, kFew>, a, notes, status);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(num_sms, kPromptRows / 16);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(num_sms, kDim / kJoinValues);
+    cfg.blockDim = dim3(kPromptRows);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv8_prompt_join_kernel<kDim>, a, (const JoinNote*)notes);
 }
