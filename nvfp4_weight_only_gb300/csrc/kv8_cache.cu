@@ -2,8 +2,8 @@
 // new tokens as they are written, the same tokens read back, and the table of
 // rotations (a load-time call).
 //
-// Write.  A run is one page's share of one sequence's new tokens; one block
-// takes one run of one head of k or v, so a page's scale has one writer and
+// Write.  A run is one page's share of one sequence's new tokens; one warp or
+// block takes one run of one head of k or v, so a page's scale has one writer and
 // nothing is atomic.  For the run's values x (k rotated in fp32, not rounded
 // in between):
 //   need   = the smallest 2^e with max |x| <= 448 * 2^e, e in -60..119
@@ -20,7 +20,9 @@ namespace nvf {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = 8;
+constexpr int kAppendThreads = kAppendWarps * 32;
+constexpr int kWideRows = 16;  // new tokens per sequence from which a run takes a block
 
 struct AppendArgs {
     Kv8CacheArgs c;
@@ -32,67 +34,98 @@ struct AppendArgs {
     __nv_bfloat16* q_out;
     long long k_stride, v_stride, q_stride;
     int heads, runs;
-    int q_blocks;  // blocks of the rotation of q, after those of the cache
+    int cache_blocks;  // blocks of the cache's part; the rest rotates q
 };
 
-// The two vectors of 8 values that slot `slot` of a head stands for: in the
-// half layout a rotated slot pairs vector `slot` with the one rot/2 values
-// later; otherwise slots are 16 consecutive values.
-__device__ __forceinline__ void slot_vectors(const RopeArgs& r, int slot, int& va, int& vb) {
-    if (!r.interleaved && slot < r.rot / 16) {
-        va = slot;
-        vb = slot + r.rot / 16;
-    } else {
-        va = 2 * slot;
-        vb = va + 1;
+// A slot is 16 values of a head, as two vectors of 8.  In the half layout a
+// rotated slot pairs vector `slot` with the one rot/2 values later; other
+// vectors are paired with those half of them further, so that neighbouring
+// slots' vectors lie side by side in memory.  A head has dim / 16 slots, which
+// divides a warp: a lane keeps one slot, and its rotations serve every head of a
+// token.
+struct Slot {
+    int a, b;            // vectors
+    bool turn_a, turn_b;  // whether they are rotated (together in the half layout)
+};
+
+__device__ __forceinline__ Slot slot_of(const RopeArgs& r, int slot, int slots) {
+    if (r.interleaved) return Slot{slot, slot + slots, slot < r.rot / 8, slot + slots < r.rot / 8};
+    const int turned = r.rot / 16;
+    if (slot < turned) return Slot{slot, slot + turned, true, true};
+    return Slot{slot + turned, slot + slots, false, false};
+}
+
+// (cos, sin) of a slot's 8 pairs at one position (those of vectors that turn).
+struct Turn {
+    float cs[16];
+};
+
+__device__ __forceinline__ Turn load_turn(const RopeArgs& r, int position, const Slot& s) {
+    Turn t;
+    const float4* const p =
+        reinterpret_cast<const float4*>(r.table + (size_t)position * r.rot);
+    // the half layout's pair i is value i of both vectors; interleaved vectors
+    // have 4 pairs of their own
+    const int at[2] = {r.interleaved ? 2 * s.a : 4 * s.a, r.interleaved ? 2 * s.b : 4 * s.a + 2};
+    const bool turns[2] = {s.turn_a, s.turn_b};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (turns[h]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 w = p[at[h] + i];
+                t.cs[8 * h + 4 * i] = w.x;
+                t.cs[8 * h + 4 * i + 1] = w.y;
+                t.cs[8 * h + 4 * i + 2] = w.z;
+                t.cs[8 * h + 4 * i + 3] = w.w;
+            }
+        }
+    return t;
+}
+
+// The slot's raw values.
+struct Raw {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const __nv_bfloat16* head, const Slot& s) {
+    return Raw{reinterpret_cast<const uint4*>(head)[s.a], reinterpret_cast<const uint4*>(head)[s.b]};
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(p[i]);
+        v[2 * i + 1] = bf16_hi(p[i]);
     }
 }
 
-// The 16 values of one slot of one head at one position, rotated.
-__device__ __forceinline__ void load_slot(const RopeArgs& r, const __nv_bfloat16* head,
-                                          int position, int slot, float (&a)[8], float (&b)[8]) {
-    int va, vb;
-    slot_vectors(r, slot, va, vb);
-    const uint4 wa = reinterpret_cast<const uint4*>(head)[va];
-    const uint4 wb = reinterpret_cast<const uint4*>(head)[vb];
-    const uint32_t pa[4] = {wa.x, wa.y, wa.z, wa.w}, pb[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[2 * i] = bf16_lo(pa[i]);
-        a[2 * i + 1] = bf16_hi(pa[i]);
-        b[2 * i] = bf16_lo(pb[i]);
-        b[2 * i + 1] = bf16_hi(pb[i]);
-    }
-    if (slot >= r.rot / 16) return;
-    // (cos, sin) of the slot's 8 pairs
-    const float4* t = reinterpret_cast<const float4*>(r.table + (size_t)position * r.rot) +
-                      4 * slot;
-    float cs[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 w = t[i];
-        cs[4 * i] = w.x;
-        cs[4 * i + 1] = w.y;
-        cs[4 * i + 2] = w.z;
-        cs[4 * i + 3] = w.w;
-    }
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+    const float u = x, w = y;
+    x = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
+    y = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
+}
+
+// The slot's values in fp32, rotated (two rounded products and their rounded
+// sum; values that do not turn pass unchanged, signs of zeros included).
+__device__ __forceinline__ void values(const RopeArgs& r, const Raw& raw, const Slot& s,
+                                       const Turn& t, float (&a)[8], float (&b)[8]) {
+    unpack8(raw.a, a);
+    unpack8(raw.b, b);
     if (!r.interleaved) {
+        if (s.turn_a)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i], c = cs[2 * i], s = cs[2 * i + 1];
-            a[i] = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-            b[i] = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-        }
+            for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], t.cs[2 * i], t.cs[2 * i + 1]);
     } else {
+        if (s.turn_a)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = a[2 * i], y = a[2 * i + 1], c = cs[2 * i], s = cs[2 * i + 1];
-            a[2 * i] = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-            a[2 * i + 1] = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-            const float z = b[2 * i], w = b[2 * i + 1], d = cs[8 + 2 * i], e = cs[8 + 2 * i + 1];
-            b[2 * i] = __fsub_rn(__fmul_rn(z, d), __fmul_rn(w, e));
-            b[2 * i + 1] = __fadd_rn(__fmul_rn(w, d), __fmul_rn(z, e));
-        }
+            for (int i = 0; i < 4; ++i)
+                turn_pair(a[2 * i], a[2 * i + 1], t.cs[2 * i], t.cs[2 * i + 1]);
+        if (s.turn_b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                turn_pair(b[2 * i], b[2 * i + 1], t.cs[8 + 2 * i], t.cs[9 + 2 * i]);
     }
 }
 
@@ -131,45 +164,119 @@ __device__ __forceinline__ int rope_position(const AppendArgs& a, int position) 
     return a.rope.positions - 1;
 }
 
-__device__ void append_run(const AppendArgs& a, int x, int head, bool is_v) {
-    Kv8Run r;
-    if (!kv8_find_run(a.bt, x, r)) return;
-    const int page = kv8_page(a.bt, a.c, r.b, r.page_index);
-    if (page < 0) return;
-    const int dim = a.c.head_dim, slots = dim / 16;
-    const int size = 1 << a.bt.page_shift;
+constexpr int kHeld = 2;  // items of a thread that stay in registers
+
+// A team's part of one head of a run: kTeam threads, each with one slot of
+// every (kTeam / slots)-th row.
+template <bool kTurn, int kTeam>
+struct RunPart {
+    RopeArgs rope;
+    const __nv_bfloat16* src;
+    long long stride;
+    int row0, step, slots;
+    Slot slot;
+    Raw held[kHeld];
+
+    // Starts the loads of the first items (all of a run of a page's worth when
+    // the team is a block).
+    __device__ __forceinline__ RunPart(const AppendArgs& a, const Kv8Run& r, int head)
+        : rope(a.rope), stride(kTurn ? a.k_stride : a.v_stride) {
+        const int mate = threadIdx.x % kTeam, dim = a.c.head_dim;
+        slots = dim / 16;
+        step = kTeam / slots;
+        row0 = mate / slots;
+        if (!kTurn) rope.rot = 0;
+        slot = slot_of(rope, mate % slots, slots);
+        src = (kTurn ? a.k : a.v) + r.token * stride + (size_t)head * dim;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int row = row0 + i * step;
+            held[i] = Raw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (row < r.rows) held[i] = load_raw(src + row * stride, slot);
+        }
+    }
+};
+
+// Quantises a run of one head into its page (`shared` joins the maxima of a
+// block's warps).  Items beyond the held ones are read twice, the second time
+// from the caches.
+template <bool kTurn, int kTeam>
+__device__ __forceinline__ void store_run(const AppendArgs& a, const Kv8Run& r, int page, int head,
+                                          const RunPart<kTurn, kTeam>& part, float* shared,
+                                          float4* kept) {
+    constexpr bool is_v = !kTurn;
+    const int mate = threadIdx.x % kTeam, dim = a.c.head_dim, slots = part.slots;
+    const int row0 = part.row0, step = part.step;
+    const Slot slot = part.slot;
+    const RopeArgs& rope = part.rope;
+    const long long stride = part.stride;
+    const __nv_bfloat16* const src = part.src;
+    const Raw(&held)[kHeld] = part.held;
     const size_t at = (size_t)page * a.c.kv_heads + head;
-    uint8_t* codes = (is_v ? a.c.v_codes : a.c.k_codes) + at * size * dim;
+    uint8_t* codes = (is_v ? a.c.v_codes : a.c.k_codes) + (at << a.bt.page_shift) * dim;
     float* scales = (is_v ? a.c.v_scales : a.c.k_scales) + at;
-    const long long stride = is_v ? a.v_stride : a.k_stride;
-    const __nv_bfloat16* src = (is_v ? a.v : a.k) + r.token * stride + (size_t)head * dim;
-    RopeArgs rope = a.rope;
-    if (is_v) rope.rot = 0;
-    const int items = r.rows * slots;
-    const int tid = threadIdx.x;
+    const float before = r.row > 0 ? *scales : 0.0f;
+    auto turned = [&](const Raw& raw, int row, float (&p)[8], float (&q)[8]) {
+        Turn t;
+        if (kTurn && (slot.turn_a || slot.turn_b))
+            t = load_turn(rope, rope_position(a, r.position + row), slot);
+        values(rope, raw, slot, t, p, q);
+    };
     float top = 0.0f;
-    for (int i = tid; i < items; i += kAppendThreads) {
-        const int row = i / slots, slot = i - row * slots;
-        float p[8], q[8];
-        load_slot(rope, src + row * stride, is_v ? 0 : rope_position(a, r.position + row), slot, p,
-                  q);
+    auto measure = [&](const float (&p)[8], const float (&q)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(p[e]), fabsf(q[e])));
+    };
+    // A block keeps rotated values in shared memory (registers are what it has too
+    // few of); a warp, which has few items, rotates again.
+    auto keep = [&](int i, float (&u)[8], float (&w)[8]) {
+        const float4 x[4] = {make_float4(u[0], u[1], u[2], u[3]), make_float4(u[4], u[5], u[6], u[7]),
+                             make_float4(w[0], w[1], w[2], w[3]), make_float4(w[4], w[5], w[6], w[7])};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kept[(4 * i + e) * kTeam + mate] = x[e];
+    };
+    auto again = [&](int i, int row, float (&u)[8], float (&w)[8]) {
+        if constexpr (kTurn && kTeam > 32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 x = kept[(4 * i + e) * kTeam + mate];
+                float* const to = e < 2 ? u + 4 * e : w + 4 * (e - 2);
+                to[0] = x.x;
+                to[1] = x.y;
+                to[2] = x.z;
+                to[3] = x.w;
+            }
+        } else {
+            turned(held[i], row, u, w);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (row0 + i * step < r.rows) {
+            float u[8], w[8];
+            turned(held[i], row0 + i * step, u, w);
+            measure(u, w);
+            if (kTurn && kTeam > 32) keep(i, u, w);
+        }
+#pragma unroll 1
+    for (int row = row0 + kHeld * step; row < r.rows; row += step) {
+        float u[8], w[8];
+        turned(load_raw(src + row * stride, slot), row, u, w);
+        measure(u, w);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    __shared__ float part[kAppendThreads / 32];
-    if ((tid & 31) == 0) part[tid >> 5] = top;
-    const float before = r.row > 0 ? *scales : 0.0f;
-    __syncthreads();
+    if constexpr (kTeam > 32) {
+        if ((mate & 31) == 0) shared[mate >> 5] = top;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, part[w]);
-    const float need = two_to(scale_exponent(top));
-    const float scale = fmaxf(before, need);
+        for (int w = 0; w < kTeam / 32; ++w) top = fmaxf(top, shared[w]);
+    }
+    const float scale = fmaxf(before, two_to(scale_exponent(top)));
     if (r.row > 0 && scale != before) {
         const float ratio = __fdiv_rn(before, scale);
         uint4* old = reinterpret_cast<uint4*>(codes);
-        for (int i = tid; i < r.row * slots; i += kAppendThreads) {
+        for (int i = mate; i < r.row * slots; i += kTeam) {
             uint4 w = old[i];
             w.x = rescale4(w.x, ratio);
             w.y = rescale4(w.y, ratio);
@@ -180,57 +287,110 @@ __device__ void append_run(const AppendArgs& a, int x, int head, bool is_v) {
     }
     // 1 / scale is exact for a power of two; a foreign scale takes one rounding
     const float inv = __fdiv_rn(1.0f, scale);
-    for (int i = tid; i < items; i += kAppendThreads) {
-        const int row = i / slots, slot = i - row * slots;
-        float p[8], q[8];
-        load_slot(rope, src + row * stride, is_v ? 0 : rope_position(a, r.position + row), slot, p,
-                  q);
-        int va, vb;
-        slot_vectors(rope, slot, va, vb);
+    auto write = [&](const float (&u)[8], const float (&w)[8], int row) {
         uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)(r.row + row) * dim);
-        dst[va] = quantise8(p, inv);
-        dst[vb] = quantise8(q, inv);
+        dst[slot.a] = quantise8(u, inv);
+        dst[slot.b] = quantise8(w, inv);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (row0 + i * step < r.rows) {
+            float u[8], w[8];
+            again(i, row0 + i * step, u, w);
+            write(u, w, row0 + i * step);
+        }
+#pragma unroll 1
+    for (int row = row0 + kHeld * step; row < r.rows; row += step) {
+        float u[8], w[8];
+        turned(load_raw(src + row * stride, slot), row, u, w);
+        write(u, w, row);
     }
-    if (tid == 0) *scales = scale;
+    if (mate == 0) *scales = scale;  // read by all before the maxima were joined
 }
 
-// Rotates q of one token per warp (or copies it without a table).
-__device__ void turn_q(const AppendArgs& a, int t) {
+// Rotates q of one token (or copies it without a table), by one warp.
+__device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
     const int b = kv8_owner(a.bt, t);
     int position = 0;
-    RopeArgs rope = a.rope;
     if (b < a.bt.batch) {
         const Kv8Seq s = kv8_seq(a.bt, b);
         position = s.kv - s.len + (t - s.q0);
-        if (s.bad && (threadIdx.x & 31) == 0) kv8_report(a.bt);
+        if (s.bad) kv8_report(a.bt);
     } else {
         kv8_report(a.bt);
     }
     position = rope_position(a, max(position, 0));
-    const int dim = a.c.head_dim, slots = dim / 16;
-    for (int i = threadIdx.x & 31; i < a.heads * slots; i += 32) {
-        const int head = i / slots, slot = i - head * slots;
+    const int dim = a.c.head_dim, slots = dim / 16, step = 32 / slots;
+    const Slot slot = slot_of(a.rope, lane % slots, slots);
+    Turn turn;
+    if (slot.turn_a || slot.turn_b) turn = load_turn(a.rope, position, slot);
+    const __nv_bfloat16* src = a.q + t * a.q_stride;
+    __nv_bfloat16* dst = a.q_out + (size_t)t * a.heads * dim;
+#pragma unroll 4
+    for (int head = lane / slots; head < a.heads; head += step) {
+        const Raw raw = load_raw(src + (size_t)head * dim, slot);
         float p[8], r[8];
-        load_slot(rope, a.q + t * a.q_stride + (size_t)head * dim, position, slot, p, r);
-        int va, vb;
-        slot_vectors(rope, slot, va, vb);
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out + ((size_t)t * a.heads + head) * dim);
-        dst[va] = pack8(p);
-        dst[vb] = pack8(r);
+        values(a.rope, raw, slot, turn, p, r);
+        uint4* to = reinterpret_cast<uint4*>(dst + (size_t)head * dim);
+        to[slot.a] = pack8(p);
+        to[slot.b] = pack8(r);
     }
 }
 
+// One token per sequence, or few: a warp per run and head of k or v (a block's
+// warps take neighbouring heads, which share the run's rotations in L1), then q,
+// a warp per token.
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
-    const int per_run = 2 * a.c.kv_heads;
-    const int cache_blocks = a.runs * per_run;
-    const int x = blockIdx.x;
-    if (x < cache_blocks) {
-        const int head = x % per_run;
-        append_run(a, x / per_run, head >> 1, head & 1);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((int)blockIdx.x < a.cache_blocks) {
+        const int per_run = 2 * a.c.kv_heads;
+        const int x = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+        const int run = x / per_run, part = x - run * per_run;
+        Kv8Run r;
+        if (run >= a.runs || !kv8_find_run(a.bt, run, r)) return;
+        const bool is_k = part < a.c.kv_heads;
+        const int head = is_k ? part : part - a.c.kv_heads;
+        if (is_k) {
+            const RunPart<true, 32> k(a, r, head);
+            const int page = kv8_page(a.bt, a.c, r.b, r.page_index);
+            if (page >= 0) store_run(a, r, page, head, k, nullptr, nullptr);
+        } else {
+            const RunPart<false, 32> v(a, r, head);
+            const int page = kv8_page(a.bt, a.c, r.b, r.page_index);
+            if (page >= 0) store_run(a, r, page, head, v, nullptr, nullptr);
+        }
     } else {
-        const int t = (x - cache_blocks) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+        const int t = (blockIdx.x - a.cache_blocks) * kAppendWarps + (threadIdx.x >> 5);
         if (t < a.bt.tokens) turn_q(a, t);
     }
+}
+
+// Prompts: a block per run and head, k and v, so that both are on their way
+// while the run and its page are looked up and k is worked on.
+__global__ void __launch_bounds__(kAppendThreads, 4) kv8_append_rows_kernel(const AppendArgs a) {
+    __shared__ float tops[2][kAppendWarps];
+    __shared__ float4 kept[kHeld * 4 * kAppendThreads];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int run = blockIdx.x / a.c.kv_heads, head = blockIdx.x - run * a.c.kv_heads;
+    Kv8Run r;
+    if (!kv8_find_run(a.bt, run, r)) return;
+    const RunPart<true, kAppendThreads> k(a, r, head);
+    const RunPart<false, kAppendThreads> v(a, r, head);
+    const int page = kv8_page(a.bt, a.c, r.b, r.page_index);
+    if (page < 0) return;
+    store_run(a, r, page, head, k, tops[0], kept);
+    store_run(a, r, page, head, v, tops[1], nullptr);
+}
+
+// q of many tokens by itself: it needs fewer registers than the cache's part.
+__global__ void __launch_bounds__(kAppendThreads, 4) kv8_turn_kernel(const AppendArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    if (t < a.bt.tokens) turn_q(a, t);
 }
 
 struct ReadArgs {
@@ -241,7 +401,12 @@ struct ReadArgs {
     int runs;
 };
 
-__global__ void __launch_bounds__(kAppendThreads) kv8_read_kernel(const ReadArgs a) {
+constexpr int kReadThreads = 128;
+
+// One run of one head of k or v per block.
+__global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int per_run = 2 * a.c.kv_heads;
     const int head = (blockIdx.x % per_run) >> 1;
     const bool is_v = blockIdx.x & 1;
@@ -255,7 +420,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_read_kernel(const ReadArgs
     const uint4* codes = reinterpret_cast<const uint4*>(
         (is_v ? a.c.v_codes : a.c.k_codes) + ((at << a.bt.page_shift) + r.row) * dim);
     __nv_bfloat16* out = is_v ? a.v_out : a.k_out;
-    for (int i = threadIdx.x; i < r.rows * slots; i += kAppendThreads) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < r.rows * slots; i += kReadThreads) {
         const int row = i / slots, slot = i - row * slots;
         const uint4 w = codes[i];
         const uint32_t p[4] = {w.x, w.y, w.z, w.w};
@@ -272,6 +438,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_read_kernel(const ReadArgs
         dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
         dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+}
+
+// A launch that may begin while the preceding kernel on the stream finishes;
+// the kernel waits for that one before it reads or writes anything.
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), unsigned blocks, int threads, cudaStream_t s,
+                         const Args& a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 struct TableArgs {
@@ -338,12 +521,18 @@ cudaError_t launch_kv8_append(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, con
     a.q_stride = q_stride;
     a.heads = heads;
     a.runs = (int)kv8_max_runs(bt.tokens, bt.batch, bt.page_shift);
-    const int per = kAppendThreads / 32;
-    const long long blocks = (long long)a.runs * 2 * c.kv_heads +
-                             (q ? ((long long)bt.tokens + per - 1) / per : 0);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kv8_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const long long runs = a.runs;
+    const long long q_blocks = q ? ((long long)bt.tokens + kAppendWarps - 1) / kAppendWarps : 0;
+    const long long cache_blocks = (runs * 2 * c.kv_heads + kAppendWarps - 1) / kAppendWarps;
+    if (runs * 2 * c.kv_heads + q_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    a.cache_blocks = (int)cache_blocks;
+    if (bt.tokens < kWideRows * bt.batch)
+        return launch_after(kv8_append_kernel, (unsigned)(cache_blocks + q_blocks), kAppendThreads,
+                            s, a);
+    const cudaError_t e = launch_after(kv8_append_rows_kernel, (unsigned)(runs * c.kv_heads),
+                                       kAppendThreads, s, a);
+    if (e != cudaSuccess || !q) return e;
+    return launch_after(kv8_turn_kernel, (unsigned)q_blocks, kAppendThreads, s, a);
 }
 
 cudaError_t launch_kv8_read(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, void* k_out,
@@ -356,8 +545,7 @@ cudaError_t launch_kv8_read(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, void*
     a.runs = (int)kv8_max_runs(bt.tokens, bt.batch, bt.page_shift);
     const long long blocks = (long long)a.runs * 2 * c.kv_heads;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kv8_read_kernel<<<(unsigned)blocks, kAppendThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(kv8_read_kernel, (unsigned)blocks, kReadThreads, s, a);
 }
 
 }  // namespace nvf

@@ -3,7 +3,8 @@
 //   y = r * (mean(r^2) + eps)^(-1/2) * (weight + weight_bias)
 // stored as bf16(y), or as E4M3 codes with one fp32 scale per row and 128
 // columns: scale = max(amax / 448, 2^-126) (1 for a group of zeros),
-// code = e4m3(y / scale), which saturates and keeps NaN.
+// code = e4m3(y / scale), which saturates and keeps NaN (the quotient is off by
+// at most 2^-22 of itself).
 //
 // One block per row; a thread holds its 8-column vectors of r in registers
 // between the sum of squares and the output, so x and the residual are read
@@ -46,6 +47,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // lanes hold one group of 128 columns.
 template <int kVecs>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const size_t row = blockIdx.x;
     const uint4* x = a.x + row * a.vecs;
@@ -102,9 +105,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float scale = top == 0.0f ? 1.0f : fmaxf(__fdiv_rn(top, 448.0f), 1.17549435e-38f);
         if (live) {
+            // y / scale through the reciprocal: off by at most 2^-22 of itself
+            const float by = __frcp_rn(scale);
             float q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(y[e], scale);
+            for (int e = 0; e < 8; ++e) q[e] = y[e] * by;
             a.codes[row * a.vecs + c] = make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
                                                    f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
             if ((c & 15) == 0) a.scales[row * a.groups + (c >> 4)] = scale;
@@ -134,13 +139,20 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
     if (per > 4) return cudaErrorInvalidValue;
     const int kv = per <= 1 ? 1 : per <= 2 ? 2 : 4;
     const int threads = ((a.vecs + kv - 1) / kv + 31) / 32 * 32;
-    if (kv == 1)
-        add_rmsnorm_kernel<1><<<M, threads, 0, s>>>(a);
-    else if (kv == 2)
-        add_rmsnorm_kernel<2><<<M, threads, 0, s>>>(a);
-    else
-        add_rmsnorm_kernel<4><<<M, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(M);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg,
+                              kv == 1   ? add_rmsnorm_kernel<1>
+                              : kv == 2 ? add_rmsnorm_kernel<2>
+                                        : add_rmsnorm_kernel<4>,
+                              a);
 }
 
 }  // namespace nvf
