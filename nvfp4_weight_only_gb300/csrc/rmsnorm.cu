@@ -43,6 +43,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                       bf16x2(v[6], v[7]));
 }
 
+constexpr int kManyRows = 512;
+
 // kVecs: vectors per thread.  The vectors of a warp are consecutive, so 16
 // lanes hold one group of 128 columns.
 template <int kVecs>
@@ -52,25 +54,33 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const size_t row = blockIdx.x;
     const uint4* x = a.x + row * a.vecs;
+    // everything the row needs is asked for at once
+    uint4 in[kVecs], more[kVecs], w[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int c = tid + i * blockDim.x;
+        in[i] = more[i] = w[i] = make_uint4(0, 0, 0, 0);
+        if (c < a.vecs) {
+            in[i] = x[c];
+            if (a.residual) more[i] = a.residual[row * a.vecs + c];
+            w[i] = a.weight[c];
+        }
+    }
     float r[kVecs][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int c = tid + i * blockDim.x;
+        unpack8(in[i], r[i]);
+        if (a.residual) {
+            float o[8];
+            unpack8(more[i], o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] = 0.0f;
-        if (c < a.vecs) {
-            unpack8(x[c], r[i]);
-            if (a.residual) {
-                float o[8];
-                unpack8(a.residual[row * a.vecs + c], o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r[i][e] += o[e];
-            }
-            if (a.sum_out) a.sum_out[row * a.vecs + c] = pack8(r[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
+            for (int e = 0; e < 8; ++e) r[i][e] += o[e];
         }
+        if (a.sum_out && c < a.vecs) a.sum_out[row * a.vecs + c] = pack8(r[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
@@ -86,14 +96,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
         const int c = tid + i * blockDim.x;
         const bool live = c < a.vecs;
         float y[8];
-        if (live) {
-            unpack8(a.weight[c], y);
+        unpack8(w[i], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = r[i][e] * inv * (y[e] + a.weight_bias);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        }
+        for (int e = 0; e < 8; ++e) y[e] = live ? r[i][e] * inv * (y[e] + a.weight_bias) : 0.0f;
         if (a.out) {
             if (live) a.out[row * a.vecs + c] = pack8(y);
             continue;
@@ -137,7 +142,10 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
     a.weight_bias = weight_bias;
     const int per = (a.vecs + 1023) / 1024;
     if (per > 4) return cudaErrorInvalidValue;
-    const int kv = per <= 1 ? 1 : per <= 2 ? 2 : 4;
+    // One vector per thread is the shortest chain for a few rows (1 x 5120: 1.8 us
+    // against 1.9 with two); many rows want small blocks, whose loads and stores
+    // overlap others' (4096 x 5376: two vectors 29.8 us, one 33.3, four 35.7).
+    const int kv = per <= 1 ? (M > kManyRows ? 2 : 1) : per <= 2 ? 2 : 4;
     const int threads = ((a.vecs + kv - 1) / kv + 31) / 32 * 32;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(M);
