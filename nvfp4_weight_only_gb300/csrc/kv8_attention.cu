@@ -56,7 +56,8 @@ struct Shape {
     // 16 warps per SM where the state leaves room for 128 registers: two blocks,
     // so that one's unit ends and begins under the other's products, or, when
     // few units are cut into many parts, one block, which halves the parts
-    static constexpr bool kNarrow = kNT == 1 && kDim <= 128;
+    static constexpr bool kNarrow = kNT * kDim <= 256 && kDim <= 128;
+    static constexpr bool kQInRegs = kNarrow ? kNT == 1 : kNT * kDim <= 256;  // else shared
     static constexpr int kBlocks = kNarrow && !kFew ? 2 : 1;
     static constexpr int kWarps = kNarrow && kFew ? 16 : 8;
     static constexpr int kThreads = kWarps * 32;
@@ -130,7 +131,7 @@ template <int kDim, int kNT, bool kFew>
 class Worker {
     using S = Shape<kDim, kNT, kFew>;
     static constexpr int kWarps = S::kWarps;
-    static constexpr bool kQInRegs = kNT < 4;
+    static constexpr bool kQInRegs = S::kQInRegs;
     static constexpr int kWords = kDim / 32;  // 32-bit words of a value row that a lane holds
 
 public:
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(Shape<kDim, kNT, kFew>::kThreads,
     // the first copies of a segment go to the stages behind the state of the one
     // before it, which may still be waiting to be joined
     constexpr int kEarly = S::kStages - kNT < S::kStages - 1 ? S::kStages - kNT : S::kStages - 1;
-    typename Worker<kDim, kNT, kFew>::QRow q[kNT < 4 ? kNT : 1];
+    typename Worker<kDim, kNT, kFew>::QRow q[S::kQInRegs ? kNT : 1];
     int ahead_pages = -2;  // of the next segment's first tiles
     auto look_ahead = [&](const Segment& g) {
         ahead_pages = w.page_of(g, g.x0 + w.warp + w.lane * kWarps);
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(Shape<kDim, kNT, kFew>::kThreads,
         const int mine = g.x0 + w.warp;
         w.pages = ahead_pages;
         w.pages_at = 0;
-        if constexpr (kNT < 4) {
+        if constexpr (S::kQInRegs) {
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) q[nt] = w.load_q(nt);
         }
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(Shape<kDim, kNT, kFew>::kThreads,
 #pragma unroll
         for (int i = kEarly; i < S::kStages - 1; ++i)
             w.issue(mine + i * kWarps, i, (kNT + i) % S::kStages);
-        if constexpr (kNT >= 4) {
+        if constexpr (!S::kQInRegs) {
             if (w.warp < kNT) w.stage_q(w.warp);
             __syncthreads();
         }
@@ -852,9 +853,10 @@ size_t kv8_attention_data_bytes(int head_dim, long long tokens, int group, int b
                                 int num_sms) {
     if (kv8_prompt_applies(head_dim, tokens, group, batch))
         return kv8_prompt_data_bytes(head_dim, num_sms);
-    // two partial states per block, of 32 rows (16 of 256 values); with two
-    // blocks per SM they have 8 rows
-    const size_t rows = head_dim == 256 ? 16 : 32;
+    // two partial states per block; the most rows that an SM's blocks hold: two
+    // blocks of 32 rows of 64 values, two of 16 or one of 32 rows of 128, one of 16
+    // of 256
+    const size_t rows = head_dim == 64 ? 64 : head_dim == 128 ? 32 : 16;
     return (size_t)num_sms * 2 * rows * (head_dim + 2) * sizeof(float);
 }
 

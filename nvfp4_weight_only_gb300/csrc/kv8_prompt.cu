@@ -40,8 +40,10 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
 constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 3) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
-// Least rows per sequence and kv head, on average, for these kernels.
-constexpr int kPromptLeastRows = 96;
+// Least rows per sequence and kv head, on average, for these kernels (8 sequences
+// of 8192 keys, 8 kv heads of 128: at 48 rows 96 us against 87 in three passes of
+// kv8_attention.cu, at 64 rows 95 against 94, at 128 rows 97 against 145).
+constexpr int kPromptLeastRows = 64;
 constexpr float kPromptBias = 6.0f;
 constexpr float kSlack = 8.0f;
 
