@@ -741,7 +741,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 mma_commit(smem_addr(&bars.s_full[w][h]));
             };
-            bool ok = wait_lane(bars.q_full, number) && wait_lane(bars.k_full, done);
+            // The second row tile begins half a step after the first, so that one's
+            // softmax fills the other's waits.
+            bool ok = wait_lane(bars.q_full, number) && wait_lane(bars.k_full, done) &&
+                      (w == 0 || wait_lane(bars.p_full[0][0], row_done[0]));
             if (ok) {
                 tmem_fence_after();
                 scores(0);
