@@ -2,20 +2,25 @@
 // a chunk of one) over the paged E4M3 cache: the same operator as
 // kv8_attention.cu, on tcgen05.
 //
-// What bounds it: the products, 4 * head_dim flops per row and key.  A block
-// takes 256 rows of one kv head as two 128-row tiles and goes through its keys
-// 128 at a time:
+// What bounds it: the products, 4 * head_dim flops per row and key, and beside
+// them 2^t for each score.  A block takes 256 rows of one kv head as two 128-row
+// tiles and goes through its keys 128 at a time:
 //   S = q K^T      128 x 128, both operands in shared memory, f16 -> fp32 in TMEM
-//   P = 2^(t - m)  t = log2(e) s + log2(v_scale), one row per thread, f16 in TMEM
+//   P = 2^(t - m)  t = log2(e) s + log2(v_scale), two threads per row, f16 in TMEM
 //   O += P V       128 x head_dim, P from TMEM, V from shared memory
 // While the softmax of one row tile runs, the tensor cores work on the other's
-// products; P is handed on in halves, so that O begins under the second half.  8 warps do the softmax, one copies pages into shared
-// memory (the bulk-copy engine, 16 keys at a time), 4 turn their E4M3 bytes into
-// f16 tiles (exactly) in the 128-byte swizzle that the tensor cores read, one
-// thread per row tile issues its products.  TMEM holds S (then P in its place) and O of both
-// tiles, all 512 columns.  K, V and q tiles are rows of 128 bytes (64 values),
-// 16-byte pieces XORed with the row; V is the transposed operand of the second
-// product, so both tiles are written alike.
+// products: one thread issues both, in turn.  16 warps do the softmax, a row's two
+// threads taking 64 keys of a tile each and exchanging the largest t (with one
+// thread per row, 8 warps, each warp's own latencies showed: 91 us against 87 for
+// 64 tokens of 64 heads on 8 kv heads of 128, over 32805 keys).  One warp copies
+// pages into shared memory (the bulk-copy engine, 16 keys at a time), 4 turn their
+// E4M3 bytes into f16 tiles (exactly) in the 128-byte swizzle that the tensor cores
+// read.  K and V tiles take turns in three buffers.  TMEM holds S (then P in its
+// place) and O of both row tiles, all 512 columns.  K, V and q tiles are rows of
+// 128 bytes (64 values), 16-byte pieces XORed with the row; V is the transposed
+// operand of the second product, so both tiles are written alike.  A softmax thread
+// has 80 registers, and a spilled value costs it more than its reload: shared
+// memory leaves the first-level cache little room.
 //
 // Softmax with a scale per page, as in kv8_attention.cu: O = sum P v_code,
 // l = sum P / v_scale.  m is the largest t when the row's O was last rescaled;
@@ -35,10 +40,11 @@ namespace {
 
 constexpr int kPromptKeys = 128;
 constexpr int kPromptRows = 256;
-constexpr int kHalfKeys = 64;  // keys of one product and one softmax step
-constexpr int kSoftmaxWarps = 8;
+constexpr int kHalfKeys = 64;  // keys of a tile that one of a row's two threads takes
+constexpr int kSoftmaxWarps = 16;
+constexpr int kBuffers = 3;    // of K and V tiles in turn
 constexpr int kConvertWarps = 4;
-constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 3) * 32;
+constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
 // Least rows per sequence and kv head, on average, for these kernels (8 sequences
 // of 8192 keys, 8 kv heads of 128: at 48 rows 96 us against 87 in three passes of
@@ -62,18 +68,19 @@ struct PromptShape {
     static constexpr int kTileBytes = 128 * kDim * 2;  // of q, K or V
     static constexpr int kQAt = 0;
     static constexpr int kKAt = kQAt + 2 * kTileBytes;
-    static constexpr int kVAt = kKAt + kTileBytes;
     // E4M3 bytes of the next K and V tile, as they come
-    static constexpr int kRawAt = kVAt + 2 * kTileBytes;
+    static constexpr int kRawAt = kKAt + kBuffers * kTileBytes;
     static constexpr int kRawBytes = kPromptKeys * kDim;
     // for each of 4 key tiles in turn and group of 16 keys: k_scale,
     // log2(v_scale), 1 / v_scale (the copies are at most 3 tiles ahead of the
     // softmax)
     static constexpr int kScalesAt = kRawAt + 2 * kRawBytes;
-    // per buffer and key: which of its values are NaN (filled where rows are masked)
+    // per V tile in turn and key: which of its values are NaN (filled where rows are masked)
     static constexpr int kNansAt = kScalesAt + 4 * kGroups * 16;
     static constexpr int kRowScaleAt = kNansAt + 2 * kPromptKeys * kDim / 8;
-    static constexpr int kSeqsAt = kRowScaleAt + kPromptRows * 4;
+    // per key tile in turn, half and row: the largest t there
+    static constexpr int kMaxAt = kRowScaleAt + kPromptRows * 4;
+    static constexpr int kSeqsAt = kMaxAt + 2 * 2 * kPromptRows * 4;
     // A partial state, in fp32 words: O as [kDim / 4][row][4] (neighbouring rows,
     // a row per thread, side by side), maxima [row], sums [row].
     static constexpr int kPartial = kPromptRows * (kDim + 2);
@@ -217,18 +224,15 @@ __device__ __forceinline__ bool sees(const ScoreRow& r, int j) {
     return !kGuard || (j < r.hi && (j >= r.lo || j < r.sinks));
 }
 
-// The largest t of the row.  The next 32 scores are on their way while 32 are
-// used.
+// The largest t of the row.
 template <bool kGuard>
 __device__ __forceinline__ float largest(const ScoreRow& r) {
     float most = -INFINITY;
-    float s[2][32];
-    tmem_load32(r.s_at, s[0]);
 #pragma unroll
     for (int c = 0; c < kHalfKeys / 32; ++c) {
-        float(&x)[32] = s[c & 1];
+        float x[32];
+        tmem_load32(r.s_at + 32 * c, x);
         tmem_wait_load(x);
-        if (c + 1 < kHalfKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -248,13 +252,11 @@ __device__ __forceinline__ float largest(const ScoreRow& r) {
 template <bool kGuard>
 __device__ __forceinline__ float weights(const ScoreRow& r, float shift) {
     float sum = 0.0f;
-    float s[2][32];
-    tmem_load32(r.s_at, s[0]);
 #pragma unroll
     for (int c = 0; c < kHalfKeys / 32; ++c) {
-        float(&x)[32] = s[c & 1];
+        float x[32];
+        tmem_load32(r.s_at + 32 * c, x);
         tmem_wait_load(x);
-        if (c + 1 < kHalfKeys / 32) tmem_load32(r.s_at + 32 * (c + 1), s[(c + 1) & 1]);
         uint32_t p[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -283,15 +285,32 @@ __device__ __forceinline__ float weights(const ScoreRow& r, float shift) {
     return sum;
 }
 
+// A barrier of 64 threads (two warps); whether all of them pass `ok`.
+__device__ __forceinline__ bool pair_barrier(int id, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n"
+        " barrier.cta.red.and.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(all)
+        : "r"(id), "r"(ok ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
+struct TileNote {
+    int j0;
+    unsigned paged;
+    bool masked;
+};
+
 // The block's barriers, each completed once per use.
 struct Barriers {
     uint64_t q_full;       // q tiles of a segment written
-    uint64_t k_full, k_empty;        // one K tile: its products run a tile ahead
-    uint64_t v_full[2], v_empty[2];  // two V tiles
+    uint64_t full[kBuffers], empty[kBuffers];  // K and V tiles in turn
     uint64_t raw_full[2], raw_empty[2];  // E4M3 bytes of K, of V
     uint64_t scales_full[4];             // page scales of 4 key tiles in turn
-    // row tile w, half h of a key tile: scores, P in their place, O with it added
-    uint64_t s_full[2][2], p_full[2][2], o_full[2][2];
+    // of row tile w: scores, P in their place, O with it added
+    uint64_t s_full[2], p_full[2], o_full[2];
 };
 
 template <int kDim, bool kFew>
@@ -306,12 +325,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ Segment segments[3];
     __shared__ int work;
     __shared__ volatile int abort;
-    __shared__ int nan_tile[2];  // per buffer: the last key tile in which a NaN was found
-    __shared__ unsigned paged[4];  // of 4 key tiles in turn: which groups of keys have a page
+    __shared__ int nan_tile[2];  // of 2 V tiles in turn: the last in which a NaN was found
+    // of 4 key tiles in turn: first key, which groups of keys have a page, whether
+    // some row does not see some key
+    __shared__ TileNote tile_notes[4];
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_addr(shared);
-    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps, kCopyWarp = kIssueWarp + 2;
+    constexpr int kIssueWarp = kSoftmaxWarps + kConvertWarps, kCopyWarp = kIssueWarp + 1;
     Seq* const seqs = reinterpret_cast<Seq*>(shared + S::kSeqsAt);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -323,17 +344,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (tid == 32) {
         mbar_init(smem_addr(&bars.q_full), kSoftmaxWarps * 32);
-        mbar_init(smem_addr(&bars.k_full), kConvertWarps * 32);
-        mbar_init(smem_addr(&bars.k_empty), 2);  // both row tiles' products
         for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars.scales_full[i]), 1);
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(smem_addr(&bars.full[i]), kConvertWarps * 32);
+            mbar_init(smem_addr(&bars.empty[i]), 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&bars.v_full[i]), kConvertWarps * 32);
-            mbar_init(smem_addr(&bars.v_empty[i]), 2);
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(smem_addr(&bars.s_full[i][h]), 1);
-                mbar_init(smem_addr(&bars.p_full[i][h]), 128);
-                mbar_init(smem_addr(&bars.o_full[i][h]), 1);
-            }
+            mbar_init(smem_addr(&bars.s_full[i]), 1);
+            mbar_init(smem_addr(&bars.p_full[i]), 256);
+            mbar_init(smem_addr(&bars.o_full[i]), 1);
             mbar_init(smem_addr(&bars.raw_full[i]), 1);
             mbar_init(smem_addr(&bars.raw_empty[i]), kConvertWarps);
             nan_tile[i] = -1;
@@ -388,16 +407,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (n <= 0) break;
 
         if (warp < kSoftmaxWarps) {
-            // ---- q, then the softmax of tile w, a row per thread
-            const int w = warp >> 2;
+            // ---- q, then the softmax of row tile w: a thread has one row's keys of
+            // half h of each key tile
+            const int w = warp >> 3, h = warp >> 2 & 1;
             {
                 constexpr int kLanes = kDim / 8;  // lanes per row
+                constexpr int kSteps = kPromptRows / kSoftmaxWarps * kLanes / 32;
                 const int sub = lane / kLanes, d = lane % kLanes;
-                uint4 x[kLanes];
+                const int row0 = warp * (kPromptRows / kSoftmaxWarps) + sub;
+                uint4 x[kSteps];
 #pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
-                    const int unit_row =
-                        g.r * kPromptRows + warp * 32 + i * (32 / kLanes) + sub;
+                for (int i = 0; i < kSteps; ++i) {
+                    const int unit_row = g.r * kPromptRows + row0 + i * (32 / kLanes);
                     const int token = token_of(a, unit_row);
                     const bool live = token < g.len;
                     const __nv_bfloat16* const from =
@@ -406,8 +427,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     x[i] = reinterpret_cast<const uint4*>(from)[d];
                 }
 #pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
-                    const int row = warp * 32 + i * (32 / kLanes) + sub;
+                for (int i = 0; i < kSteps; ++i) {
+                    const int row = row0 + i * (32 / kLanes);
                     // rows beyond the last are zeros
                     if (token_of(a, g.r * kPromptRows + row) >= g.len)
                         x[i] = make_uint4(0, 0, 0, 0);
@@ -424,14 +445,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 126);
                     float up = __uint_as_float((uint32_t)(e + 127) << 23);
                     if (a.scale < 0.0f) up = -up;
-                    uint32_t h[4];
+                    uint32_t f[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = f16x2(bf16_lo(u[k]) * up, bf16_hi(u[k]) * up);
+                        f[k] = f16x2(bf16_lo(u[k]) * up, bf16_hi(u[k]) * up);
                     uint8_t* const to = shared + S::kQAt + (row >> 7) * S::kTileBytes +
                                         (d >> 3) * 128 * 128 + (row & 127) * 128 +
                                         ((d ^ row) & 7) * 16;
-                    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(f[0], f[1], f[2], f[3]);
                     if (d == 0)
                         reinterpret_cast<float*>(shared + S::kRowScaleAt)[row] =
                             fabsf(a.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
@@ -441,80 +462,103 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             if (w < tiles) {
                 bool ok = wait(bars.q_full, number);  // and the row scales
-                const int row = tid & 127;
-                const int unit_row = g.r * kPromptRows + w * 128 + row;
+                const int row = w * 128 + (tid & 127);
+                const int unit_row = g.r * kPromptRows + row;
                 const int token = token_of(a, unit_row);
                 const int hi = token < g.len ? g.first + token + 1 : 0;
                 const int lo = a.window > 0 ? max(hi - a.window, 0) : 0;
                 const float row_scale =
-                    reinterpret_cast<const float*>(shared + S::kRowScaleAt)[w * 128 + row];
+                    reinterpret_cast<const float*>(shared + S::kRowScaleAt)[row];
                 const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-                const uint32_t s_at = lanes + w * 128, o_at = lanes + S::kO + w * kDim;
+                const uint32_t s_at = lanes + w * 128 + h * kHalfKeys;
+                constexpr int kMine = kDim / 2;  // columns of O that this thread scales and writes
+                const uint32_t o_at = lanes + S::kO + w * kDim + h * kMine;
+                const int partners = 1 + w * 4 + (warp & 3);  // their barrier
+                float* const maxima = reinterpret_cast<float*>(shared + S::kMaxAt) + row;
                 float top = -INFINITY, sum = 0.0f;
-                uint32_t nans[kDim / 32];
-#pragma unroll
-                for (int i = 0; i < kDim / 32; ++i) nans[i] = 0;
                 const unsigned before = w ? row_done[1] : row_done[0];
-                for (int i = 0; i < 2 * n && ok; ++i) {
-                    const int h = i & 1;
-                    const unsigned at = done + (i >> 1);
-                    const int buf = at & 1;
-                    const int j0 = tile_start(g.x0 + (i >> 1));
-                    const bool guard = masked(j0);
-                    ok = wait(bars.scales_full[at & 3], at >> 2) &&
-                         wait(bars.s_full[w][h], before + (i >> 1));
-                    if (!ok) break;
+                {
+                    float zero[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) zero[e] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kMine / 32; ++c) tmem_store32(o_at + 32 * c, zero);
+                }
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const unsigned at = done + i;
+                    ok = ok && wait(bars.scales_full[at & 3], at >> 2) &&
+                         wait(bars.s_full[w], before + i);
                     tmem_fence_after();
-                    const int from = j0 + h * kHalfKeys;
-                    const ScoreRow scores{s_at + h * kHalfKeys, row_scale,
+                    const int from = tile_notes[at & 3].j0 + h * kHalfKeys;
+                    const bool guard = tile_notes[at & 3].masked;
+                    const ScoreRow scores{s_at, row_scale,
                                           reinterpret_cast<const float4*>(shared + S::kScalesAt) +
                                               (at & 3) * kGroups + h * (kGroups / 2),
                                           hi - from, lo - from, a.sinks - from};
-                    const float most = guard ? largest<true>(scores) : largest<false>(scores);
+                    float most = guard ? largest<true>(scores) : largest<false>(scores);
+                    float* const here = maxima + (at & 1) * 2 * kPromptRows;
+                    here[h * kPromptRows] = most;
+                    // A row's two threads leave the loop together.
+                    ok = pair_barrier(partners, ok);
+                    if (!ok) break;
+                    most = fmaxf(most, here[(h ^ 1) * kPromptRows]);
                     if (__any_sync(0xffffffffu, most > top + kSlack)) {
                         const float now = fmaxf(most, top);
                         const float keep = now == -INFINITY ? 1.0f : exp2_fast(top - now);
                         top = now;
                         sum *= keep;
-                        if (i > 0) {  // all of O so far: these scores came after all but one half
-                            ok = wait(bars.o_full[w][h ^ 1], before + ((i - 1) >> 1));
-                            if (!ok) break;
-                            tmem_fence_after();
+                        // all of O so far: these scores came after it
+#pragma unroll 1
+                        for (int c = 0; c < kMine / 32 && i > 0; ++c) {
+                            float v[32];
+                            tmem_load32(o_at + 32 * c, v);
+                            tmem_wait_load(v);
 #pragma unroll
-                            for (int c = 0; c < kDim / 32; ++c) {
-                                float v[32];
-                                tmem_load32(o_at + 32 * c, v);
-                                tmem_wait_load(v);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] *= keep;
-                                tmem_store32(o_at + 32 * c, v);
-                            }
+                            for (int e = 0; e < 32; ++e) v[e] *= keep;
+                            tmem_store32(o_at + 32 * c, v);
                         }
                     }
                     const float shift = kPromptBias - (top == -INFINITY ? 0.0f : top);
                     sum += guard ? weights<true>(scores, shift) : weights<false>(scores, shift);
                     if (guard) {
-                        ok = wait(bars.v_full[buf], at >> 1);
-                        if (!ok) break;
-                        if (nan_tile[buf] == (int)at) {
-                            const uint32_t* const bits = reinterpret_cast<const uint32_t*>(
-                                shared + S::kNansAt + buf * kPromptKeys * kDim / 8 +
-                                h * kHalfKeys * kDim / 8);
-                            for (int j = 0; j < kHalfKeys; ++j)
-                                if (sees<true>(scores, j)) {
+                        const unsigned item = 2 * at + 1;
+                        ok = wait(bars.full[item % kBuffers], item / kBuffers);
+                        if (ok && nan_tile[at & 1] == (int)at) {
+                            // NaNs among the keys that the row sees, straight into O
+                            const uint32_t* const bits =
+                                reinterpret_cast<const uint32_t*>(shared + S::kNansAt +
+                                                                  (at & 1) * kPromptKeys * kDim / 8) +
+                                h * kMine / 32;
+#pragma unroll 1
+                            for (int c = 0; c < kMine / 32; ++c) {
+                                uint32_t bad = 0;
+                                for (int j = 0; j < kPromptKeys; ++j)
+                                    if (sees<true>(scores, j - h * kHalfKeys))
+                                        bad |= bits[j * kDim / 32 + c];
+                                __syncwarp();
+                                tmem_wait_store();
+                                float v[32];
+                                tmem_load32(o_at + 32 * c, v);
+                                tmem_wait_load(v);
 #pragma unroll
-                                    for (int k = 0; k < kDim / 32; ++k)
-                                        nans[k] |= bits[j * kDim / 32 + k];
-                                }
+                                for (int e = 0; e < 32; ++e)
+                                    if (bad >> e & 1) v[e] = NAN;
+                                tmem_store32(o_at + 32 * c, v);
+                            }
                         }
                         __syncwarp();
                     }
                     tmem_wait_store();
                     tmem_fence_before();
-                    mbar_arrive(smem_addr(&bars.p_full[w][h]));
+                    mbar_arrive(smem_addr(&bars.p_full[w]));
                 }
-                if (ok && wait(bars.o_full[w][0], before + n - 1) &&
-                    wait(bars.o_full[w][1], before + n - 1)) {
+                ok = ok && wait(bars.o_full[w], before + n - 1);
+                // in the place that the partner has read two tiles ago
+                float* const here = maxima + ((done + n) & 1) * 2 * kPromptRows;
+                here[h * kPromptRows] = sum;
+                if (pair_barrier(partners, ok)) {
+                    sum += here[(h ^ 1) * kPromptRows];
                     tmem_fence_after();
                     const bool live = token < g.len;
                     const bool whole = g.parts == 1;
@@ -524,17 +568,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     float* const part = a.partials + (size_t)g.slot * S::kPartial;
                     const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll
-                    for (int c = 0; c < kDim / 32; ++c) {
+                    for (int c = 0; c < kMine / 32; ++c) {
                         float v[32];
                         __syncwarp();
                         tmem_load32(o_at + 32 * c, v);
                         tmem_wait_load(v);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (nans[c] >> e & 1) v[e] = NAN;
                         if (live && whole) {
-                            uint4* const to =
-                                reinterpret_cast<uint4*>(a.out + out_row * kDim + 32 * c);
+                            uint4* const to = reinterpret_cast<uint4*>(a.out + out_row * kDim +
+                                                                       h * kMine + 32 * c);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 to[e] = make_uint4(bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
@@ -543,20 +584,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                                    bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
                         } else if (live) {
                             float4* const to = reinterpret_cast<float4*>(part) +
-                                               8 * c * kPromptRows + w * 128 + row;
+                                               (h * kMine + 32 * c) / 4 * kPromptRows + row;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                to[e * kPromptRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2],
-                                                    v[4 * e + 3]);
+                                to[e * kPromptRows] = make_float4(v[4 * e], v[4 * e + 1],
+                                                                  v[4 * e + 2], v[4 * e + 3]);
                         }
                     }
-                    if (live && whole && a.lse)
+                    if (live && whole && a.lse && h == 0)
                         a.lse[out_row] = sum == 0.0f ? -INFINITY
                                                      : 0.69314718055994531f *
                                                            ((top - kPromptBias) + log2f(sum));
-                    if (live && !whole) {
-                        part[kPromptRows * kDim + w * 128 + row] = top;
-                        part[kPromptRows * (kDim + 1) + w * 128 + row] = sum;
+                    if (live && !whole && h == 0) {
+                        part[kPromptRows * kDim + row] = top;
+                        part[kPromptRows * (kDim + 1) + row] = sum;
                     }
                     tmem_fence_before();
                 }
@@ -589,14 +630,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
                 const unsigned at = done + i;
-                const int buf = at & 1;
-                const int j0 = tile_start(g.x0 + i);
-                const bool guard = masked(j0);
+                // a buffer's barrier completes once per use
+                auto buffer = [&](unsigned item) {
+                    if (item >= kBuffers)
+                        ok = wait(bars.empty[item % kBuffers], item / kBuffers - 1);
+                    return S::kKAt + item % kBuffers * S::kTileBytes;
+                };
                 ok = wait(bars.raw_full[0], at);
-                // the barriers of empty buffers complete once per use
-                if (ok && at >= 1) ok = wait(bars.k_empty, at - 1);
                 if (!ok) break;
-                const unsigned pages = paged[at & 3];
+                const int j0 = tile_notes[at & 3].j0;
+                const bool guard = tile_notes[at & 3].masked;
+                const unsigned pages = tile_notes[at & 3].paged;
                 const bool partly = pages != (1u << kGroups) - 1 || j0 + kPromptKeys > keys.hi ||
                                     (j0 < keys.lo && j0 + kPromptKeys > a.sinks);
                 // all of a tile's bytes first: their latency is paid once
@@ -616,17 +660,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                 };
                 read(0);
-#pragma unroll
-                for (int m = 0; m < kItems; ++m)
-                    store(x[m], S::kKAt, row0 + m * kRowStep);
-                fence_shared_to_async();
-                mbar_arrive(smem_addr(&bars.k_full));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[0]));
+                const uint32_t k_at = buffer(2 * at);
+                if (!ok) break;
+#pragma unroll
+                for (int m = 0; m < kItems; ++m) store(x[m], k_at, row0 + m * kRowStep);
+                fence_shared_to_async();
+                mbar_arrive(smem_addr(&bars.full[2 * at % kBuffers]));
                 ok = wait(bars.raw_full[1], at);
                 if (!ok) break;
                 read(1);
-                if (at >= 2) ok = wait(bars.v_empty[buf], (at >> 1) - 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[1]));
+                const uint32_t v_at = buffer(2 * at + 1);
                 if (!ok) break;
                 if (guard) {
                     // NaNs out of the product, and where they were
@@ -644,17 +691,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         any |= bits;
                         reinterpret_cast<uint16_t*>(
                             shared + S::kNansAt +
-                            buf * kPromptKeys * kDim / 8)[(row0 + m * kRowStep) * kDim / 16 + piece] =
+                            (at & 1) * kPromptKeys * kDim / 8)[(row0 + m * kRowStep) * kDim / 16 + piece] =
                             (uint16_t)bits;
                     }
-                    if (any) nan_tile[buf] = (int)at;
+                    if (any) nan_tile[at & 1] = (int)at;
                 }
 #pragma unroll
-                for (int m = 0; m < kItems; ++m) store(x[m], S::kVAt + buf * S::kTileBytes, row0 + m * kRowStep);
+                for (int m = 0; m < kItems; ++m) store(x[m], v_at, row0 + m * kRowStep);
                 fence_shared_to_async();
-                mbar_arrive(smem_addr(&bars.v_full[buf]));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&bars.raw_empty[1]));
+                mbar_arrive(smem_addr(&bars.full[(2 * at + 1) % kBuffers]));
             }
         } else if (warp == kCopyWarp) {
             // ---- pages into shared memory as they are: a group of 16 keys is one
@@ -699,7 +744,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                 have ? make_float4(ks, __log2f(v), __fdividef(1.0f, v), 0.0f)
                                      : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
                         }
-                        if (lane == 0) paged[at & 3] = groups;
+                        if (lane == 0) {
+                            const int j0 = tile_start(x);
+                            tile_notes[at & 3] = TileNote{j0, groups, masked(j0)};
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&bars.scales_full[at & 3]));
                     }
@@ -716,65 +764,62 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 vs = vs1;
             }
             if (!ok) __nanosleep(100000);  // copies under way end before their memory is left
-        } else if (lane == 0 && warp - kIssueWarp < tiles) {
-            // ---- the products of row tile w
-            const int w = warp - kIssueWarp;
-            const uint64_t q_op = operand(smem + S::kQAt + w * S::kTileBytes, 16);
+        } else if (lane == 0) {
+            // ---- the products.  One thread issues both row tiles' in turn: issued by
+            // two, they would share the tensor cores evenly and end together, and both
+            // softmaxes would then run at one time and leave the tensor cores idle.
+            const uint64_t q_op = operand(smem + S::kQAt, 16);
             const uint64_t k_op = operand(smem + S::kKAt, 16);
-            const uint64_t v_op = operand(smem + S::kVAt, 128 * 128);
+            const uint64_t v_op = operand(smem + S::kKAt, 128 * 128);
             constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBlockUnits = 128 * 128 >> 4;
-            constexpr uint32_t kHalfUnits = kHalfKeys * 128 >> 4;
-            const uint32_t s_at = tmem + w * 128, o_at = tmem + S::kO + w * kDim;
-            const unsigned before = w ? row_done[1] : row_done[0];
-            // A buffer is empty when both row tiles are done with it; a single one
-            // answers for both.
-            auto release = [&](uint64_t& bar) {
-                mma_commit(smem_addr(&bar));
-                if (tiles == 1) mma_commit(smem_addr(&bar));
+            auto filled = [&](unsigned item) {
+                return wait_lane(bars.full[item % kBuffers], item / kBuffers);
             };
-            auto scores = [&](int h) {
+            auto release = [&](unsigned item) {
+                mma_commit(smem_addr(&bars.empty[item % kBuffers]));
+            };
+            auto scores = [&](int w, unsigned item) {
+                const uint64_t q = q_op + w * kTileUnits, key = k_op + item % kBuffers * kTileUnits;
 #pragma unroll
                 for (int k = 0; k < kDim / 16; ++k) {
                     const uint32_t off = (k / 4) * kBlockUnits + (k % 4) * 2;
-                    mma_shared(s_at + h * kHalfKeys, q_op + off, k_op + h * kHalfUnits + off,
-                               instruction(kHalfKeys, false), k > 0);
+                    mma_shared(tmem + w * 128, q + off, key + off, instruction(kPromptKeys, false),
+                               k > 0);
                 }
-                mma_commit(smem_addr(&bars.s_full[w][h]));
+                mma_commit(smem_addr(&bars.s_full[w]));
+                if (w + 1 == tiles) release(item);
             };
-            // The second row tile begins half a step after the first, so that one's
-            // softmax fills the other's waits.
-            bool ok = wait_lane(bars.q_full, number) && wait_lane(bars.k_full, done) &&
-                      (w == 0 || wait_lane(bars.p_full[0][0], row_done[0]));
+            bool ok = wait_lane(bars.q_full, number) && filled(2 * done);
             if (ok) {
                 tmem_fence_after();
-                scores(0);
-                scores(1);
-                release(bars.k_empty);
+#pragma unroll 1
+                for (int w = 0; w < tiles; ++w) scores(w, 2 * done);
             }
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
-                const unsigned at = done + i;
-                const int buf = at & 1;
-                ok = wait_lane(bars.v_full[buf], at >> 1);
-                for (int h = 0; h < 2 && ok; ++h) {
-                    ok = wait_lane(bars.p_full[w][h], before + i);
+                const unsigned item = 2 * (done + i) + 1;  // V
+                const uint64_t value = v_op + item % kBuffers * kTileUnits;
+                ok = filled(item);
+#pragma unroll 1
+                for (int w = 0; w < tiles && ok; ++w) {
+                    const unsigned use = (w ? row_done[1] : row_done[0]) + i;
+                    ok = wait_lane(bars.p_full[w], use);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kHalfKeys / 16; ++k)
-                        mma_tmem(o_at, s_at + h * kHalfKeys + 8 * k,
-                                 v_op + buf * kTileUnits + h * kHalfUnits + k * (2048 >> 4),
-                                 instruction(kDim, true), i > 0 || h > 0 || k > 0);
-                    mma_commit(smem_addr(&bars.o_full[w][h]));
-                    if (h == 1) release(bars.v_empty[buf]);
+                    for (int k = 0; k < kPromptKeys / 16; ++k)
+                        mma_tmem(tmem + S::kO + w * kDim,
+                                 tmem + w * 128 + (k / 4) * kHalfKeys + (k % 4) * 8,
+                                 value + k * (2048 >> 4), instruction(kDim, true), true);
+                    mma_commit(smem_addr(&bars.o_full[w]));
+                    if (w + 1 == tiles) release(item);
                     if (i + 1 == n) continue;
-                    // The next scores take the place of this P: products on different
-                    // sums are not ordered, so this one has to be complete.
-                    ok = (h == 1 || wait_lane(bars.k_full, at + 1)) &&
-                         wait_lane(bars.o_full[w][h], before + i);
+                    // The next scores take the place of P: products on different sums are
+                    // not ordered, so these have to be complete.
+                    ok = filled(item + 1) && wait_lane(bars.o_full[w], use);
                     if (!ok) break;
                     tmem_fence_after();
-                    scores(h);
-                    if (h == 1) release(bars.k_empty);
+                    scores(w, item + 1);
                 }
             }
             if (!ok) {
