@@ -45,8 +45,11 @@ constexpr float kBias = 14.0f;  // the largest weight is 2^14 in f16
 constexpr int kTile = 16;  // keys per tile: within one page
 constexpr int kMostBlocks = 320;
 
-// Units of kRows rows in tiles of kTile keys; at least 16 tiles per block, and
-// a unit, or a piece of one, costs about 24 tiles beside its own.
+// Units of kRows rows in tiles of kTile keys; at least 16 tiles per block (one
+// sequence of 1000 keys: 8.5 us; 9.6 with 4, 10.8 with 64), and a unit, or a piece
+// of one, costs about 24 tiles beside its own (16 sequences of 4 new tokens, window
+// 1024: 19.3 us, 23.3 with 8, 19.3 with 72; 32 sequences of 1000 to 16000 keys and
+// one new token: 65.8, 66.8 and 68.1).
 template <int kRows>
 using Tiling = TilingOf<kRows, kTile, 16, 24>;
 
@@ -837,14 +840,19 @@ cudaError_t launch_as(const AttentionArgs& a, int num_sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<kDim, kNT, kFew>, a);
 }
 
-// At most this many units (row tiles times kv heads of all sequences) leave
-// blocks to cut them up.
+// Few units (row tiles times kv heads of all sequences) are cut into equal parts,
+// which takes at least two blocks per unit (heads of 128, 8 of them: one sequence of
+// 131071 keys 49.8 us against 54.1 in one line of tiles, 8 of 8192 keys 28.9 against
+// 31.8, 4 of 20000 keys and two new tokens 53.1 against 52.2).
 template <int kDim, int kNT>
 cudaError_t launch(const AttentionArgs& a, int num_sms, cudaStream_t s) {
+    constexpr int kRows = 8 * kNT;
     const long long rows = (long long)a.bt.tokens * a.group;
-    const long long units = (rows / (8 * kNT) + a.bt.batch) * a.c.kv_heads;
-    return units <= num_sms / 4 ? launch_as<kDim, kNT, true>(a, num_sms, s)
-                                : launch_as<kDim, kNT, false>(a, num_sms, s);
+    // a sequence's rows are a multiple of the group: so much its last tile can lack
+    const int lack = kRows - min(kRows, a.group & -a.group);
+    const long long most = (rows + (long long)a.bt.batch * lack) / kRows * a.c.kv_heads;
+    return most <= num_sms / 2 ? launch_as<kDim, kNT, true>(a, num_sms, s)
+                               : launch_as<kDim, kNT, false>(a, num_sms, s);
 }
 
 }  // namespace

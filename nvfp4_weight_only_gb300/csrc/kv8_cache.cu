@@ -22,7 +22,10 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 constexpr int kAppendThreads = kAppendWarps * 32;
-constexpr int kWideRows = 16;  // new tokens per sequence from which a run takes a block
+// New tokens per sequence, on average, from which a run takes a block (8 sequences,
+// 8 kv heads of 128, 40 q heads: 1 token 5.3 us against 8.0, 16 tokens 5.9 against 8.5,
+// 32 tokens 9.1 both ways, 128 tokens 15.4 in blocks against 17.9).
+constexpr int kWideRows = 32;
 
 struct AppendArgs {
     Kv8CacheArgs c;

@@ -46,13 +46,18 @@ constexpr int kBuffers = 3;    // of K and V tiles in turn
 constexpr int kConvertWarps = 4;
 constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
-// Least rows per sequence and kv head, on average, for these kernels (8 sequences
-// of 8192 keys, 8 kv heads of 128: at 48 rows 96 us against 87 in three passes of
-// kv8_attention.cu, at 64 rows 95 against 94, at 128 rows 97 against 145).
-constexpr int kPromptLeastRows = 64;
+// Rows per sequence and kv head, on average, up to which one pass of
+// kv8_attention.cu holds them and is the faster (8 sequences of 8192 keys, 8 kv
+// heads of 128: 32 rows 67 us against 76 here, 40 rows 119 against 76, 128 rows 145
+// against 71; one sequence of 1000 keys, where this kernel's longer start shows:
+// 32 rows 14.9 against 16.8, 64 rows 15.4 against 17.1, 128 rows 17.6 against 17.7).
+constexpr int kPromptRowsAbove = 32;
 constexpr float kPromptBias = 6.0f;
 constexpr float kSlack = 8.0f;
 
+// At least 2 tiles per block; a unit, or a piece of one, costs about 4 tiles beside
+// its own (2 prompts of 1500 tokens, 32 heads on 8: 106 us, 124 with 2, 106 with 7;
+// 8 ragged ones of up to 1024 tokens over up to 2000 keys, 40 heads: 217, 248, 238).
 using PromptTiling = TilingOf<kPromptRows, kPromptKeys, 2, 4>;
 
 // One block's note for the join: the unit whose first part it has, if that
@@ -930,7 +935,7 @@ cudaError_t launch(const AttentionArgs& a, JoinNote* notes, int* status, int num
 }  // namespace
 
 bool kv8_prompt_applies(int head_dim, long long tokens, int group, int batch) {
-    return head_dim <= 128 && tokens * group >= (long long)kPromptLeastRows * batch;
+    return head_dim <= 128 && tokens * group > (long long)kPromptRowsAbove * batch;
 }
 
 size_t kv8_prompt_data_bytes(int head_dim, int num_sms) {
@@ -943,6 +948,8 @@ cudaError_t launch_kv8_prompt(AttentionArgs a, void* data, int* status, int num_
     JoinNote* const notes = reinterpret_cast<JoinNote*>(data);
     a.partials = reinterpret_cast<float*>(reinterpret_cast<char*>(data) +
                                           ((size_t)num_sms * sizeof(JoinNote) + 255) / 256 * 256);
+    // equal parts, as in kv8_attention.cu (one prompt of 512 tokens, 32 heads on 8: 24.5 us
+    // against 26.0 in one line of tiles)
     const long long rows = (long long)a.bt.tokens * a.group;
     const bool few = (rows / kPromptRows + a.bt.batch) * a.c.kv_heads <= num_sms / 2;
     if (a.c.head_dim == 64)

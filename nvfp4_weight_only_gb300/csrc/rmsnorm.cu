@@ -43,7 +43,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                       bf16x2(v[6], v[7]));
 }
 
-constexpr int kManyRows = 512;
+constexpr int kManyRows = 256;
 
 // kVecs: vectors per thread.  The vectors of a warp are consecutive, so 16
 // lanes hold one group of 128 columns.
@@ -142,9 +142,10 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
     a.weight_bias = weight_bias;
     const int per = (a.vecs + 1023) / 1024;
     if (per > 4) return cudaErrorInvalidValue;
-    // One vector per thread is the shortest chain for a few rows (1 x 5120: 1.8 us
-    // against 1.9 with two); many rows want small blocks, whose loads and stores
-    // overlap others' (4096 x 5376: two vectors 29.8 us, one 33.3, four 35.7).
+    // One vector per thread is the shortest chain for a few rows (H = 5120: 1 row 1.9
+    // us both ways, 256 rows 3.1 against 3.2 with two); many rows want small blocks,
+    // whose loads and stores overlap others' (512 rows 4.0 against 3.6 with two; 4096
+    // rows of 5376 into E4M3 33.3, two 29.8, four 35.7).
     const int kv = per <= 1 ? (M > kManyRows ? 2 : 1) : per <= 2 ? 2 : 4;
     const int threads = ((a.vecs + kv - 1) / kv + 31) / 32 * 32;
     cudaLaunchConfig_t cfg{};
