@@ -530,6 +530,8 @@ size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* ba
  * window, sinks >= 0 (sinks without a window have no effect).  Within a
  * sequence the pages' v_scales may differ by up to 2^100 (a smaller one's
  * weights may be lost beyond that).
+ * A kernel that waited for itself longer than its limit leaves wrong outputs and
+ * NVFP4_ERR_TIMEOUT for nvfp4_workspace_status on ws.
  */
 nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int heads,
                            const kv8_cache* cache, const kv8_batch* batch, float softmax_scale,

@@ -343,7 +343,8 @@ __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
 
 // One token per sequence, or few: a warp per run and head of k or v (a block's
 // warps take neighbouring heads, which share the run's rotations in L1), then q,
-// a warp per token.
+// a warp per token.  Latency bounds it: list, table and page are found one
+// after the other (4.2 us for one token of 40 heads on 8, 7.2 for 64 tokens).
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -371,7 +372,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
 }
 
 // Prompts: a block per run and head, k and v, so that both are on their way
-// while the run and its page are looked up and k is worked on.
+// while the run and its page are looked up and k is worked on.  Memory bounds it: a
+// run's rows stay on chip between the maximum and the codes, so they are read once
+// (up to 3001 tokens of 5 sequences, 32 heads on 16, with q: 98 us for 436 MB, 4.4 TB/s;
+// a block waits for its run's table, rows and sum one after the other).
 __global__ void __launch_bounds__(kAppendThreads, 4) kv8_append_rows_kernel(const AppendArgs a) {
     __shared__ float tops[2][kAppendWarps];
     __shared__ float4 kept[kHeld * 4 * kAppendThreads];
@@ -406,7 +410,8 @@ struct ReadArgs {
 
 constexpr int kReadThreads = 128;
 
-// One run of one head of k or v per block.
+// One run of one head of k or v per block; memory bounds it (93 us for 587 MB, 6.3
+// TB/s of 6.8 that a copy reaches).
 __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const ReadArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

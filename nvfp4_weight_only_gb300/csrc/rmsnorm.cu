@@ -10,6 +10,10 @@
 // between the sum of squares and the output, so x and the residual are read
 // once.  The sum, the norm and y stay in fp32 (the residual stream's rounding
 // to bf16 does not enter the norm).
+//
+// Memory bounds many rows (4096 x 5376 with residual, into E4M3: 29.5 us for 155 MB,
+// 5.2 TB/s; the block's sum is a wait that other blocks of the SM fill only in part),
+// one row the launch (1.8 us).
 #include "kv8.cuh"
 
 namespace nvf {
