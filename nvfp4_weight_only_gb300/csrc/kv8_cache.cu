@@ -23,9 +23,9 @@ namespace {
 constexpr int kAppendWarps = 8;
 constexpr int kAppendThreads = kAppendWarps * 32;
 // New tokens per sequence, on average, from which a run takes a block (8 sequences,
-// 8 kv heads of 128, 40 q heads: 1 token 5.3 us against 8.0, 16 tokens 5.9 against 8.5,
-// 32 tokens 9.1 both ways, 128 tokens 15.4 in blocks against 17.9).
-constexpr int kWideRows = 32;
+// 8 kv heads of 128, 40 q heads: 1 token 4.4 us against 4.8 in blocks, 8 tokens 4.5
+// against 5.0, 16 tokens 5.5 against 5.1, 128 tokens 17.4 against 9.4).
+constexpr int kWideRows = 16;
 
 struct AppendArgs {
     Kv8CacheArgs c;
@@ -37,7 +37,7 @@ struct AppendArgs {
     __nv_bfloat16* q_out;
     long long k_stride, v_stride, q_stride;
     int heads, runs;
-    int cache_blocks;  // blocks of the cache's part; the rest rotates q
+    int cache_blocks, q_blocks;  // blocks of the cache's part; those that rotate q
 };
 
 // A slot is 16 values of a head, as two vectors of 8.  In the half layout a
@@ -311,9 +311,25 @@ __device__ __forceinline__ void store_run(const AppendArgs& a, const Kv8Run& r, 
     if (mate == 0) *scales = scale;  // read by all before the maxima were joined
 }
 
-// Rotates q of one token (or copies it without a table), by one warp.
+// Rotates q of one token (or copies it without a table), by one warp.  The first
+// heads are on their way while the token's position is looked up.
+template <int kAhead>
 __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
     const int lane = threadIdx.x & 31;
+    const int dim = a.c.head_dim, slots = dim / 16, step = 32 / slots;
+    const Slot slot = slot_of(a.rope, lane % slots, slots);
+    const __nv_bfloat16* src = a.q + t * a.q_stride;
+    __nv_bfloat16* dst = a.q_out + (size_t)t * a.heads * dim;
+    const int head0 = lane / slots;
+    Raw raw[kAhead];
+    auto load = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int head = first + i * step;
+            if (head < a.heads) raw[i] = load_raw(src + (size_t)head * dim, slot);
+        }
+    };
+    load(head0);
     const int b = kv8_owner(a.bt, t);
     int position = 0;
     if (b < a.bt.batch) {
@@ -324,27 +340,29 @@ __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
         kv8_report(a.bt);
     }
     position = rope_position(a, max(position, 0));
-    const int dim = a.c.head_dim, slots = dim / 16, step = 32 / slots;
-    const Slot slot = slot_of(a.rope, lane % slots, slots);
     Turn turn;
     if (slot.turn_a || slot.turn_b) turn = load_turn(a.rope, position, slot);
-    const __nv_bfloat16* src = a.q + t * a.q_stride;
-    __nv_bfloat16* dst = a.q_out + (size_t)t * a.heads * dim;
-#pragma unroll 4
-    for (int head = lane / slots; head < a.heads; head += step) {
-        const Raw raw = load_raw(src + (size_t)head * dim, slot);
-        float p[8], r[8];
-        values(a.rope, raw, slot, turn, p, r);
-        uint4* to = reinterpret_cast<uint4*>(dst + (size_t)head * dim);
-        to[slot.a] = pack8(p);
-        to[slot.b] = pack8(r);
+#pragma unroll 1
+    for (int first = head0; first < a.heads;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int head = first + i * step;
+            if (head >= a.heads) break;
+            float p[8], r[8];
+            values(a.rope, raw[i], slot, turn, p, r);
+            uint4* to = reinterpret_cast<uint4*>(dst + (size_t)head * dim);
+            to[slot.a] = pack8(p);
+            to[slot.b] = pack8(r);
+        }
+        first += kAhead * step;
+        load(first);
     }
 }
 
 // One token per sequence, or few: a warp per run and head of k or v (a block's
 // warps take neighbouring heads, which share the run's rotations in L1), then q,
 // a warp per token.  Latency bounds it: list, table and page are found one
-// after the other (4.2 us for one token of 40 heads on 8, 7.2 for 64 tokens).
+// after the other (3.2 us for one token of 40 heads on 8).
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -367,21 +385,32 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         }
     } else {
         const int t = (blockIdx.x - a.cache_blocks) * kAppendWarps + (threadIdx.x >> 5);
-        if (t < a.bt.tokens) turn_q(a, t);
+        if (t < a.bt.tokens) turn_q<4>(a, t);
     }
 }
 
 // Prompts: a block per run and head, k and v, so that both are on their way
 // while the run and its page are looked up and k is worked on.  Memory bounds it: a
 // run's rows stay on chip between the maximum and the codes, so they are read once
-// (up to 3001 tokens of 5 sequences, 32 heads on 16, with q: 98 us for 436 MB, 4.4 TB/s;
-// a block waits for its run's table, rows and sum one after the other).
+// (up to 3001 tokens of 5 sequences, 32 heads on 16, with q: 82 us for 436 MB, 5.4 TB/s).
+// A block waits for its run's table, rows and sum one after the other and then has
+// much to compute; q's warps mostly wait for memory: mixed, they fill each other's gaps
+// (99 us in two launches).
 __global__ void __launch_bounds__(kAppendThreads, 4) kv8_append_rows_kernel(const AppendArgs a) {
     __shared__ float tops[2][kAppendWarps];
     __shared__ float4 kept[kHeld * 4 * kAppendThreads];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int run = blockIdx.x / a.c.kv_heads, head = blockIdx.x - run * a.c.kv_heads;
+    // q's blocks lie evenly among the others
+    const unsigned q_before =
+        (unsigned)((unsigned long long)blockIdx.x * a.q_blocks / gridDim.x);
+    if ((unsigned)((unsigned long long)(blockIdx.x + 1) * a.q_blocks / gridDim.x) != q_before) {
+        const int t = q_before * kAppendWarps + (threadIdx.x >> 5);
+        if (t < a.bt.tokens) turn_q<2>(a, t);
+        return;
+    }
+    const int x = blockIdx.x - q_before;
+    const int run = x / a.c.kv_heads, head = x - run * a.c.kv_heads;
     Kv8Run r;
     if (!kv8_find_run(a.bt, run, r)) return;
     const RunPart<true, kAppendThreads> k(a, r, head);
@@ -390,14 +419,6 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv8_append_rows_kernel(cons
     if (page < 0) return;
     store_run(a, r, page, head, k, tops[0], kept);
     store_run(a, r, page, head, v, tops[1], nullptr);
-}
-
-// q of many tokens by itself: it needs fewer registers than the cache's part.
-__global__ void __launch_bounds__(kAppendThreads, 4) kv8_turn_kernel(const AppendArgs a) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-    if (t < a.bt.tokens) turn_q(a, t);
 }
 
 struct ReadArgs {
@@ -534,13 +555,13 @@ cudaError_t launch_kv8_append(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, con
     const long long cache_blocks = (runs * 2 * c.kv_heads + kAppendWarps - 1) / kAppendWarps;
     if (runs * 2 * c.kv_heads + q_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     a.cache_blocks = (int)cache_blocks;
+    a.q_blocks = (int)q_blocks;
     if (bt.tokens < kWideRows * bt.batch)
         return launch_after(kv8_append_kernel, (unsigned)(cache_blocks + q_blocks), kAppendThreads,
                             s, a);
-    const cudaError_t e = launch_after(kv8_append_rows_kernel, (unsigned)(runs * c.kv_heads),
-                                       kAppendThreads, s, a);
-    if (e != cudaSuccess || !q) return e;
-    return launch_after(kv8_turn_kernel, (unsigned)q_blocks, kAppendThreads, s, a);
+    a.cache_blocks = (int)(runs * c.kv_heads);
+    return launch_after(kv8_append_rows_kernel, (unsigned)(a.cache_blocks + q_blocks),
+                        kAppendThreads, s, a);
 }
 
 cudaError_t launch_kv8_read(const Kv8CacheArgs& c, const Kv8BatchArgs& bt, void* k_out,
