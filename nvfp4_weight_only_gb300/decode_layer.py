@@ -37,7 +37,7 @@ class DecodeLayer:
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.rope, self.interleaved = rope, interleaved
         self.window, self.sinks, self.eps, self.act = window, sinks, eps, act
-        self.softmax_scale = softmax_scale or 1.0 / math.sqrt(head_dim)
+        self.softmax_scale = 1.0 / math.sqrt(head_dim) if softmax_scale is None else softmax_scale
         self.norm_in, self.norm_ffn = norm_in, norm_ffn
         H, I = self.H, self.I
         self.rows = (heads + 2 * kv_heads) * head_dim

@@ -141,3 +141,8 @@ def test_step_refuses_other_sizes(dev):
     x = torch.zeros((65, H), dtype=torch.bfloat16, device=dev)
     with pytest.raises(ValueError):
         layer.step(x, x, None, None)
+
+
+def test_a_softmax_scale_of_zero_is_kept(dev):
+    layer = DecodeLayer.synthetic(H, I, HEADS, KV_HEADS, DIM, dev, softmax_scale=0.0)
+    assert layer.softmax_scale == 0.0
