@@ -620,7 +620,7 @@ def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tenso
     """Write k, v [tokens, kv_heads, head_dim] into the cache, k rotated by the rope table; with
     q [tokens, heads, head_dim] given, return it rotated (contiguous, in q_out when given)."""
     device, dim = _same_device(cache, batch), cache.head_dim
-    T = len(k)
+    T = k.shape[0]
     k_at, k_stride = _rows(k, "k", T, cache.kv_heads, dim, device)
     v_at, v_stride = _rows(v, "v", T, cache.kv_heads, dim, device)
     q_at = out_at = rope_at = None
@@ -651,7 +651,7 @@ def kv8_append(cache: Kv8Cache, batch: Kv8Batch, k: torch.Tensor, v: torch.Tenso
 def kv8_read(cache: Kv8Cache, batch: Kv8Batch, k_out: torch.Tensor, v_out: torch.Tensor):
     """Read the batch's tokens back: k_out, v_out bf16 [tokens, kv_heads, head_dim]."""
     device = _same_device(cache, batch)
-    T = len(k_out)
+    T = k_out.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
     code = (_lib or load()).kv8_read(cache.ref, batch.ref, T,
                                      _plain(k_out, "k_out", _BF16, shape, device),
