@@ -289,6 +289,79 @@ def test_large_scores_and_values(dev):
     assert bool((err[0, 4] <= 2.0 ** -8 * want[0, 4].abs() + 1e-30).all())
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,marks", [
+    (0, [(10, 3), (551, 1), (600, -1), (639, 40), (640, 32), (699, 7)]),
+    (200, [(360, 2), (400, 35), (511, 0), (512, -1), (575, 20)])])
+def test_value_nans_of_many_rows_reach_the_rows_that_see_them(dev, dim, window, marks):
+    """150 tokens of 4 heads per kv head: several units of two row tiles, cut into parts."""
+    n, kv, page = 150, 700, 32
+    s = Setup(dev, [n], [kv], 2, dim, page, seed=21)
+    want = torch.zeros((n, dim), dtype=torch.bool)
+    p = torch.arange(kv - n, kv)
+    for j, d in marks:
+        s.codes["v"][int(s.table[0, j // page]), 1, j % page, d] = NAN_CODE
+        want[(j <= p) & ((j > p - window) if window else True), d] = True
+    s.upload()
+    out, lse = run_attention(s, draw_q(n, 8, dim, 5), 0.02, window)
+    bad = torch.isnan(out.cpu().float())
+    assert not bad[:, :4].any()
+    assert torch.equal(bad[:, 4:], want[:, None].expand(n, 4, dim))
+    assert not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("n", [1, 40])
+def test_largest_score_moves_from_tile_to_tile(dev, dim, rising, n):
+    """Keys' scales that rise (or fall) by 2^0.75 from page to page, values' that jump by 2^10:
+    scores to over a thousand, a new maximum in nearly every tile."""
+    kv, heads = 1000, 8
+    s = Setup(dev, [n], [kv], 1, dim, 64, seed=23)
+    for i in range(16):
+        at = int(s.table[0, i])
+        s.scales["k"][at] = 2.0 ** (0.75 * (i if rising else 15 - i) - 9)
+        s.scales["v"][at] *= 2.0 ** (10 * (i % 3))
+    s.upload()
+    q = draw_q(n, heads, dim, 6)
+    scale = 1.0 / math.sqrt(dim)
+    out, lse = run_attention(s, q, scale)
+    rows = s.table[0].long()
+    k, v = (s.values(x)[rows, 0].flatten(0, 1)[:kv] for x in "kv")
+    hidden = torch.arange(kv)[None] > torch.arange(kv - n, kv)[:, None]
+    for h in range(heads):
+        x = q[:, h].double()
+        sc = (x @ k.T) * scale
+        d = (dim + 8) * 2.0 ** -24 * (x.abs() @ k.abs().T).masked_fill(hidden, 0).amax(1) * scale
+        sc = sc.masked_fill(hidden, -math.inf)
+        want_lse = torch.logsumexp(sc, 1)
+        w = torch.exp(sc - want_lse[:, None])
+        # scores this large are off by d, so weights by a factor e^(2d)
+        bound = (torch.expm1(2 * d)[:, None] + 2.0 ** -10) * (w @ v.abs())
+        assert bool(ref.rounds_to(out[:, h], w @ v, bound).all())
+        off = (lse[:, h].cpu().double() - want_lse).abs()
+        assert bool((off <= d + 2.0 ** -20 + kv * 2.0 ** -24 + 2.0 ** -22 * want_lse.abs()).all())
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim", [
+    ([8, 8], [500, 700], 8, 2, 128),        # 32 rows each: one pass
+    ([9, 8], [500, 700], 8, 2, 128),        # one row more on average
+    ([33, 0], [400, 90], 4, 4, 64),         # an empty sequence in the average
+    ([1] * 9 + [300], [50] * 9 + [310], 3, 1, 128),  # single tokens beside a prompt
+    ([1] * 9 + [300], [50] * 9 + [310], 3, 1, 64),
+    ([1] * 9, [2000 + i for i in range(9)], 40, 8, 128),  # 72 units, 76 the most that count as few
+    ([1] * 10, [2000 + i for i in range(10)], 40, 8, 128),
+    ([2] * 3, [1500, 1, 2], 24, 8, 128)])
+def test_attention_around_the_rules(dev, q_lens, kv_lens, heads, kv_heads, dim):
+    """Sizes on both sides of where one kernel or way of cutting gives way to another."""
+    q_lens = [min(n, kv) for n, kv in zip(q_lens, kv_lens)]
+    s = Setup(dev, q_lens, kv_lens, kv_heads, dim, 64, seed=29)
+    q = draw_q(s.tokens, heads, dim, 8)
+    scale = 1.0 / math.sqrt(dim)
+    out, lse = run_attention(s, q, scale)
+    check_attention(s, q, out, lse, scale, 0, 0)
+
+
 def test_long_cache_offsets(dev):
     """Pages whose codes lie beyond 2^32 bytes and 2^31 rows of the buffers."""
     pages, kv_heads, page, dim = 33000, 8, 128, 128
