@@ -11,9 +11,10 @@
 // once.  The sum, the norm and y stay in fp32 (the residual stream's rounding
 // to bf16 does not enter the norm).
 //
-// Memory bounds many rows (4096 x 5376 with residual, into E4M3: 29.5 us for 155 MB,
-// 5.2 TB/s; the block's sum is a wait that other blocks of the SM fill only in part),
-// one row the launch (1.8 us).
+// Memory bounds many rows (4096 x 5376 with residual, into E4M3: 25 us for 155 MB,
+// 6.2 TB/s; the block's sum is a wait that other blocks of the SM have to fill),
+// one row the launch (1.8 us).  Arithmetic on pairs halves its instructions, which
+// took 63% of the issue slots (29.5 us before).
 #include "kv8.cuh"
 
 namespace nvf {
@@ -33,26 +34,32 @@ struct NormArgs {
     float inv_h, eps, weight_bias;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+// 8 bf16 values as pairs of fp32.
+__device__ __forceinline__ void unpack8(const uint4& w, uint64_t (&v)[4]) {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(a[i]);
-        v[2 * i + 1] = bf16_hi(a[i]);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = pair(bf16_lo(a[i]), bf16_hi(a[i]));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                      bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = unpair(v[i]);
+        w[i] = bf16x2(p.x, p.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 constexpr int kManyRows = 256;
 
 // kVecs: vectors per thread.  The vectors of a warp are consecutive, so 16
 // lanes hold one group of 128 columns.
+// Registers are given out by eights: 40 per thread let one block more onto an SM
+// than the 42 that the compiler would take (4096 x 5376 into E4M3, 352 threads: 25.1
+// us against 28.0; 28.4 with 32, which spill).  Blocks have up to 1024 threads.
 template <int kVecs>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __maxnreg__(kVecs == 1 ? 32 : kVecs == 2 ? 40 : 64) add_rmsnorm_kernel(const NormArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -70,22 +77,22 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
             w[i] = a.weight[c];
         }
     }
-    float r[kVecs][8];
-    float ss = 0.0f;
+    uint64_t r[kVecs][4], squares = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int c = tid + i * blockDim.x;
         unpack8(in[i], r[i]);
         if (a.residual) {
-            float o[8];
+            uint64_t o[4];
             unpack8(more[i], o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[i][e] += o[e];
+            for (int e = 0; e < 4; ++e) r[i][e] = add2(r[i][e], o[e]);
         }
         if (a.sum_out && c < a.vecs) a.sum_out[row * a.vecs + c] = pack8(r[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
+        for (int e = 0; e < 4; ++e) squares = fma2(r[i][e], r[i][e], squares);
     }
+    float ss = unpair(squares).x + unpair(squares).y;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     __shared__ float part[32];
@@ -95,32 +102,36 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     const float inv = rsqrtf(total * a.inv_h + a.eps);
+    const uint64_t by_inv = pair(inv, inv), bias = pair(a.weight_bias, a.weight_bias);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int c = tid + i * blockDim.x;
         const bool live = c < a.vecs;
-        float y[8];
+        uint64_t y[4];
         unpack8(w[i], y);
+        // beyond the row 0, or NaN when the norm is not finite: neither enters a maximum
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = live ? r[i][e] * inv * (y[e] + a.weight_bias) : 0.0f;
+        for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(r[i][e], by_inv), add2(y[e], bias));
         if (a.out) {
             if (live) a.out[row * a.vecs + c] = pack8(y);
             continue;
         }
         float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+        for (int e = 0; e < 4; ++e)
+            top = fmaxf(top, fmaxf(fabsf(unpair(y[e]).x), fabsf(unpair(y[e]).y)));
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float scale = top == 0.0f ? 1.0f : fmaxf(__fdiv_rn(top, 448.0f), 1.17549435e-38f);
         if (live) {
             // y / scale through the reciprocal: off by at most 2^-22 of itself
             const float by = __frcp_rn(scale);
-            float q[8];
+            float2 q[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = y[e] * by;
-            a.codes[row * a.vecs + c] = make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
-                                                   f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
+            for (int e = 0; e < 4; ++e) q[e] = unpair(mul2(y[e], pair(by, by)));
+            a.codes[row * a.vecs + c] =
+                make_uint2(f32x4_to_e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y),
+                           f32x4_to_e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
             if ((c & 15) == 0) a.scales[row * a.groups + (c >> 4)] = scale;
         }
     }
@@ -146,10 +157,11 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
     a.weight_bias = weight_bias;
     const int per = (a.vecs + 1023) / 1024;
     if (per > 4) return cudaErrorInvalidValue;
-    // One vector per thread is the shortest chain for a few rows (H = 5120: 1 row 1.9
-    // us both ways, 256 rows 3.1 against 3.2 with two); many rows want small blocks,
-    // whose loads and stores overlap others' (512 rows 4.0 against 3.6 with two; 4096
-    // rows of 5376 into E4M3 33.3, two 29.8, four 35.7).
+    // One vector per thread is the shortest chain for a few rows (H = 5120 into bf16: 1
+    // row 1.9 us against 2.0 with two, 256 rows 3.0 against 3.1); many rows want small
+    // blocks, whose loads and stores overlap others' (512 rows 3.9 against 3.5 with
+    // two, 4096 rows 26.8 against 25.8).  Four are for rows that 1024 threads with two
+    // do not hold.
     const int kv = per <= 1 ? (M > kManyRows ? 2 : 1) : per <= 2 ? 2 : 4;
     const int threads = ((a.vecs + kv - 1) / kv + 31) / 32 * 32;
     cudaLaunchConfig_t cfg{};
