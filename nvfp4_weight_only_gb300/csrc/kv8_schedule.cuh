@@ -168,7 +168,9 @@ __device__ __forceinline__ void store_row(const AttentionArgs& a, int q0, int le
 // cut into equal ranges, one per block.  Few units (a single sequence, say):
 // each is cut evenly into parts of at most `most` tiles, one per block; with U
 // units, total / (blocks - U) tiles per part give at most `blocks` parts.  About as
-// many units as blocks, none much longer than the others: one block each.
+// many units as blocks, none much longer than the others: one block each.  A part or
+// range always has a block: a unit's counter and partial states are joined when all
+// its parts have come, so one part too many would spoil the workspace for later calls.
 template <typename T>
 struct Plan {
     unsigned total, ranges;
@@ -263,15 +265,25 @@ public:
         }
         if (sum == kMostTiles) kv8_report(a.bt);  // over 8e12 bytes of keys and values
         if (sum == 0 || sum == kMostTiles) return false;
-        // at most half of the blocks go to rounding (the host has bounded the units)
-        if (kFew)
-            p.most = max((unsigned)kMinTiles, sum / (gridDim.x - min(units, gridDim.x / 2)) + 1);
+        // At most half of the blocks go to rounding.  The host has bounded the units by
+        // the tokens; a malformed list, whose sequences overlap, may hold more of them,
+        // and their equal parts would outnumber the blocks: it takes the line, which
+        // any number of units fits.
+        if (kFew) {
+            p.most = units > gridDim.x / 2
+                         ? 0
+                         : max((unsigned)kMinTiles, sum / (gridDim.x - units) + 1);
+            if (p.most == 0 && sum + (unsigned long long)units * kUnitCost > kMostTiles) {
+                kv8_report(a.bt);
+                return false;
+            }
+        }
         // a block per unit, where cutting the longest would cost more than it saves
         if (!kFew && units <= gridDim.x) {
             longest = __reduce_max_sync(0xffffffffu, longest);
             if ((unsigned)longest <= sum / gridDim.x) p.most = longest;
         }
-        if (batch > 1 || p.most) {
+        if (batch > 1 || kFew || p.most) {
             sum = 0;
 #pragma unroll 1
             for (int b0 = 0; b0 < batch; b0 += 32) {

@@ -1,0 +1,63 @@
+"""Lists that do not fit the call's buffers, or strain the kernels' index arithmetic: what they
+concern is left out and reported, everything else is right, and the workspace serves the next call.
+Tolerances are those of test_gpu_kv8.py."""
+import math
+
+import pytest
+import torch
+
+import kv8_reference as ref
+from nvfp4_weight_only_gb300 import ffi
+from test_gpu_kv8 import Setup, check_attention, draw_q, run_attention
+
+pytestmark = pytest.mark.gpu
+
+RANGE = 4
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ffi.load(build_if_missing=True)
+    return torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("sequences,tokens,group,keys", [
+    (60, 2048, 1, 2 ** 20),  # many rows per sequence: 240 units of 256 rows where 68 are the bound
+    (64, 64, 8, 2 ** 19)])   # few rows: 2048 units of 8 rows where 64 are the bound
+def test_overlapping_sequences_leave_the_workspace_whole(dev, dim, sequences, tokens, group, keys):
+    """q_start = 0, T, 0, T, ...: every second sequence has all T tokens, so there are many more
+    units than tokens allow.  The call reports it; the next, on the same workspace, is right."""
+    page = 256
+    pages = 8
+    shape = (pages, 1, page, dim)
+    g = torch.Generator().manual_seed(3)
+    codes = [ref.round_e4m3(torch.randn(shape, generator=g) * 100).to(dev) for _ in "kv"]
+    cache = ffi.Kv8Cache(*codes, *[torch.full((pages, 1), 2.0 ** -7, device=dev) for _ in "kv"])
+    starts = [tokens * (b % 2) for b in range(sequences + 1)]
+    lens = [tokens] * sequences
+    lens[36] = keys  # its units stand where the blocks would end
+    # pages may be shared by sequences that are only read
+    table = (torch.arange(keys // page, dtype=torch.int32) % pages).expand(sequences, -1)
+    bad = ffi.Kv8Batch(torch.tensor(starts, dtype=torch.int32, device=dev),
+                       torch.tensor(lens, dtype=torch.int32, device=dev),
+                       table.contiguous().to(dev))
+    q = draw_q(tokens, group, dim, 5).to(dev)
+    ws = ffi.workspace(ffi.kv8_attention_workspace_bytes(cache, bad, tokens, group), dev)
+    ffi.kv8_attention(q, cache, bad, 0.1, ws=ws)
+    assert ffi.kv8_batch_status(bad) == RANGE
+    assert ffi.nvfp4_workspace_status(ws) == 0
+    # the same sizes in order: T / sequences tokens each, and one sequence with all of them
+    for batch in (ffi.Kv8Batch(
+            torch.tensor([tokens * b // sequences for b in range(sequences + 1)], dtype=torch.int32,
+                         device=dev), bad.kv_len, bad.page_table),
+                  ffi.Kv8Batch(torch.tensor([0, tokens], dtype=torch.int32, device=dev),
+                               bad.kv_len[36:37].contiguous(), bad.page_table[36:37].contiguous())):
+        fresh = ffi.workspace(ffi.kv8_attention_workspace_bytes(cache, batch, tokens, group), dev)
+        want = ffi.kv8_attention(q, cache, batch, 0.1, ws=fresh)
+        if fresh.numel() <= ws.numel():
+            for _ in range(2):
+                assert torch.equal(ffi.kv8_attention(q, cache, batch, 0.1, ws=ws), want)
+        assert ffi.kv8_batch_status(batch) == 0
