@@ -18,7 +18,10 @@ extern "C" {
  * runs with a producer that issues no weight copies, and with its bounded
  * waits limited to wait_limit_ns (1000 .. 1e9 ns, else NVFP4_ERR_RANGE): each
  * consumer's first wait runs out, the kernel sets its device status word and
- * returns, and the call's outputs are left unwritten.  The kernel still ends
+ * returns, and the call's outputs are left unwritten.  kv8_attention with more
+ * than 32 rows (new tokens times query heads per kv head) per sequence on
+ * average, and heads of at most 128 values, copies half of a block's pages and
+ * then none, and leaves wrong outputs.  The kernel still ends
  * every wait and leaves no copy in flight.  enable == 0 restores normal
  * operation (1 s limit).  Not synchronised with launches on other threads.
  */

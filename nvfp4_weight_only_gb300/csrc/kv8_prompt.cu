@@ -31,7 +31,8 @@
 // Blocks that share a unit leave partial states, which a second kernel joins
 // in the order of their ranges (its blocks read 16 bytes of many rows at once; joined
 // by the last block of a unit instead, one SM would read all of its parts).  Every
-// wait is bounded.
+// wait is bounded; when one runs out the block's others end too, then the copies and
+// products under way (again with a limit), and the status word says so.
 //
 // Measured, 64 tokens of 64 heads over 32805 keys: 87 us, 793 Tflop/s.  A key tile
 // takes 4580 cycles, of which the products need 2160 (512 each for S, 560 for PV) and
@@ -40,6 +41,7 @@
 // TMEM holds no third row tile or second S to fill those waits with.
 #include <atomic>
 
+#include "internal.h"
 #include "kv8_schedule.cuh"
 
 namespace nvf {
@@ -302,11 +304,21 @@ struct Barriers {
     uint64_t scales_full[4];             // page scales of 4 key tiles in turn
     // of row tile w: scores, P in their place, O with it added
     uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t drained;      // after a wait that ran out: all products issued
+};
+
+// Where the kernel leaves its notes for the join and its status, and how long a wait
+// may take.  stall (testing only): the copies stop behind half of a segment's tiles.
+struct PromptRun {
+    JoinNote* notes;
+    int* status;
+    unsigned long long wait_ns;
+    int stall;
 };
 
 template <int kDim, bool kFew>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    kv8_prompt_kernel(const AttentionArgs a, JoinNote* const notes, int* const status) {
+    kv8_prompt_kernel(const AttentionArgs a, const PromptRun run) {
     using S = PromptShape<kDim>;
     extern __shared__ __align__(1024) uint8_t dynamic[];
     // the swizzle goes by address: tiles begin on multiples of 1024
@@ -348,6 +360,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(smem_addr(&bars.raw_empty[i]), kConvertWarps);
             nan_tile[i] = -1;
         }
+        mbar_init(smem_addr(&bars.drained), 1);
         abort = 0;
         fence_mbar_init();
     }
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const bool some = scheduler.start();
         if (lane == 0) {
             work = some;
-            notes[blockIdx.x].parts = 0;
+            run.notes[blockIdx.x].parts = 0;
         }
     }
     tmem_fence_before();
@@ -368,9 +381,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // Waits for a barrier's completion number `uses` (from 0); false, with the
     // status set, when it does not come in time.
     auto wait_lane = [&](uint64_t& bar, unsigned uses) {
-        if (mbar_wait_bounded(smem_addr(&bar), uses & 1, &abort)) return true;
+        if (mbar_wait_bounded(smem_addr(&bar), uses & 1, &abort, run.wait_ns)) return true;
         abort = 1;
-        *status = kKv8Timeout;
+        *run.status = kKv8Timeout;
         return false;
     };
     auto wait = [&](uint64_t& bar, unsigned uses) {  // the same answer for a whole warp
@@ -380,6 +393,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // of the segments before this one: key tiles, and those of the two row tiles
     // (a unit may lack the second)
     unsigned done = 0, row_done[2] = {0, 0};
+    unsigned copied[2] = {0, 0};  // copying warp: tiles of K, of V whose copies were started
     for (int number = 0; work; ++number) {
         const Segment& g = segments[number % 3];
         const int n = g.x1 - g.x0;
@@ -545,6 +559,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     mbar_arrive(smem_addr(&bars.p_full[w]));
                 }
                 ok = ok && wait(bars.o_full[w], before + n - 1);
+                tmem_wait_store();  // where the loop was left early
                 // in the place that the partner has read two tiles ago
                 float* const here = maxima + ((done + n) & 1) * 2 * kPromptRows;
                 here[h * kPromptRows] = sum;
@@ -709,7 +724,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             int page = find_page(g.x0), next = find_page(g.x0 + 1);
             float ks = scale_of(a.c.k_scales, page), vs = scale_of(a.c.v_scales, page);
             bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
+            const int tiles_to_copy = run.stall ? n / 2 : n;
+            for (int i = 0; i < tiles_to_copy && ok; ++i) {
                 const unsigned at = done + i;
                 const int x = g.x0 + i;
                 const bool have = exists(page);
@@ -744,6 +760,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     const uint32_t bar = smem_addr(&bars.raw_full[which]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    copied[which] = at + 1;
                     __syncwarp();
                     if (have)
                         bulk_copy_g2s(smem + S::kRawAt + which * S::kRawBytes + lane * 16 * kDim,
@@ -754,7 +771,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 ks = ks1;
                 vs = vs1;
             }
-            if (!ok) __nanosleep(100000);  // copies under way end before their memory is left
         } else if (lane == 0) {
             // ---- the products.  One thread issues both row tiles' in turn: issued by
             // two, they would share the tensor cores evenly and end together, and both
@@ -813,16 +829,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     scores(w, item + 1);
                 }
             }
-            if (!ok) {
-                // products under way end before the memory they use is given back
-                mma_commit(smem_addr(&bars.q_full));
-                __nanosleep(100000);
-            }
         }
         __syncwarp();
         if (warp == kIssueWarp) {
             if (lane == 0 && g.parts > 1 && g.counter == blockIdx.x)
-                notes[blockIdx.x] =
+                run.notes[blockIdx.x] =
                     JoinNote{g.parts, g.q0, g.len, g.head, g.r, g.slot0, g.slot1, 0};
             if (!last) scheduler.next();
         }
@@ -833,6 +844,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncthreads();
         tmem_fence_after();
         if (last || abort) break;
+    }
+    if (abort) {
+        // Copies and products under way end before the memory that they use is left:
+        // by the threads that started them, whose waits heed no other's.
+        const int none = 0;
+        if (warp == kCopyWarp && lane == 0)
+            for (int i = 0; i < 2; ++i)
+                if (copied[i] > 0)
+                    mbar_wait_bounded(smem_addr(&bars.raw_full[i]), (copied[i] - 1) & 1, &none);
+        if (warp == kIssueWarp && lane == 0) {
+            mma_commit(smem_addr(&bars.drained));
+            mbar_wait_bounded(smem_addr(&bars.drained), 0, &none);
+        }
     }
     __syncthreads();
     if (warp == 0)
@@ -886,8 +910,7 @@ __global__ void __launch_bounds__(kPromptRows) kv8_prompt_join_kernel(const Atte
 }
 
 template <int kDim, bool kFew>
-cudaError_t launch(const AttentionArgs& a, JoinNote* notes, int* status, int num_sms,
-                   cudaStream_t s) {
+cudaError_t launch(const AttentionArgs& a, const PromptRun& run, int num_sms, cudaStream_t s) {
     using S = PromptShape<kDim>;
     static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
     int dev = 0;
@@ -910,12 +933,13 @@ cudaError_t launch(const AttentionArgs& a, JoinNote* notes, int* status, int num
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<kDim, kFew>, a, notes, status);
+    e = cudaLaunchKernelEx(&cfg, kv8_prompt_kernel<kDim, kFew>, a, run);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(num_sms, kDim / kJoinValues);
     cfg.blockDim = dim3(kPromptRows);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv8_prompt_join_kernel<kDim>, a, (const JoinNote*)notes);
+    return cudaLaunchKernelEx(&cfg, kv8_prompt_join_kernel<kDim>, a,
+                              (const JoinNote*)run.notes);
 }
 
 }  // namespace
@@ -931,7 +955,7 @@ size_t kv8_prompt_data_bytes(int head_dim, int num_sms) {
 
 cudaError_t launch_kv8_prompt(AttentionArgs a, void* data, int* status, int num_sms,
                               cudaStream_t s) {
-    JoinNote* const notes = reinterpret_cast<JoinNote*>(data);
+    const PromptRun run{reinterpret_cast<JoinNote*>(data), status, test_wait_ns(), test_stall()};
     a.partials = reinterpret_cast<float*>(reinterpret_cast<char*>(data) +
                                           ((size_t)num_sms * sizeof(JoinNote) + 255) / 256 * 256);
     // equal parts, as in kv8_attention.cu (one prompt of 512 tokens, 32 heads on 8: 24.5 us
@@ -939,10 +963,10 @@ cudaError_t launch_kv8_prompt(AttentionArgs a, void* data, int* status, int num_
     const long long rows = (long long)a.bt.tokens * a.group;
     const bool few = (rows / kPromptRows + a.bt.batch) * a.c.kv_heads <= num_sms / 2;
     if (a.c.head_dim == 64)
-        return few ? launch<64, true>(a, notes, status, num_sms, s)
-                   : launch<64, false>(a, notes, status, num_sms, s);
-    return few ? launch<128, true>(a, notes, status, num_sms, s)
-               : launch<128, false>(a, notes, status, num_sms, s);
+        return few ? launch<64, true>(a, run, num_sms, s)
+                   : launch<64, false>(a, run, num_sms, s);
+    return few ? launch<128, true>(a, run, num_sms, s)
+               : launch<128, false>(a, run, num_sms, s);
 }
 
 }  // namespace nvf
