@@ -457,7 +457,9 @@ typedef struct {
  * check them: a page outside the cache, a length beyond the table, decreasing
  * or too large q_start, n > kv_len or a position beyond the rotation table
  * reads and writes nothing outside the buffers (what it concerns is left out:
- * not written, or masked) and sets the status word.
+ * not written, or masked) and sets the status word.  Where a decreasing q_start
+ * gives rows to several sequences, any of them may have written a row, and
+ * kv8_attention may leave out the whole batch.
  */
 typedef struct {
     const int* q_start;    /* (device) [batch + 1], from 0, not decreasing */
