@@ -527,11 +527,14 @@ size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* ba
  *   lse (device, out) fp32 [tokens, heads], or NULL;
  *   ws (device) >= kv8_attention_workspace_bytes.
  * A query that sees nothing gets 0 and -infinity.  Masked keys and values do
- * not enter the result, whatever they hold.  Scores, maxima and sums are fp32.
+ * not enter the result, whatever they hold.  Scores, maxima and sums are fp32;
+ * softmax_j v_scale_j is rounded to 11 bits before it multiplies v's codes, and
+ * lost from out (not from lse) below 2^-30 of the largest one of its row.
  * heads a multiple of kv_heads, tokens * heads / kv_heads at most 2^30;
- * window, sinks >= 0 (sinks without a window have no effect).  Within a
- * sequence the pages' v_scales may differ by up to 2^100 (a smaller one's
- * weights may be lost beyond that).
+ * window, sinks >= 0 (sinks without a window have no effect).  v_scales below
+ * 2^-80 or above 2^126 count as these; those of one sequence's visible keys may
+ * differ by up to 2^100 (beyond that a page with the smaller one may be lost from
+ * lse too).
  * A kernel that waited for itself longer than its limit leaves wrong outputs and
  * NVFP4_ERR_TIMEOUT for nvfp4_workspace_status on ws.
  */

@@ -452,7 +452,7 @@ public:
         const bool page_ok = vs > 0.0f;  // copied as 0 without a page
         const bool guard = !page_ok || j0 + kTile > keys.hi_min ||
                            (j0 < keys.lo_max && j0 + kTile > a.sinks);
-        vs = fmaxf(vs, 1.17549435e-38f);
+        vs = usable_scale(vs);
         float s[kNT][4];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)

@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (!ok) break;
                     if (which == 0) {
                         if (lane < kGroups) {
-                            const float v = fmaxf(vs, 1.17549435e-38f);
+                            const float v = usable_scale(vs);
                             reinterpret_cast<float4*>(shared +
                                                       S::kScalesAt)[(at & 3) * kGroups + lane] =
                                 have ? make_float4(ks, __log2f(v), __fdividef(1.0f, v), 0.0f)

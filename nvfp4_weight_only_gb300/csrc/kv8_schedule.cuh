@@ -137,6 +137,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// Value scales as the softmax takes them.  The denominator is a sum of P / v_scale, P up
+// to 2^14, over fewer than 2^31 keys: finite down to 2^-83; and the fast reciprocal of
+// a number above 2^126 is 0.
+__device__ __forceinline__ float usable_scale(float vs) {
+    return fminf(fmaxf(vs, 0x1p-80f), 0x1p126f);
+}
+
 __device__ __forceinline__ float weight_of(float top, float all) {
     return all == -INFINITY ? 0.0f : exp2_fast(top - all);
 }
