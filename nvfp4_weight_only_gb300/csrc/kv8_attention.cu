@@ -343,7 +343,7 @@ public:
     __device__ __forceinline__ bool sees(int nt, int e, int j, bool page_ok) const {
         const int i = token_of(a, seg->r * S::kRows + nt * 8 + 2 * c + e);
         const int hi = seg->first + i + 1;
-        const int lo = a.window > 0 ? hi - a.window : 0;
+        const int lo = window_start(a, hi);
         return page_ok && i < seg->len && j < hi && (j >= lo || j < a.sinks);
     }
 
@@ -895,7 +895,7 @@ cudaError_t launch_kv8_attention(const void* q, long long q_stride, int heads,
     a.group = heads / c.kv_heads;
     a.group_inverse = a.group == 1 ? 0xffffffffu : (unsigned)((1ull << 32) / a.group);
     a.scale = softmax_scale * 1.4426950408889634f;
-    a.window = window;
+    a.window = window > 0 ? window : 0x7fffffff;
     a.sinks = sinks;
     if (kv8_prompt_applies(c.head_dim, bt.tokens, a.group, bt.batch))
         return launch_kv8_prompt(a, partials, status, num_sms, s);

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const int unit_row = g.r * kPromptRows + row;
                 const int token = token_of(a, unit_row);
                 const int hi = token < g.len ? g.first + token + 1 : 0;
-                const int lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+                const int lo = window_start(a, hi);
                 const float row_scale =
                     reinterpret_cast<const float*>(shared + S::kRowScaleAt)[row];
                 const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);

@@ -23,7 +23,7 @@ struct AttentionArgs {
     int heads, group;
     unsigned group_inverse;  // floor(2^32 / group), at most 2^32 - 1
     float scale;  // softmax_scale * log2(e)
-    int window, sinks;
+    int window, sinks;  // window 2^31 - 1: every key
 };
 
 // row / group: the product with the inverse is the quotient or one less.
@@ -60,6 +60,12 @@ struct Keys {
     int sink_tiles, tiles;
 };
 
+// The first key in the window of a query that sees keys below hi (negative for a token
+// without a position: as low as -2^30).
+__device__ __forceinline__ int window_start(const AttentionArgs& a, int hi) {
+    return hi > a.window ? hi - a.window : 0;
+}
+
 template <typename T>
 __device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int len, int r) {
     constexpr int kRows = T::kRows, kTile = T::kTile;
@@ -68,8 +74,8 @@ __device__ __forceinline__ Keys unit_keys(const AttentionArgs& a, int first, int
     const int i1 = min(token_of(a, r * kRows + kRows - 1), len - 1);
     k.hi_min = first + i0 + 1;
     k.hi = first + i1 + 1;
-    k.lo = a.window > 0 ? max(k.hi_min - a.window, 0) : 0;
-    k.lo_max = a.window > 0 ? max(k.hi - a.window, 0) : 0;
+    k.lo = window_start(a, k.hi_min);
+    k.lo_max = window_start(a, k.hi);
     const int lo_tile = k.lo / kTile;
     k.sink_tiles = min((min(a.sinks, k.lo) + kTile - 1) / kTile, lo_tile);
     // a tile that holds no key writes the empty result

@@ -61,3 +61,22 @@ def test_overlapping_sequences_leave_the_workspace_whole(dev, dim, sequences, to
             for _ in range(2):
                 assert torch.equal(ffi.kv8_attention(q, cache, batch, 0.1, ws=ws), want)
         assert ffi.kv8_batch_status(batch) == 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,group", [([7, 1], [2, 50], 1), ([40, 1], [10, 50], 2)])
+def test_a_window_of_any_size_beside_missing_positions(dev, q_lens, kv_lens, group):
+    """More new tokens than the length, by more than one, under the largest windows, few rows and
+    many: the tokens that have a position, and the other sequence, get their results."""
+    s = Setup(dev, q_lens, kv_lens, 2, 64, 16)
+    q = draw_q(s.tokens, 2 * group, 64, 2)
+    none = q_lens[0] - kv_lens[0]
+    want, want_lse = run_attention(s, q, 0.1)
+    assert ffi.kv8_batch_status(s.batch) == RANGE
+    assert bool((want[:none] == 0).all()) and bool((want_lse[:none] == -math.inf).all())
+    assert bool(torch.isfinite(want_lse[none:]).all())
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30):
+        out = torch.full_like(want, 7.0)
+        lse = torch.full_like(want_lse, 7.0)
+        ffi.kv8_attention(q.to(dev), s.cache, s.batch, 0.1, window, 3, out=out, lse=lse)
+        assert ffi.kv8_batch_status(s.batch) == RANGE
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
