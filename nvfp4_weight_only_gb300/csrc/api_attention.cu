@@ -172,7 +172,7 @@ nvfp4_status kv8_append(const kv8_cache* cache, const kv8_batch* batch, int toke
             overlap(q_out, n, v, reach(tokens, v_stride, kw)))
             return NVFP4_ERR_ALIAS;
     }
-    nvf::RopeArgs r{rope, 0, 0, interleaved ? 1 : 0};
+    nvf::RopeArgs r{rope, 0x7fffffff, 0, interleaved ? 1 : 0};
     if (rope) {
         if (rope_positions < 1 || rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > dim)
             return NVFP4_ERR_SHAPE;

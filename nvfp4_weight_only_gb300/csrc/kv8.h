@@ -41,7 +41,8 @@ inline long long kv8_max_runs(long long tokens, long long batch, int page_shift)
 
 struct RopeArgs {
     const float* table;  // [positions][rot / 2][2] (cos, sin), or null
-    int positions, rot;  // rot a multiple of 16, 0 without a table
+    int positions;       // 2^31 - 1 without a table
+    int rot;             // a multiple of 16, 0 without a table
     int interleaved;
 };
 

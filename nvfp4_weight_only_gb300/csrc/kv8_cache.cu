@@ -161,10 +161,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
     return f32x4_to_e4m3x4(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
 }
 
-__device__ __forceinline__ int rope_position(const AppendArgs& a, int position) {
-    if (a.rope.rot == 0 || position < a.rope.positions) return position;
-    kv8_report(a.bt);
-    return a.rope.positions - 1;
+// Finds the x-th run, without the tokens behind the rotation table (reported, and not
+// written); false when nothing is left.
+__device__ __forceinline__ bool find_run(const AppendArgs& a, int x, Kv8Run& r) {
+    if (!kv8_find_run(a.bt, x, r)) return false;
+    const int left = a.rope.positions - r.position;
+    if (left < r.rows) {
+        kv8_report(a.bt);
+        if (left <= 0) return false;
+        r.rows = left;
+    }
+    return true;
 }
 
 constexpr int kHeld = 2;  // items of a thread that stay in registers
@@ -222,7 +229,7 @@ __device__ __forceinline__ void store_run(const AppendArgs& a, const Kv8Run& r, 
     auto turned = [&](const Raw& raw, int row, float (&p)[8], float (&q)[8]) {
         Turn t;
         if (kTurn && (slot.turn_a || slot.turn_b))
-            t = load_turn(rope, rope_position(a, r.position + row), slot);
+            t = load_turn(rope, r.position + row, slot);
         values(rope, raw, slot, t, p, q);
     };
     float top = 0.0f;
@@ -339,7 +346,11 @@ __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
     } else {
         kv8_report(a.bt);
     }
-    position = rope_position(a, max(position, 0));
+    position = max(position, 0);
+    if (position >= a.rope.positions) {
+        kv8_report(a.bt);
+        return;
+    }
     Turn turn;
     if (slot.turn_a || slot.turn_b) turn = load_turn(a.rope, position, slot);
 #pragma unroll 1
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         const int x = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
         const int run = x / per_run, part = x - run * per_run;
         Kv8Run r;
-        if (run >= a.runs || !kv8_find_run(a.bt, run, r)) return;
+        if (run >= a.runs || !find_run(a, run, r)) return;
         const bool is_k = part < a.c.kv_heads;
         const int head = is_k ? part : part - a.c.kv_heads;
         if (is_k) {
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv8_append_rows_kernel(cons
     const int x = blockIdx.x - q_before;
     const int run = x / a.c.kv_heads, head = x - run * a.c.kv_heads;
     Kv8Run r;
-    if (!kv8_find_run(a.bt, run, r)) return;
+    if (!find_run(a, run, r)) return;
     const RunPart<true, kAppendThreads> k(a, r, head);
     const RunPart<false, kAppendThreads> v(a, r, head);
     const int page = kv8_page(a.bt, a.c, r.b, r.page_index);

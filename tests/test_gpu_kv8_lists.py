@@ -80,3 +80,52 @@ def test_a_window_of_any_size_beside_missing_positions(dev, q_lens, kv_lens, gro
         ffi.kv8_attention(q.to(dev), s.cache, s.batch, 0.1, window, 3, out=out, lse=lse)
         assert ffi.kv8_batch_status(s.batch) == RANGE
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim,inter", [
+    ([1, 1], [8, 9], 4, 2, 64, False),         # the second token just behind the table
+    ([3, 2], [10, 3], 6, 1, 128, True),        # a run that crosses the table's end
+    ([40, 1], [60, 5], 4, 2, 128, False),      # a prompt, of which 8 rows stay
+])
+def test_positions_behind_the_rotation_table_are_not_written(dev, q_lens, kv_lens, heads, kv_heads,
+                                                             dim, inter):
+    positions = 28 if max(q_lens) > 16 else 8
+    page = 16
+    s = Setup(dev, q_lens, kv_lens, kv_heads, dim, page, seed=41)
+    t = sum(q_lens)
+    x = torch.randn((t, heads + 2 * kv_heads, dim), generator=torch.Generator().manual_seed(6))
+    x = x.bfloat16().to(dev)
+    q, k, v = x.split((heads, kv_heads, kv_heads), 1)
+    rope = ffi.rope_table(positions, dim, 10000.0, dev)
+    q_out = torch.full((t, heads, dim), 7.0, dtype=torch.bfloat16, device=dev)
+    before = [c.clone() for c in (s.cache.k_codes, s.cache.v_codes)]
+    scales = [c.clone() for c in (s.cache.k_scales, s.cache.v_scales)]
+    ffi.kv8_append(s.cache, s.batch, k, v, q=q, q_out=q_out, rope=rope, interleaved=inter)
+    assert ffi.kv8_batch_status(s.batch) == RANGE
+    # the same with a table that holds every position, and only the tokens that the short one holds
+    kept = [i for i in range(t)]
+    at, n_lens, m_lens = 0, [], []
+    keep = []
+    for n, kv in zip(q_lens, kv_lens):
+        some = [i for i in range(n) if kv - n + i < positions]
+        keep += [at + i for i in some]
+        n_lens.append(len(some))
+        m_lens.append(kv - n + len(some))
+        at += n
+    assert 0 < len(keep) < len(kept)
+    o = Setup(dev, q_lens, kv_lens, kv_heads, dim, page, seed=41)
+    starts = [sum(n_lens[:b]) for b in range(len(n_lens) + 1)]
+    batch = ffi.Kv8Batch(torch.tensor(starts, dtype=torch.int32, device=dev),
+                         torch.tensor(m_lens, dtype=torch.int32, device=dev), o.batch.page_table)
+    some = x[keep]
+    want_q = ffi.kv8_append(o.cache, batch, some[:, heads:heads + kv_heads],
+                            some[:, heads + kv_heads:], q=some[:, :heads],
+                            rope=ffi.rope_table(100, dim, 10000.0, dev), interleaved=inter)
+    assert ffi.kv8_batch_status(batch) == 0
+    for a, b in ((s.cache.k_codes, o.cache.k_codes), (s.cache.v_codes, o.cache.v_codes)):
+        assert torch.equal(a, b)
+    for a, b in ((s.cache.k_scales, o.cache.k_scales), (s.cache.v_scales, o.cache.v_scales)):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+    assert torch.equal(q_out[keep], want_q)
+    left = [i for i in kept if i not in keep]
+    assert bool((q_out[left] == 7).all())
