@@ -452,7 +452,9 @@ typedef struct {
  * q_start[b+1] - 1 of the call's rows belong to sequence b and take the last
  * positions of its kv_len[b]: with n of them, the i-th has position
  * kv_len[b] - n + i.  Position p lies in page page_table[b][p / page], row
- * p % page.  n may be 0 (the sequence takes no part).
+ * p % page.  n may be 0 (the sequence takes no part).  Rows in front of q_start[0]
+ * and from q_start[batch] on belong to no sequence: nothing is written or
+ * reported for them, so a captured call may have rows to spare.
  * The lists live on the device and are not read by the host.  The kernels
  * check them: a page outside the cache, a length beyond the table, decreasing
  * or too large q_start, n > kv_len or a position beyond the rotation table

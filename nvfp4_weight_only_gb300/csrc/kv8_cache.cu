@@ -318,7 +318,8 @@ __device__ __forceinline__ void store_run(const AppendArgs& a, const Kv8Run& r, 
     if (mate == 0) *scales = scale;  // read by all before the maxima were joined
 }
 
-// Rotates q of one token (or copies it without a table), by one warp.  The first
+// Rotates q of one token that has a position (or copies it without a table), by one
+// warp.  The first
 // heads are on their way while the token's position is looked up.
 template <int kAhead>
 __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
@@ -338,15 +339,11 @@ __device__ __forceinline__ void turn_q(const AppendArgs& a, int t) {
     };
     load(head0);
     const int b = kv8_owner(a.bt, t);
-    int position = 0;
-    if (b < a.bt.batch) {
-        const Kv8Seq s = kv8_seq(a.bt, b);
-        position = s.kv - s.len + (t - s.q0);
-        if (s.bad) kv8_report(a.bt);
-    } else {
-        kv8_report(a.bt);
-    }
-    position = max(position, 0);
+    if (b >= a.bt.batch) return;  // the token belongs to no sequence
+    const Kv8Seq s = kv8_seq(a.bt, b);
+    if (s.bad) kv8_report(a.bt);
+    const int i = t - s.q0, position = s.kv - s.len + i;
+    if (i < 0 || i >= s.len || position < 0) return;
     if (position >= a.rope.positions) {
         kv8_report(a.bt);
         return;

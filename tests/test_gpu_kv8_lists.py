@@ -129,3 +129,34 @@ def test_positions_behind_the_rotation_table_are_not_written(dev, q_lens, kv_len
     assert torch.equal(q_out[keep], want_q)
     left = [i for i in kept if i not in keep]
     assert bool((q_out[left] == 7).all())
+
+
+def test_rows_of_no_sequence_take_no_part(dev):
+    """A call of a fixed number of rows (a captured step, say) of which the last belong to nobody:
+    no call computes or reports anything for them."""
+    s = Setup(dev, [2, 1], [30, 9], 2, 64, 16, seed=43)
+    x = torch.randn((6, 4 + 4, 64), generator=torch.Generator().manual_seed(9)).bfloat16().to(dev)
+    rope = ffi.rope_table(40, 64, 10000.0, dev)
+    q_out = torch.full((6, 4, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    out = torch.full((6, 4, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    ffi.kv8_append(s.cache, s.batch, x[:, 4:6], x[:, 6:], q=x[:, :4], q_out=q_out, rope=rope)
+    ffi.kv8_attention(q_out, s.cache, s.batch, 0.1, out=out)
+    k, v = [torch.full((6, 2, 64), 7.0, dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    ffi.kv8_read(s.cache, s.batch, k, v)
+    assert ffi.kv8_batch_status(s.batch) == 0
+    for t in (q_out, out, k, v):
+        assert bool((t[3:] == 7).all()) and not bool((t[:3] == 7).all(-1).any())
+
+
+def test_tokens_in_front_of_position_0_keep_their_q(dev):
+    """More new tokens than the length: rotated q is written for those that have a position."""
+    s = Setup(dev, [4], [2], 1, 64, 16, seed=44)
+    x = torch.randn((4, 4, 64), generator=torch.Generator().manual_seed(9)).bfloat16().to(dev)
+    rope = ffi.rope_table(40, 64, 10000.0, dev)
+    q_out = torch.full((4, 2, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    ffi.kv8_append(s.cache, s.batch, x[:, 2:3], x[:, 3:], q=x[:, :2], q_out=q_out, rope=rope)
+    assert ffi.kv8_batch_status(s.batch) == RANGE
+    assert bool((q_out[:2] == 7).all())
+    only = Setup(dev, [2], [2], 1, 64, 16, seed=44)
+    want = ffi.kv8_append(only.cache, only.batch, x[2:, 2:3], x[2:, 3:], q=x[2:, :2], rope=rope)
+    assert torch.equal(q_out[2:], want)
