@@ -404,8 +404,8 @@ nvfp4_status add_rmsnorm_bf16(const void* x, const void* residual, const void* w
 /*
  * The same norm into 8 bits: for each row and group of 128 columns (the last
  * one may be shorter) scale = max(amax|y| / 448, 2^-126), or 1 when amax is 0,
- * and code = E4M3(y / scale), to nearest even, saturated, NaN kept (the
- * quotient is off by at most 2^-22 of itself before it is rounded).
+ * and code = E4M3(y / scale), to nearest even, saturated, NaN kept (of the
+ * quotient rounded to fp32).
  *   codes (device, out) u8 [M, H];  scales (device, out) fp32 [M, ceil(H/128)].
  * Neither overlaps another buffer.
  */

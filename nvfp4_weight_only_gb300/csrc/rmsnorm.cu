@@ -3,16 +3,15 @@
 //   y = r * (mean(r^2) + eps)^(-1/2) * (weight + weight_bias)
 // stored as bf16(y), or as E4M3 codes with one fp32 scale per row and 128
 // columns: scale = max(amax / 448, 2^-126) (1 for a group of zeros),
-// code = e4m3(y / scale), which saturates and keeps NaN (the quotient is off by
-// at most 2^-22 of itself).
+// code = e4m3(y / scale), the quotient rounded to fp32, which saturates and keeps NaN.
 //
 // One block per row; a thread holds its 8-column vectors of r in registers
 // between the sum of squares and the output, so x and the residual are read
 // once.  The sum, the norm and y stay in fp32 (the residual stream's rounding
 // to bf16 does not enter the norm).
 //
-// Memory bounds many rows (4096 x 5376 with residual, into E4M3: 25 us for 155 MB,
-// 6.2 TB/s; the block's sum is a wait that other blocks of the SM have to fill),
+// Memory bounds many rows (4096 x 5376 with residual, into E4M3: 25.3 us for 155 MB,
+// 6.1 TB/s; the block's sum is a wait that other blocks of the SM have to fill),
 // one row the launch (1.8 us).  Arithmetic on pairs halves its instructions, which
 // took 63% of the issue slots (29.5 us before).
 #include "kv8.cuh"
@@ -124,11 +123,18 @@ __global__ void __maxnreg__(kVecs == 1 ? 32 : kVecs == 2 ? 40 : 64) add_rmsnorm_
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float scale = top == 0.0f ? 1.0f : fmaxf(__fdiv_rn(top, 448.0f), 1.17549435e-38f);
         if (live) {
-            // y / scale through the reciprocal: off by at most 2^-22 of itself
-            const float by = __frcp_rn(scale);
+            // y / scale, rounded once, through the reciprocal as a sum of two floats: by,
+            // not above it, and rest = (1 - scale * by) * by, which is exact to 2^-24 of
+            // itself, so that y * by + y * rest is off by 2^-47 of the quotient before its
+            // one rounding.  (rest is not negative: a zero keeps its sign.)  With by alone,
+            // rounded to nearest, codes beside a tie fall to the wrong side (4096 x 5376:
+            // 25.0 us against 25.3; 29.2 with a division per value).
+            const float by = __frcp_rd(scale);
+            const float rest = by == 0.0f ? 0.0f : __fmaf_rn(-scale, by, 1.0f) * by;
             float2 q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = unpair(mul2(y[e], pair(by, by)));
+            for (int e = 0; e < 4; ++e)
+                q[e] = unpair(fma2(y[e], pair(by, by), mul2(y[e], pair(rest, rest))));
             a.codes[row * a.vecs + c] =
                 make_uint2(f32x4_to_e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y),
                            f32x4_to_e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
