@@ -511,8 +511,9 @@ nvfp4_status kv8_append(const kv8_cache* cache, const kv8_batch* batch, int toke
 nvfp4_status kv8_read(const kv8_cache* cache, const kv8_batch* batch, int tokens, void* k_out,
                       void* v_out, cudaStream_t stream);
 
-/* Workspace bytes for kv8_attention on the current device (0 for invalid
- * arguments); contract as for nvfp4_gemv (zero-fill once, calls sharing one
+/* Workspace bytes for kv8_attention on the current device, from the sizes alone
+ * (the descriptions' pointers may be NULL), 0 for sizes that the call refuses;
+ * contract as for nvfp4_gemv (zero-fill once, calls sharing one
  * ordered). */
 size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* batch, int tokens,
                                      int heads);

@@ -29,26 +29,44 @@ size_t reach(int T, long long stride, size_t width) {
     return ((size_t)(T - 1) * (size_t)stride + width) * 2;
 }
 
-nvfp4_status check_cache(const kv8_cache* c) {
-    if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return NVFP4_ERR_NULL;
+nvfp4_status check_cache_sizes(const kv8_cache* c) {
     if (c->pages < 1 || c->kv_heads < 1) return NVFP4_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_SHAPE;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+nvfp4_status check_cache(const kv8_cache* c) {
+    if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return NVFP4_ERR_NULL;
+    const nvfp4_status e = check_cache_sizes(c);
+    if (e != NVFP4_OK) return e;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) ||
         !aligned(c->v_scales, 4))
         return NVFP4_ERR_ALIGN;
     return NVFP4_OK;
 }
 
-nvfp4_status check_batch(const kv8_batch* b, const kv8_cache* c, int tokens) {
-    if (!b || !b->q_start || !b->kv_len || !b->page_table) return NVFP4_ERR_NULL;
+nvfp4_status check_batch_sizes(const kv8_batch* b, const kv8_cache* c, int tokens) {
     if (b->batch < 1 || b->batch > nvf::kKv8MaxBatch || tokens < 1) return NVFP4_ERR_RANGE;
     if (b->table_width < 1 || (long long)b->table_width * c->page > 0x7fffff00LL)
         return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+nvfp4_status check_batch(const kv8_batch* b, const kv8_cache* c, int tokens) {
+    if (!b || !b->q_start || !b->kv_len || !b->page_table) return NVFP4_ERR_NULL;
+    const nvfp4_status e = check_batch_sizes(b, c, tokens);
+    if (e != NVFP4_OK) return e;
     if (!aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->page_table, 4) ||
         !aligned(b->status, 4))
         return NVFP4_ERR_ALIGN;
     return NVFP4_OK;
+}
+
+// Query heads of the call: a multiple of the cache's, and rows that the kernels count.
+nvfp4_status check_heads(const kv8_cache* c, int tokens, int heads) {
+    if (heads < 1 || heads % c->kv_heads != 0) return NVFP4_ERR_SHAPE;
+    return (long long)tokens * (heads / c->kv_heads) > (1LL << 30) ? NVFP4_ERR_RANGE : NVFP4_OK;
 }
 
 nvf::Kv8CacheArgs cache_args(const kv8_cache* c) {
@@ -200,8 +218,9 @@ nvfp4_status kv8_read(const kv8_cache* cache, const kv8_batch* batch, int tokens
 
 size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* batch, int tokens,
                                      int heads) {
-    if (!cache || !batch || tokens < 1 || cache->kv_heads < 1 || heads < cache->kv_heads ||
-        batch->batch < 1)
+    if (!cache || !batch || check_cache_sizes(cache) != NVFP4_OK ||
+        check_batch_sizes(batch, cache, tokens) != NVFP4_OK ||
+        check_heads(cache, tokens, heads) != NVFP4_OK)
         return 0;
     const int sms = nvf::device_sm_count();
     return nvf::kDataOffset +
@@ -218,9 +237,9 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
     if (e != NVFP4_OK) return e;
     if (!q || !out || !ws) return NVFP4_ERR_NULL;
     const int dim = cache->head_dim;
-    if (heads < 1 || heads % cache->kv_heads != 0) return NVFP4_ERR_SHAPE;
+    e = check_heads(cache, tokens, heads);
+    if (e != NVFP4_OK) return e;
     if (window < 0 || sinks < 0 || !std::isfinite(softmax_scale)) return NVFP4_ERR_RANGE;
-    if ((long long)tokens * (heads / cache->kv_heads) > (1LL << 30)) return NVFP4_ERR_RANGE;
     e = check_rows(q, heads, q_stride, dim);
     if (e != NVFP4_OK) return e;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 16)) return NVFP4_ERR_ALIGN;
