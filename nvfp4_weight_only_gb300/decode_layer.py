@@ -57,7 +57,10 @@ class DecodeLayer:
                             L.nvfp4_gemv_workspace_bytes(M, H, heads * head_dim),
                             L.ffn_swiglu_nvfp4_workspace_bytes(M, H, I))
         self.ws = ffi.workspace(self.ws_bytes, dev)
-        self.attention_ws = {}
+        # as much as any step asks for: single tokens of a full batch, or many rows of one sequence
+        self.attention_ws = ffi.workspace(
+            max(ffi.kv8_attention_workspace_size(kv_heads, head_dim, 1024, 1, heads),
+                ffi.kv8_attention_workspace_size(kv_heads, head_dim, 1, M, heads)), dev)
 
     def step(self, x: torch.Tensor, residual: torch.Tensor, cache: ffi.Kv8Cache,
              batch: ffi.Kv8Batch):
@@ -73,21 +76,13 @@ class DecodeLayer:
         q = ffi.kv8_append(cache, batch, k, v, q=q, q_out=self.turned[:M], rope=self.rope,
                            interleaved=self.interleaved)
         a = ffi.kv8_attention(q, cache, batch, self.softmax_scale, window=self.window,
-                              sinks=self.sinks, ws=self._workspace(cache, batch, M),
-                              out=self.attended[:M])
+                              sinks=self.sinks, ws=self.attention_ws, out=self.attended[:M])
         p = ffi.nvfp4_gemv(a.view(M, -1), self.out, s["out"], self.H, ws=self.ws,
                            out=self.projected[:M])
         ffi.add_rmsnorm_bf16(p, self.norm_ffn, self.eps, residual=r, sum_out=r, out=n)
         out = ffi.ffn_swiglu_nvfp4(n, self.gate_up, s["gate"], s["up"], self.down, s["down"], self.I,
                                    self.act, ws=self.ws, out=self.result[:M])
         return out, r
-
-    def _workspace(self, cache, batch, tokens):
-        """The attention's workspace: one per size that its calls ask for, kept."""
-        need = ffi.kv8_attention_workspace_bytes(cache, batch, tokens, self.heads)
-        if need not in self.attention_ws:
-            self.attention_ws[need] = ffi.workspace(need, self.norm_in.device)
-        return self.attention_ws[need]
 
     @classmethod
     def synthetic(cls, H, I, heads, kv_heads, head_dim, device, layer=0, **options):

@@ -666,6 +666,15 @@ def kv8_attention_workspace_bytes(cache: Kv8Cache, batch: Kv8Batch, tokens: int,
     return load().kv8_attention_workspace_bytes(cache.ref, batch.ref, tokens, heads)
 
 
+def kv8_attention_workspace_size(kv_heads: int, head_dim: int, sequences: int, tokens: int,
+                                 heads: int) -> int:
+    """The same from sizes, before there is a cache."""
+    cache = _CacheStruct(pages=1, kv_heads=kv_heads, page=16, head_dim=head_dim)
+    batch = _BatchStruct(batch=sequences, table_width=1)
+    return load().kv8_attention_workspace_bytes(ctypes.addressof(cache), ctypes.addressof(batch),
+                                                tokens, heads)
+
+
 def kv8_attention(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, softmax_scale: float,
                   window: int = 0, sinks: int = 0, ws: torch.Tensor = None,
                   out: torch.Tensor = None, lse: torch.Tensor = None) -> torch.Tensor:
