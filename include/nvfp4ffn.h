@@ -494,7 +494,9 @@ nvfp4_status kv8_batch_status(const kv8_batch* batch, cudaStream_t stream);
  *           tokens of the page, else need
  *   codes = E4M3(value / scale) (nearest even, saturated, NaN kept; NaN does
  *           not enter the maximum); the older rows' codes are re-scaled by
- *           old scale / scale when it changed.
+ *           old scale / scale when it changed.  An old scale that is kept but is
+ *           no power of two (it did not come from this call) takes
+ *           value * fp32(1 / scale).
  * A page that gets new tokens belongs to one sequence of the batch.
  */
 nvfp4_status kv8_append(const kv8_cache* cache, const kv8_batch* batch, int tokens, const void* k,
@@ -531,13 +533,16 @@ size_t kv8_attention_workspace_bytes(const kv8_cache* cache, const kv8_batch* ba
  *   ws (device) >= kv8_attention_workspace_bytes.
  * A query that sees nothing gets 0 and -infinity.  Masked keys and values do
  * not enter the result, whatever they hold.  Scores, maxima and sums are fp32;
- * softmax_j v_scale_j is rounded to 11 bits before it multiplies v's codes, and
- * lost from out (not from lse) below 2^-30 of the largest one of its row.
+ * softmax_j v_scale_j is rounded to 11 bits before it multiplies v's codes; below
+ * 2^-20 of the largest one of its row it has fewer, and below 2^-30 it is lost from
+ * out (not from lse).
  * heads a multiple of kv_heads, tokens * heads / kv_heads at most 2^30;
  * window, sinks >= 0 (sinks without a window have no effect).  v_scales below
  * 2^-80 or above 2^126 count as these; those of one sequence's visible keys may
  * differ by up to 2^100 (beyond that a page with the smaller one may be lost from
- * lse too).
+ * lse too).  A batch of 2^31 or more tiles is left out and reported: a tile is 16
+ * keys by 8 to 32 rows (128 by 256 for many rows of up to 128 values) of one kv
+ * head, as in 131072 new tokens with 16 query heads on each of 8 kv heads of 256.
  * A kernel that waited for itself longer than its limit leaves wrong outputs and
  * NVFP4_ERR_TIMEOUT for nvfp4_workspace_status on ws.
  */

@@ -37,8 +37,10 @@
 // Measured (8 kv heads of 128 unless said): one sequence of 131071 keys, 8 rows per
 // kv head, 49 us for 269 MB (5.4 TB/s; 7.0 while the tiles run, then about 4 us
 // before the first, for lengths, cut and pages, and 5 after the last, for the
-// slowest warp and the join); 32 sequences of 1000 to 16000 keys 64 us for 363 MB
-// (5.6 TB/s); one of 1000 keys 8.4 us, which is those two ends.
+// slowest warp and the join); 32 sequences of 1000 to 16000 keys 66 us for 363 MB
+// (5.5 TB/s); one of 1000 keys 8.2 us, which is those two ends.  From 9 rows on the
+// work per tile of 16 keys, which grows with every 8 rows, shows (8 sequences of 8192
+// keys, 134 MB: 29 us with 8 rows, 45 with 16, 70 with 24 and 32).
 #include <atomic>
 
 #include "kv8_schedule.cuh"

@@ -34,11 +34,13 @@
 // wait is bounded; when one runs out the block's others end too, then the copies and
 // products under way (again with a limit), and the status word says so.
 //
-// Measured, 64 tokens of 64 heads over 32805 keys: 87 us, 793 Tflop/s.  A key tile
-// takes 4580 cycles, of which the products need 2160 (512 each for S, 560 for PV) and
-// 2^t 1350.  The rest is a row tile's own chain, about 1900 cycles of softmax, 420
-// until the products see P, 895 for PV with its completion and 955 for S with its:
-// TMEM holds no third row tile or second S to fill those waits with.
+// Measured, 64 tokens of 64 heads over 32805 keys: 84 us, 822 Tflop/s.  A key tile
+// took 4580 cycles (in calls of 86.4 us), of which the products need 2160 (512 each
+// for S, 560 for PV) and 2^t 1350.  The rest is a row tile's own chain, about 1900
+// cycles of softmax, 420 until the products see P, 895 for PV with its completion and
+// 955 for S with its.  With heads of 128 values TMEM holds no third row tile or second
+// S to fill those waits with; with 64, columns 384..511 are idle.  Up to 128 rows there
+// is one row tile, with nothing beside its chain.
 #include <atomic>
 
 #include "internal.h"
@@ -58,16 +60,16 @@ constexpr int kPromptThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 constexpr int kGroups = kPromptKeys / 16;  // page scales per tile
 // Rows per sequence and kv head, on average, up to which one pass of
 // kv8_attention.cu holds them and is the faster (8 sequences of 8192 keys, 8 kv
-// heads of 128: 32 rows 67 us against 76 here, 40 rows 119 against 76, 128 rows 145
-// against 71; one sequence of 1000 keys, where this kernel's longer start shows:
-// 32 rows 14.9 against 16.8, 64 rows 15.4 against 17.1, 128 rows 17.6 against 17.7).
+// heads of 128: 32 rows 70 us against 75 here, 40 rows 124 against 75, 128 rows 233
+// against 70; one sequence of 1000 keys, where this kernel's longer start shows:
+// 32 rows 14.6 against 16.6, 64 rows 15.1 against 16.9, 128 rows 15.8 against 17.6).
 constexpr int kPromptRowsAbove = 32;
 constexpr float kPromptBias = 6.0f;
 constexpr float kSlack = 8.0f;
 
 // At least 2 tiles per block; a unit, or a piece of one, costs about 4 tiles beside
-// its own (2 prompts of 1500 tokens, 32 heads on 8: 106 us, 124 with 2, 106 with 7;
-// 8 ragged ones of up to 1024 tokens over up to 2000 keys, 40 heads: 217, 248, 238).
+// its own (2 prompts of 1500 tokens, 32 heads on 8: 96 us, 109 with 2, 97 with 7;
+// 8 ragged ones of up to 1024 tokens over up to 2000 keys, 40 heads: 208, 256, 203).
 using PromptTiling = TilingOf<kPromptRows, kPromptKeys, 2, 4>;
 
 // One block's note for the join: the unit whose first part it has, if that
@@ -958,8 +960,8 @@ cudaError_t launch_kv8_prompt(AttentionArgs a, void* data, int* status, int num_
     const PromptRun run{reinterpret_cast<JoinNote*>(data), status, test_wait_ns(), test_stall()};
     a.partials = reinterpret_cast<float*>(reinterpret_cast<char*>(data) +
                                           ((size_t)num_sms * sizeof(JoinNote) + 255) / 256 * 256);
-    // equal parts, as in kv8_attention.cu (one prompt of 512 tokens, 32 heads on 8: 24.5 us
-    // against 26.0 in one line of tiles)
+    // equal parts, as in kv8_attention.cu (one prompt of 512 tokens, 32 heads on 8: 24.2 us
+    // against 25.1 in one line of tiles)
     const long long rows = (long long)a.bt.tokens * a.group;
     const bool few = (rows / kPromptRows + a.bt.batch) * a.c.kv_heads <= num_sms / 2;
     if (a.c.head_dim == 64)

@@ -276,7 +276,7 @@ public:
             sum = __reduce_add_sync(0xffffffffu, sum);
             units = __reduce_add_sync(0xffffffffu, units);
         }
-        if (sum == kMostTiles) kv8_report(a.bt);  // over 8e12 bytes of keys and values
+        if (sum == kMostTiles) kv8_report(a.bt);  // more than the line can count
         if (sum == 0 || sum == kMostTiles) return false;
         // At most half of the blocks go to rounding.  The host has bounded the units by
         // the tokens; only a malformed list, whose sequences overlap, holds more of them,

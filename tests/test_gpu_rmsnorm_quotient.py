@@ -72,7 +72,8 @@ def test_zeros_keep_their_signs_and_infinities_take_the_scale(dev):
     groups = part.float().view(16, 128)
     known = groups.masked_fill(torch.isnan(groups), 0)
     assert torch.equal(scales, torch.from_numpy(known.amax(1).numpy() / np.float32(448)))
-    q = torch.from_numpy(groups.numpy() / scales.numpy()[:, None])  # 0 below an infinite scale
+    with np.errstate(invalid="ignore"):  # inf / inf
+        q = torch.from_numpy(groups.numpy() / scales.numpy()[:, None])
     want = ref.round_e4m3(q.flatten()) | minus[0]
     nan = torch.isnan(q.flatten())
     assert torch.equal(codes[0][~nan], want[~nan])
