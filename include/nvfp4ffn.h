@@ -551,6 +551,153 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
                            int window, int sinks, void* out, float* lse, void* ws, size_t ws_bytes,
                            cudaStream_t stream);
 
+/* ------------------------------------------------------ 4-bit activations (w4a4) */
+
+/*
+ * Products for many token rows, on the FP4 tensor cores: activations are
+ * quantised to NVFP4 like the weights (the W4A4 prefill path of "spark_model/
+ * layers/dense_ffn.rs", forward_prefill_inner: quantize_bf16_to_nvfp4, then
+ * w4a4_gemm), dense or grouped by expert.  Other numerics than the calls above,
+ * which keep activations in bf16: a user chooses.  These calls take any number of
+ * rows up to 2^22 (RANGE beyond), K, H and I multiples of 16 up to 65536, N up to
+ * 2^20.  They are asynchronous, use programmatic dependent launch, read no input
+ * before the preceding kernel on `stream` has completed, and their results are
+ * bit-reproducible.  Blocks do not wait for one another, so calls on different
+ * streams may overlap if their workspaces (and rows buffers) differ.
+ *
+ * A row of x [M, K] becomes a scale r per row, one E4M3 scale per 16 values and
+ * E2M1 codes (all to nearest, ties to even, saturating):
+ *   r    = the smallest 2^e with max|x| <= 2688 * 2^e, e in -100..117; 1 for a row
+ *          of zeros, NaN for a row that holds an infinity or a NaN
+ *   s_b  = E4M3(max|x_b| / 6 / r)        per block b of 16
+ *   code = E2M1(x / (s_b * r))           0 where s_b is 0
+ * A row's result depends on that row alone.  A row that is not finite gives an
+ * output row of NaN and leaves the others as they are.
+ */
+
+/*
+ * Weights in the products' layout: canonical NVFP4 codes [experts, N, K/2] and
+ * scales [experts, N, K/16] (nvfp4_quantize's), moved byte by byte, zero-padded to
+ * N' = roundup(N, 256) and K' = roundup(K, 256).  experts 1..1024, 1 for a dense
+ * weight.  The gate/up pair [experts, I, H] interleaves gate and up (I a multiple
+ * of 16; padded to 128 features).  Sizes are 0 where the call refuses.
+ */
+size_t w4a4_repacked_bytes(int experts, int N, int K);
+size_t w4a4_repacked_gate_up_bytes(int experts, int I, int H);
+nvfp4_status w4a4_repack(const uint8_t* codes, const uint8_t* scales, int experts, int N, int K,
+                         void* packed, cudaStream_t stream);
+nvfp4_status w4a4_repack_gate_up(const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                 const uint8_t* up_codes, const uint8_t* up_scales, int experts,
+                                 int I, int H, void* packed, cudaStream_t stream);
+/* Inverse of w4a4_repack (a test and inspection aid). */
+nvfp4_status w4a4_unpack(const void* packed, int experts, int N, int K, uint8_t* codes,
+                         uint8_t* scales, cudaStream_t stream);
+
+/*
+ * Rows that belong to experts: rows start[e] .. start[e+1] - 1 of the call's M to
+ * expert e.  start does not decrease; rows in front of start[0] and from
+ * start[experts] on belong to none: nothing is read or written for them.  The
+ * lists live on the device and are not read by the host.  The kernels check them:
+ * an expert whose rows do not lie in 0..M has none.
+ */
+typedef struct {
+    const int* start;  /* (device) [experts + 1] */
+    const int* source; /* (device) [M], for w4a4_quantize: the row of x that each row is, or
+                          NULL (row m is x's row m); a source outside x is a row of zeros */
+    int experts;       /* 1..1024 */
+    int sources;       /* rows of x, where source is given */
+} w4a4_groups;
+
+/* Bytes of M quantised rows (0 for sizes that the calls refuse); experts as in the
+ * groups, 1 without. */
+size_t w4a4_rows_bytes(int M, int K, int experts);
+
+/*
+ * x (device) bf16 [M, K], or [sources, K] with a source list, -> rows (device, out,
+ * w4a4_rows_bytes, opaque).  groups NULL for a dense product.
+ */
+nvfp4_status w4a4_quantize(const void* x, int M, int K, const w4a4_groups* groups, void* rows,
+                           cudaStream_t stream);
+
+/* The values that rows stand for: out (device, out) bf16 [M, K] = code * s_b * r, which
+ * bf16 holds exactly unless r is near the end of its range (a test and inspection aid;
+ * groups as for w4a4_quantize, without its sources). */
+nvfp4_status w4a4_dequantize(const void* rows, int M, int K, const w4a4_groups* groups, void* out,
+                             cudaStream_t stream);
+
+/* Workspace bytes for the products below on the current device (N features, of a
+ * weight or a gate/up pair; experts 1 without groups); contract as for nvfp4_gemv. */
+size_t w4a4_gemm_workspace_bytes(int M, int N, int K, int experts);
+
+/*
+ * y[m][n] = bf16(r_m * (scale2 * sum_k xc[m][k] xs[m][k/16] wc[n][k] ws[n][k/16])),
+ * sums in fp32:  rows from w4a4_quantize(M, K);  packed_w from w4a4_repack(1, N, K);
+ * y (device, out) bf16 [M, N].  N may be odd.
+ */
+nvfp4_status w4a4_gemm(const void* rows, int M, int K, const void* packed_w, float scale2, int N,
+                       void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* h[m][i] = bf16(act(g) * u) with g, u such products in bf16, of the gate and the up
+ * weight: gate_up_packed from w4a4_repack_gate_up(1, I, H); h (device, out) bf16 [M, I]. */
+nvfp4_status w4a4_gate_up(const void* rows, int M, int H, const void* gate_up_packed,
+                          float gate_scale2, float up_scale2, int I, nvfp4_act act, void* h,
+                          void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The same with each row's weight that of its expert: packed from w4a4_repack(experts,
+ * ...), scale2 (device) fp32 [experts], rows quantised with the same groups. */
+nvfp4_status w4a4_experts_gemm(const void* rows, int M, int K, const w4a4_groups* groups,
+                               const void* packed_w, const float* scale2, int N, void* y, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
+nvfp4_status w4a4_experts_gate_up(const void* rows, int M, int H, const w4a4_groups* groups,
+                                  const void* gate_up_packed, const float* gate_scale2,
+                                  const float* up_scale2, int I, nvfp4_act act, void* h, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The FFN on quantised activations: x quantised, h = act(gate(x)) * up(x) in bf16,
+ * h quantised, out = down(h).  x (device) bf16 [M, H], out (device, out) bf16 [M, H],
+ * not overlapping; ws >= ffn_swiglu_w4a4_workspace_bytes (contract as for nvfp4_gemv).
+ */
+size_t ffn_swiglu_w4a4_workspace_bytes(int M, int H, int I);
+nvfp4_status ffn_swiglu_w4a4(const void* x, int M, int H, int I, const void* gate_up_packed,
+                             float gate_scale2, float up_scale2, const void* down_packed,
+                             float down_scale2, nvfp4_act act, void* out, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/*
+ * A routed batch in the order of its experts: ids (device) int32 [tokens, choices] are
+ * the experts of each token; one outside 0..experts-1 belongs to none (a token of a
+ * padded batch).  Pairs (token, choice) are sorted by expert, those of an expert in
+ * the order of the list:
+ *   start  (device, out) [experts + 1]: each expert's first row, and their end
+ *   source (device, out) [tokens * choices]: each row's token, -1 from the end on
+ *   place  (device, out) [tokens, choices]: each pair's row, -1 for none
+ * choices 1..64, tokens * choices up to 2^22.
+ */
+nvfp4_status experts_order(const int* ids, int tokens, int choices, int experts, int* start,
+                           int* source, int* place, cudaStream_t stream);
+
+/*
+ * out[t] = bf16(sum_j weights[t][j] * y[place[t][j]]) in fp32, in the order of j:
+ * y (device) bf16 [rows, H], weights (device) fp32 [tokens, choices], out (device,
+ * out) bf16 [tokens, H].  A place outside 0..rows-1 adds nothing, whatever its weight.
+ */
+nvfp4_status experts_sum(const void* y, int rows, const int* place, const float* weights, int tokens,
+                         int choices, int H, void* out, cudaStream_t stream);
+
+/*
+ * The experts' FFN of a routed batch: experts_order, the rows' FFN (as ffn_swiglu_w4a4,
+ * with each expert's weights; its output rows in bf16), experts_sum.  x, out (device)
+ * bf16 [tokens, H]; scales (device) fp32 [experts].  A token without an expert gets 0.
+ */
+size_t experts_swiglu_w4a4_workspace_bytes(int tokens, int choices, int experts, int H, int I);
+nvfp4_status experts_swiglu_w4a4(const void* x, int tokens, int H, int I, const int* ids,
+                                 const float* weights, int choices, int experts,
+                                 const void* gate_up_packed, const float* gate_scale2,
+                                 const float* up_scale2, const void* down_packed,
+                                 const float* down_scale2, nvfp4_act act, void* out, void* ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ utilities */
 
 /* Zero-fill a workspace (asynchronous memset on `stream`). */

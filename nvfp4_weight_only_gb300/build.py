@@ -15,7 +15,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4ffn.so")
 SOURCES = ["api.cu", "quantize.cu", "repack.cu", "stream_gemv.cu", "stream_gemv_fp8.cu",
            "ffn_noalloc.cu", "lora.cu", "api_attention.cu", "rmsnorm.cu", "kv8_cache.cu",
-           "kv8_attention.cu", "kv8_prompt.cu"]
+           "kv8_attention.cu", "kv8_prompt.cu", "api_w4a4.cu", "w4a4_rows.cu", "w4a4_gemm.cu",
+           "experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,304 @@
+// w4a4_rows.cu -- NVFP4 operands into the tiles of w4a4.h: weights once, by
+// moving bytes; activation rows at every call, by quantising them.
+//
+// A row of x becomes r (2^e with the smallest e that keeps max|x| <= 2688 r, in
+// -100..117), per 16 values s = E4M3(max|x| / 6 / r), and codes E2M1(x / (s r)).
+// x / r is exact, so the two roundings are of quotients of a bf16 value: by 6,
+// where fp32 division cannot reach a tie of E4M3 that the quotient is not (they
+// are 2^-10 apart), and by s.  The latter is a product with 1/s, off by 2^-23 of
+// itself, brought to multiples of 2^-14 by adding and taking away 768: a quotient
+// that is a tie of E2M1 lands on it, any other is 2^-10 or more away and stays on
+// its side.  So codes are those of the exact quotients, without a division each.
+#include "kv8.cuh"
+#include "w4a4.h"
+
+namespace nvf {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMinExp = -100, kMaxExp = 117;
+
+// One thread per 16 code bytes of a tile (two scale bytes with them).
+__global__ void __launch_bounds__(kThreads) repack_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    const uint8_t* __restrict__ codes2, const uint8_t* __restrict__ scales2, long long total, int N,
+    int K, int row_blocks, int k_blocks, uint8_t* __restrict__ packed) {
+    for (long long idx = blockIdx.x * (long long)kThreads + threadIdx.x; idx < total;
+         idx += (long long)gridDim.x * kThreads) {
+        const int piece = (int)(idx & 7), r = (int)(idx >> 3 & 127);
+        const long long tile = idx >> 10;
+        const int kb = (int)(tile % k_blocks);
+        const long long rb = tile / k_blocks;
+        const long long expert = rb / row_blocks;
+        const int block = (int)(rb % row_blocks);
+        const bool second = codes2 && (r & 16);
+        const int n = codes2 ? block * 64 + (r >> 5) * 16 + (r & 15) : block * 128 + r;
+        const int k = kb * kW4K + piece * 32;
+        uint8_t* out = packed + tile * kW4Tile;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        uint32_t sc = 0;
+        if (n < N && k < K) {
+            const long long row = expert * N + n;
+            const uint8_t* c = (second ? codes2 : codes) + row * (K / 2) + k / 2;
+            const uint8_t* s = (second ? scales2 : scales) + row * (K / 16) + k / 16;
+            // K is a multiple of 16: 8 bytes or 16 of this piece are there
+            uint32_t v[4] = {0, 0, 0, 0};
+            const int have = K - k >= 32 ? 4 : 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < have)
+                    v[i] = c[4 * i] | c[4 * i + 1] << 8 | c[4 * i + 2] << 16 |
+                           (uint32_t)c[4 * i + 3] << 24;
+            w = make_uint4(v[0], v[1], v[2], v[3]);
+            sc = s[0] | (have == 4 ? s[1] << 8 : 0);
+        }
+        *reinterpret_cast<uint4*>(out + w4_code_at(r, piece * 16)) = w;
+        *reinterpret_cast<uint16_t*>(out + w4_scale_at(r, piece * 2)) = (uint16_t)sc;
+    }
+    // Visible GPU-wide before this block exits: the product may start on its weights as
+    // soon as every block has.
+    __threadfence();
+}
+
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ packed,
+                                                          long long total, int N, int K,
+                                                          int row_blocks, int k_blocks,
+                                                          uint8_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales) {
+    const int blocks = K / 16;
+    for (long long idx = blockIdx.x * (long long)kThreads + threadIdx.x; idx < total;
+         idx += (long long)gridDim.x * kThreads) {
+        const int b = (int)(idx % blocks);
+        const long long row = idx / blocks;
+        const int n = (int)(row % N);
+        const uint8_t* tile =
+            packed +
+            ((row / N * row_blocks + n / kW4Rows) * k_blocks + b / 16) * (long long)kW4Tile;
+        const int r = n % kW4Rows;
+        for (int i = 0; i < 8; ++i)
+            codes[row * (K / 2) + b * 8 + i] = tile[w4_code_at(r, (b % 16) * 8 + i)];
+        scales[row * blocks + b] = tile[w4_scale_at(r, b % 16)];
+    }
+}
+
+// The expert of a row and its place; false for a row of none.  All threads of the
+// block call it.
+__device__ __forceinline__ bool find_place(const W4Groups& g, int row, long long& block, int& r) {
+    int expert = 0, first = 0;
+    if (g.start) {
+        // the last expert that starts at or before the row: empty ones in front of it
+        // start there too
+        int before = 0;
+        for (int base = 0; base < g.experts; base += blockDim.x) {
+            const int e = base + threadIdx.x;
+            before += __syncthreads_count(e < g.experts && g.start[e] <= row);
+        }
+        expert = before - 1;
+        if (expert < 0) return false;
+        first = g.start[expert];
+        if (first < 0 || first > row || row >= g.start[expert + 1]) return false;
+    }
+    const int i = row - first;
+    block = first / kW4Rows + expert + i / kW4Rows;
+    r = i % kW4Rows;
+    return true;
+}
+
+// Four pairs of quotients -> eight codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
+    uint32_t w;
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(w)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    return w;
+}
+
+// The larger of two pairs of bf16, NaN if either is.
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// One block per row; a warp takes 256 values at a time, 8 per lane, which stay in
+// registers between the row's maximum and the codes, so x is read once.
+template <int kIter>
+__global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict__ x, int K,
+                                                        int k_blocks, const W4Groups g,
+                                                        uint8_t* __restrict__ rows,
+                                                        float* __restrict__ row_scales) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int row = blockIdx.x;
+    long long block;
+    int r;
+    if (!find_place(g, row, block, r)) return;
+    const int from = g.source ? g.source[row] : row;
+    // a row without a source is a row of zeros
+    const int vecs = K / 8, have = from >= 0 && from < g.sources ? vecs : 0;
+    const uint4* src = x + (have ? (size_t)from * vecs : 0);
+    uint4 v[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        const int c = (warp + i * warps) * 32 + lane;
+        v[i] = c < have ? src[c] : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t top[kIter];  // the largest of each block of 16, as bf16
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t m = max2_nan(max2_nan(v[i].x & kAbs, v[i].y & kAbs),
+                                    max2_nan(v[i].z & kAbs, v[i].w & kAbs));
+        top[i] = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        most = max2_nan(most, top[i]);
+    }
+#pragma unroll
+    for (int d = 16; d > 1; d >>= 1) most = max2_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
+    __shared__ uint32_t part[32];
+    if (lane == 0) part[warp] = most;
+    __syncthreads();
+    most = lane < warps ? part[lane] : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) most = max2_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
+    // as integers, bf16 magnitudes keep their order, NaN on top
+    const uint32_t amax = max(most & 0xffffu, most >> 16);
+    int e = 0;  // of r
+    if (amax) {
+        // 2688 = 1.3125 * 2^11, and 0x3fa8 is 1.3125
+        const int exponent = max((int)(amax >> 7), 1) - 127;
+        e = exponent - 11 + ((amax & 0x7f) > (0x3fa8 & 0x7f) ? 1 : 0);
+        e = min(max(e, kMinExp), kMaxExp);
+    }
+    if (tid == 0)
+        row_scales[row] = amax >= 0x7f80 ? __uint_as_float(0x7fffffffu)
+                                         : __uint_as_float((uint32_t)(e + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 1 / r
+    uint8_t* const out = rows + (size_t)block * k_blocks * kW4Tile;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        const int kb = warp + i * warps;
+        if (kb >= k_blocks) break;
+        const float largest = __uint_as_float(max(top[i] & 0xffffu, top[i] >> 16) << 16) * down;
+        const uint32_t code = f32_to_e4m3(__fdiv_rn(largest, 6.0f));
+        const float s = e4m3_to_f32(code);
+        const float by = code ? __frcp_rn(s) * down : 0.0f;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float q[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            q[2 * p] = __fmaf_rn(bf16_lo(w[p]), by, 768.0f) - 768.0f;
+            q[2 * p + 1] = __fmaf_rn(bf16_hi(w[p]), by, 768.0f) - 768.0f;
+        }
+        uint8_t* const tile = out + (size_t)kb * kW4Tile;
+        *reinterpret_cast<uint32_t*>(tile + w4_code_at(r, lane * 4)) = e2m1x8(q);
+        // the four scales of 64 values: lanes 8j, 8j + 2, 8j + 4, 8j + 6
+        uint32_t sc = code;
+        sc |= __shfl_down_sync(0xffffffffu, sc, 2) << 8;
+        sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 16;
+        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile + w4_scale_at(r, lane / 2)) = sc;
+    }
+}
+
+// The values that the codes stand for: scale, block scale and code have 7 bits
+// together, so bf16 holds them exactly (between its least and largest value).
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ rows,
+                                                              const float* __restrict__ row_scales,
+                                                              int K, int k_blocks,
+                                                              const W4Groups g,
+                                                              uint4* __restrict__ out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row = blockIdx.x;
+    long long block;
+    int r;
+    if (!find_place(g, row, block, r)) return;
+    const float scale = row_scales[row];
+    for (int c = threadIdx.x; c < K / 8; c += blockDim.x) {
+        const uint8_t* tile = rows + ((size_t)block * k_blocks + c / 32) * kW4Tile;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + w4_code_at(r, c % 32 * 4));
+        const float s = e4m3_to_f32(tile[w4_scale_at(r, c % 32 / 2)]);
+        uint32_t h[4], o[4];
+        e2m1x8_to_f16x2x4(w, h[0], h[1], h[2], h[3]);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[p]));
+            o[p] = bf16x2(f.x * s * scale, f.y * s * scale);
+        }
+        out[(size_t)row * (K / 8) + c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), int blocks, int threads, cudaStream_t s,
+                   Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int grid_of(long long work) {
+    const long long want = (work + kThreads - 1) / kThreads, most = 16LL * 152;
+    return (int)(want < most ? want : most);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_repack(const uint8_t* codes, const uint8_t* scales, const uint8_t* codes2,
+                             const uint8_t* scales2, int experts, int N, int K, uint8_t* packed,
+                             cudaStream_t s) {
+    const int row_blocks = w4_row_blocks(N, codes2 ? 2 : 1), k_blocks = w4_k_blocks(K);
+    const long long total = (long long)experts * row_blocks * k_blocks * 1024;
+    repack_kernel<<<grid_of(total), kThreads, 0, s>>>(codes, scales, codes2, scales2, total, N, K,
+                                                      row_blocks, k_blocks, packed);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, uint8_t* codes,
+                             uint8_t* scales, cudaStream_t s) {
+    const long long total = (long long)experts * N * (K / 16);
+    unpack_kernel<<<grid_of(total), kThreads, 0, s>>>(packed, total, N, K, w4_row_blocks(N, 1),
+                                                      w4_k_blocks(K), codes, scales);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
+                               cudaStream_t s) {
+    const int k_blocks = w4_k_blocks(K);
+    // 8 warps and up to 8 vectors per lane, then more warps
+    int iter = 1;
+    while (iter < 8 && (k_blocks + iter - 1) / iter > 8) iter *= 2;
+    const int warps = (k_blocks + iter - 1) / iter;
+    auto kernel = iter == 1   ? quantize_kernel<1>
+                  : iter == 2 ? quantize_kernel<2>
+                  : iter == 4 ? quantize_kernel<4>
+                              : quantize_kernel<8>;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(rows);
+    float* const scales =
+        reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, g.experts));
+    return launch(kernel, M, warps * 32, s, reinterpret_cast<const uint4*>(x), K, k_blocks, g, base,
+                  scales);
+}
+
+cudaError_t launch_w4_dequantize(const void* rows, int M, int K, const W4Groups& g, void* out,
+                                 cudaStream_t s) {
+    const uint8_t* const base = reinterpret_cast<const uint8_t*>(rows);
+    const float* const scales =
+        reinterpret_cast<const float*>(base + w4_rows_scale_offset(M, K, g.experts));
+    return launch(dequantize_kernel, M, kThreads, s, base, scales, K, w4_k_blocks(K), g,
+                  reinterpret_cast<uint4*>(out));
+}
+
+}  // namespace nvf

@@ -44,6 +44,11 @@ EXPORTS = [
     "ffn_swiglu_w8a16_workspace_bytes", "ffn_swiglu_w8a16",
     "add_rmsnorm_bf16", "add_rmsnorm_e4m3", "rope_table", "kv8_batch_status", "kv8_append",
     "kv8_read", "kv8_attention_workspace_bytes", "kv8_attention",
+    "w4a4_repacked_bytes", "w4a4_repacked_gate_up_bytes", "w4a4_repack", "w4a4_repack_gate_up",
+    "w4a4_unpack", "w4a4_rows_bytes", "w4a4_quantize", "w4a4_dequantize",
+    "w4a4_gemm_workspace_bytes", "w4a4_gemm", "w4a4_gate_up", "w4a4_experts_gemm",
+    "w4a4_experts_gate_up", "ffn_swiglu_w4a4_workspace_bytes", "ffn_swiglu_w4a4", "experts_order",
+    "experts_sum", "experts_swiglu_w4a4_workspace_bytes", "experts_swiglu_w4a4",
     "nvfp4_workspace_init", "nvfp4_workspace_status", "nvfp4_status_string",
 ]
 # Every symbol declared in include/nvfp4ffn_testing.h (test hooks).
@@ -118,6 +123,26 @@ def load(build_if_missing: bool = False):
         "kv8_read": (i32, [vp, vp, i32, vp, vp, vp]),
         "kv8_attention_workspace_bytes": (sz, [vp, vp, i32, i32]),
         "kv8_attention": (i32, [vp, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, vp, sz, vp]),
+        "w4a4_repacked_bytes": (sz, [i32, i32, i32]),
+        "w4a4_repacked_gate_up_bytes": (sz, [i32, i32, i32]),
+        "w4a4_repack": (i32, [vp, vp, i32, i32, i32, vp, vp]),
+        "w4a4_repack_gate_up": (i32, [vp, vp, vp, vp, i32, i32, i32, vp, vp]),
+        "w4a4_unpack": (i32, [vp, i32, i32, i32, vp, vp, vp]),
+        "w4a4_rows_bytes": (sz, [i32, i32, i32]),
+        "w4a4_quantize": (i32, [vp, i32, i32, vp, vp, vp]),
+        "w4a4_dequantize": (i32, [vp, i32, i32, vp, vp, vp]),
+        "w4a4_gemm_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "w4a4_gemm": (i32, [vp, i32, i32, vp, f32, i32, vp, vp, sz, vp]),
+        "w4a4_gate_up": (i32, [vp, i32, i32, vp, f32, f32, i32, i32, vp, vp, sz, vp]),
+        "w4a4_experts_gemm": (i32, [vp, i32, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "w4a4_experts_gate_up": (i32, [vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
+        "ffn_swiglu_w4a4_workspace_bytes": (sz, [i32, i32, i32]),
+        "ffn_swiglu_w4a4": (i32, [vp, i32, i32, i32, vp, f32, f32, vp, f32, i32, vp, vp, sz, vp]),
+        "experts_order": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
+        "experts_sum": (i32, [vp, i32, vp, vp, i32, i32, i32, vp, vp]),
+        "experts_swiglu_w4a4_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "experts_swiglu_w4a4": (i32, [vp, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32,
+                                      vp, vp, sz, vp]),
         "nvfp4_workspace_init": (i32, [vp, sz, vp]),
         "nvfp4_workspace_status": (i32, [vp, vp]),
         "nvfp4_status_string": (ctypes.c_char_p, [i32]),
@@ -696,4 +721,301 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, softmax_sca
         _plain(ws, "ws", _U8, ws.shape, device), ws.numel(), _raw_stream(device))
     if code:
         _check("kv8_attention", code)
+    return out
+
+
+# ------------------------------------------------------------------ 4-bit activations (w4a4)
+
+class _GroupsStruct(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("source", ctypes.c_void_p), ("experts", ctypes.c_int),
+                ("sources", ctypes.c_int)]
+
+
+def _stacked(codes, scales, name):
+    """Checks codes u8 [N, K/2] or [experts, N, K/2] and their scales: (experts, N, K, device,
+    addresses)."""
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"{name} codes must be [N, K/2] or [experts, N, K/2]")
+    shape, device = codes.shape, codes.get_device()
+    at = _plain(codes, f"{name} codes", _U8, shape, device)
+    scales_at = _plain(scales, f"{name} scales", _U8, (*shape[:-1], shape[-1] // 8), device)
+    return (shape[0] if len(shape) == 3 else 1), shape[-2], 2 * shape[-1], device, at, scales_at
+
+
+def w4a4_repack(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """NVFP4 codes [N, K/2] and scales [N, K/16], or those of experts stacked in front, -> the
+    layout of the products on 4-bit activations."""
+    experts, N, K, device, at, scales_at = _stacked(codes, scales, "w4a4_repack")
+    L = load()
+    out = torch.empty(L.w4a4_repacked_bytes(experts, N, K), dtype=_U8, device=codes.device)
+    _check("w4a4_repack", L.w4a4_repack(at, scales_at, experts, N, K, out.data_ptr(),
+                                        _raw_stream(device)))
+    return out
+
+
+def w4a4_repack_gate_up(gate_codes, gate_scales, up_codes, up_scales) -> torch.Tensor:
+    """Gate and up projections [I, H] (experts stacked in front) into one blob."""
+    experts, I, H, device, gate, gate_s = _stacked(gate_codes, gate_scales, "gate")
+    if up_codes.shape != gate_codes.shape or up_codes.get_device() != device:
+        raise ValueError("gate and up must have the same shape and device")
+    *_, up, up_s = _stacked(up_codes, up_scales, "up")
+    L = load()
+    out = torch.empty(L.w4a4_repacked_gate_up_bytes(experts, I, H), dtype=_U8,
+                      device=gate_codes.device)
+    _check("w4a4_repack_gate_up",
+           L.w4a4_repack_gate_up(gate, gate_s, up, up_s, experts, I, H, out.data_ptr(),
+                                 _raw_stream(device)))
+    return out
+
+
+def w4a4_unpack(packed: torch.Tensor, N: int, K: int, experts: int = None):
+    """Inverse of w4a4_repack; codes and scales have experts in front when it is given."""
+    L, n = load(), experts or 1
+    device = packed.get_device()
+    at = _plain(packed, "packed", _U8, (L.w4a4_repacked_bytes(n, N, K),), device)
+    front = () if experts is None else (experts,)
+    codes = torch.empty((*front, N, K // 2), dtype=_U8, device=packed.device)
+    scales = torch.empty((*front, N, K // 16), dtype=_U8, device=packed.device)
+    _check("w4a4_unpack", L.w4a4_unpack(at, n, N, K, codes.data_ptr(), scales.data_ptr(),
+                                        _raw_stream(device)))
+    return codes, scales
+
+
+class W4a4Rows:
+    """M rows of K values in 4 bits, as w4a4_quantize writes them; with start int32 [experts + 1]
+    (rows start[e] .. start[e+1] - 1 belong to expert e, read on the device when a call runs)
+    they are an expert product's."""
+
+    def __init__(self, data, M, K, start=None):
+        self.data, self.M, self.K, self.start = data, M, K, start
+        self.device = data.get_device()
+        self.experts = 1 if start is None else start.numel() - 1
+        size = load().w4a4_rows_bytes(M, K, self.experts)
+        if size == 0:
+            raise ValueError(f"no rows of M={M}, K={K}, experts={self.experts}")
+        self.at = _plain(data, "data", _U8, (size,), self.device)
+        self.struct = self.groups = None
+        if start is not None:
+            self.struct = _GroupsStruct(_plain(start, "start", _I32, start.shape, self.device), None,
+                                        self.experts, 0)
+            self.groups = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, M, K, device, start=None):
+        """Rows that nothing has been written to."""
+        experts = 1 if start is None else start.numel() - 1
+        size = load().w4a4_rows_bytes(M, K, experts)
+        return cls(torch.empty(size, dtype=_U8, device=device), M, K, start)
+
+
+def w4a4_quantize(x: torch.Tensor, start: torch.Tensor = None, source: torch.Tensor = None,
+                  out: W4a4Rows = None) -> W4a4Rows:
+    """x bf16 [M, K] in 4 bits.  With start (see W4a4Rows) the rows are an expert product's; with
+    source int32 [M] as well, row m is x's row source[m]."""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
+                         f"{list(x.shape)} on {x.device}")
+    n, K = x.shape
+    device = x.get_device()
+    M = n if source is None else source.numel()
+    if out is None:
+        out = W4a4Rows.empty(M, K, x.device, start)
+    elif start is not None and start is not out.start:
+        raise ValueError("start is not that of out")
+    if out.M != M or out.K != K or out.device != device:
+        raise ValueError(f"out holds {out.M} rows of {out.K} on device {out.device}, "
+                         f"got {M} of {K} on {device}")
+    groups, struct = out.groups, None
+    if source is not None:
+        if groups is None:
+            raise ValueError("a source list needs start")
+        struct = _GroupsStruct(out.struct.start, _plain(source, "source", _I32, (M,), device),
+                               out.experts, n)
+        groups = ctypes.addressof(struct)
+    code = (_lib or load()).w4a4_quantize(x.data_ptr(), M, K, groups, out.at, _raw_stream(device))
+    if code:
+        _check("w4a4_quantize", code)
+    return out
+
+
+def w4a4_dequantize(rows: W4a4Rows, out: torch.Tensor = None) -> torch.Tensor:
+    """The values that rows stand for, bf16 [M, K] (rows of no expert are left as they were)."""
+    if out is None:
+        out = torch.zeros((rows.M, rows.K), dtype=_BF16, device=rows.data.device)
+    _check("w4a4_dequantize",
+           load().w4a4_dequantize(rows.at, rows.M, rows.K, rows.groups,
+                                  _plain(out, "out", _BF16, (rows.M, rows.K), rows.device),
+                                  _raw_stream(rows.device)))
+    return out
+
+
+def w4a4_gemm_workspace_bytes(M: int, N: int, K: int, experts: int = 1) -> int:
+    return load().w4a4_gemm_workspace_bytes(M, N, K, experts)
+
+
+def _w4a4_buffers(rows, N, packed, size, ws, out, name):
+    """Checks a product's buffers, allocates those not given: (out, its address, ws, its address)."""
+    if ws is None:
+        ws = workspace(load().w4a4_gemm_workspace_bytes(rows.M, N, rows.K, rows.experts),
+                       rows.data.device)
+    if out is None:
+        out = torch.empty((rows.M, N), dtype=_BF16, device=rows.data.device)
+    return (out, _plain(out, name, _BF16, (rows.M, N), rows.device), ws,
+            _plain(ws, "ws", _U8, ws.shape, rows.device),
+            _plain(packed, "packed weight", _U8, (size,), rows.device))
+
+
+def _per_expert(scale, name, rows):
+    return _plain(scale, name, _F32, (rows.experts,), rows.device)
+
+
+def w4a4_gemm(rows: W4a4Rows, packed_w: torch.Tensor, scale2, N: int, ws: torch.Tensor = None,
+              out: torch.Tensor = None) -> torch.Tensor:
+    """y bf16 [M, N]: quantised rows by a weight of w4a4_repack.  Rows with experts take each
+    expert's weight, scale2 is then fp32 [experts] on the device, and rows of no expert are left
+    as they were."""
+    L = _lib or load()
+    out, out_at, ws, ws_at, w = _w4a4_buffers(
+        rows, N, packed_w, L.w4a4_repacked_bytes(rows.experts, N, rows.K), ws, out, "out")
+    if rows.groups is None:
+        code = L.w4a4_gemm(rows.at, rows.M, rows.K, w, scale2, N, out_at, ws_at, ws.numel(),
+                           _raw_stream(rows.device))
+    else:
+        code = L.w4a4_experts_gemm(rows.at, rows.M, rows.K, rows.groups, w,
+                                   _per_expert(scale2, "scale2", rows), N, out_at, ws_at,
+                                   ws.numel(), _raw_stream(rows.device))
+    if code:
+        _check("w4a4_gemm", code)
+    return out
+
+
+def w4a4_gate_up(rows: W4a4Rows, gate_up_packed: torch.Tensor, gate_scale2, up_scale2, I: int,
+                 act: int = NVFP4_ACT_SILU, ws: torch.Tensor = None,
+                 h: torch.Tensor = None) -> torch.Tensor:
+    """h bf16 [M, I] = act(gate(x)) * up(x) for quantised rows; scales as for w4a4_gemm."""
+    L = _lib or load()
+    h, h_at, ws, ws_at, w = _w4a4_buffers(
+        rows, I, gate_up_packed, L.w4a4_repacked_gate_up_bytes(rows.experts, I, rows.K), ws, h, "h")
+    if rows.groups is None:
+        code = L.w4a4_gate_up(rows.at, rows.M, rows.K, w, gate_scale2, up_scale2, I, act, h_at,
+                              ws_at, ws.numel(), _raw_stream(rows.device))
+    else:
+        code = L.w4a4_experts_gate_up(rows.at, rows.M, rows.K, rows.groups, w,
+                                      _per_expert(gate_scale2, "gate_scale2", rows),
+                                      _per_expert(up_scale2, "up_scale2", rows), I, act, h_at,
+                                      ws_at, ws.numel(), _raw_stream(rows.device))
+    if code:
+        _check("w4a4_gate_up", code)
+    return h
+
+
+def ffn_swiglu_w4a4_workspace_bytes(M: int, H: int, I: int) -> int:
+    return load().ffn_swiglu_w4a4_workspace_bytes(M, H, I)
+
+
+def _matrix(x, name):
+    """(rows, width, device) of a contiguous bf16 CUDA matrix."""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
+                         f"{list(x.shape)} on {x.device}")
+    return (*x.shape, x.get_device())
+
+
+def ffn_swiglu_w4a4(x: torch.Tensor, gate_up_packed: torch.Tensor, gate_scale2: float,
+                    up_scale2: float, down_packed: torch.Tensor, down_scale2: float, I: int,
+                    act: int = NVFP4_ACT_SILU, ws: torch.Tensor = None,
+                    out: torch.Tensor = None) -> torch.Tensor:
+    """out bf16 [M, H] = down(act(gate(x)) * up(x)) on quantised activations, any number of rows."""
+    M, H, device = _matrix(x, "x")
+    L = _lib or load()
+    if ws is None:
+        ws = workspace(L.ffn_swiglu_w4a4_workspace_bytes(M, H, I), x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    code = L.ffn_swiglu_w4a4(
+        x.data_ptr(), M, H, I,
+        _plain(gate_up_packed, "gate_up_packed", _U8, (L.w4a4_repacked_gate_up_bytes(1, I, H),),
+               device), gate_scale2, up_scale2,
+        _plain(down_packed, "down_packed", _U8, (L.w4a4_repacked_bytes(1, H, I),), device),
+        down_scale2, act, _plain(out, "out", _BF16, x.shape, device),
+        _plain(ws, "ws", _U8, ws.shape, device), ws.numel(), _raw_stream(device))
+    if code:
+        _check("ffn_swiglu_w4a4", code)
+    return out
+
+
+def experts_order(ids: torch.Tensor, experts: int, start: torch.Tensor = None,
+                  source: torch.Tensor = None, place: torch.Tensor = None):
+    """ids int32 [tokens, choices] sorted by expert: (start [experts + 1], source [tokens *
+    choices], place [tokens, choices]), int32."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, choices]")
+    shape, device = ids.shape, ids.get_device()
+    at = _plain(ids, "ids", _I32, shape, device)
+    pairs = shape[0] * shape[1]
+    new = lambda *n: torch.empty(n, dtype=_I32, device=ids.device)  # noqa: E731
+    start = new(experts + 1) if start is None else start
+    source = new(pairs) if source is None else source
+    place = new(*shape) if place is None else place
+    code = (_lib or load()).experts_order(
+        at, shape[0], shape[1], experts, _plain(start, "start", _I32, (experts + 1,), device),
+        _plain(source, "source", _I32, (pairs,), device),
+        _plain(place, "place", _I32, shape, device), _raw_stream(device))
+    if code:
+        _check("experts_order", code)
+    return start, source, place
+
+
+def experts_sum(y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor,
+                out: torch.Tensor = None) -> torch.Tensor:
+    """out bf16 [tokens, H] = each token's sum of weights fp32 [tokens, choices] times the rows of
+    y bf16 [rows, H] at place int32 [tokens, choices] (below 0: none)."""
+    rows, H, device = _matrix(y, "y")
+    shape = place.shape
+    if len(shape) != 2:
+        raise ValueError("place must be [tokens, choices]")
+    if out is None:
+        out = torch.empty((shape[0], H), dtype=_BF16, device=y.device)
+    code = (_lib or load()).experts_sum(
+        y.data_ptr(), rows, _plain(place, "place", _I32, shape, device),
+        _plain(weights, "weights", _F32, shape, device), shape[0], shape[1], H,
+        _plain(out, "out", _BF16, (shape[0], H), device), _raw_stream(device))
+    if code:
+        _check("experts_sum", code)
+    return out
+
+
+def experts_swiglu_w4a4_workspace_bytes(tokens: int, choices: int, experts: int, H: int,
+                                        I: int) -> int:
+    return load().experts_swiglu_w4a4_workspace_bytes(tokens, choices, experts, H, I)
+
+
+def experts_swiglu_w4a4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                        gate_up_packed: torch.Tensor, gate_scale2: torch.Tensor,
+                        up_scale2: torch.Tensor, down_packed: torch.Tensor,
+                        down_scale2: torch.Tensor, I: int, act: int = NVFP4_ACT_SILU,
+                        ws: torch.Tensor = None, out: torch.Tensor = None) -> torch.Tensor:
+    """The experts' FFN of a routed batch: x bf16 [tokens, H], ids int32 and weights fp32 [tokens,
+    choices], experts' weights stacked (w4a4_repack), their scales fp32 [experts] on the device."""
+    T, H, device = _matrix(x, "x")
+    shape, experts = ids.shape, gate_scale2.numel()
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"ids must be [{T}, choices], got {list(shape)}")
+    L = _lib or load()
+    if ws is None:
+        ws = workspace(L.experts_swiglu_w4a4_workspace_bytes(T, shape[1], experts, H, I), x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    scales = [_plain(t, f"{n}_scale2", _F32, (experts,), device)
+              for t, n in ((gate_scale2, "gate"), (up_scale2, "up"), (down_scale2, "down"))]
+    code = L.experts_swiglu_w4a4(
+        x.data_ptr(), T, H, I, _plain(ids, "ids", _I32, shape, device),
+        _plain(weights, "weights", _F32, shape, device), shape[1], experts,
+        _plain(gate_up_packed, "gate_up_packed", _U8,
+               (L.w4a4_repacked_gate_up_bytes(experts, I, H),), device), scales[0], scales[1],
+        _plain(down_packed, "down_packed", _U8, (L.w4a4_repacked_bytes(experts, H, I),), device),
+        scales[2], act, _plain(out, "out", _BF16, x.shape, device),
+        _plain(ws, "ws", _U8, ws.shape, device), ws.numel(), _raw_stream(device))
+    if code:
+        _check("experts_swiglu_w4a4", code)
     return out
