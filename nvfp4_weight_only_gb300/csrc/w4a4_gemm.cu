@@ -196,11 +196,18 @@ __device__ __forceinline__ void commit(uint32_t bar) {
                  : "memory");
 }
 
-// act(g) * u; a quotient of fast functions is within 2^-20 of it, the rounding to bf16
-// that follows is off by up to 2^-9.
+// act(g) * u for g and u in bf16: act(g) = g * sigmoid(y), y = g or the argument of GeLU's
+// tanh, doubled.  g * u is exact in fp32, and for y > 0 what sigmoid takes away from
+// it is subtracted, with one rounding.  Where that is too little for fp32, g * u itself
+// may be a tie of bf16 (it has 16 bits); the result is below it, so it goes towards 0.
 __device__ __forceinline__ float gated(int act, float g, float u) {
     const float y = act == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
-    return __fdividef(g, 1.0f + __expf(-y)) * u;
+    const float e = __expf(-fabsf(y)), s = __fdividef(e, 1.0f + e);  // sigmoid(-|y|)
+    if (!(y > 0.0f)) return g * s * u;
+    const float t = g * u;
+    const float p = fabsf(t) < INFINITY ? fmaf(-t, s, t) : t;
+    const uint32_t bits = __float_as_uint(p);
+    return p == t && (bits & 0xffffu) == 0x8000u ? __uint_as_float(bits - 1) : p;
 }
 
 struct Barriers {
