@@ -19,6 +19,17 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
         : "memory");
 }
 
+// Eight columns, waited for.
+__device__ __forceinline__ void tmem_load8(uint32_t at, float (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7])
+        : "r"(at)
+        : "memory");
+}
+
 // The values pass through the wait, so that no use of them moves in front of it.
 __device__ __forceinline__ void tmem_wait_load(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"

@@ -18,6 +18,8 @@
 // tile leaves its sums in the workspace; the block that comes last adds all parts
 // up in the order of their ranges, so results do not depend on timing, and no block
 // waits for another.
+#include <cuda.h>
+
 #include <atomic>
 
 #include "internal.h"
@@ -29,21 +31,24 @@ namespace nvf {
 
 namespace {
 
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;
+constexpr int kJoin = 4;  // parts of a cut tile that are read at a time
 constexpr int kThreads = (2 + kEpilogueWarps) * 32;
 constexpr int kEpilogueThreads = kEpilogueWarps * 32;
 // Token tiles that take turns with one weight tile before the next one: their tiles
 // (16 x 256 tokens of K = 17408: 40 MB) stay in L2 for it.
 constexpr int kSuper = 16;
-// K blocks that a range of a cut tile has at least.
-constexpr int kLeastRange = 2;
 
 template <int kTokens>
 struct Shape {
-    static constexpr int kStages = kTokens == 256 ? 4 : 6;
+    // Blocks that share a tile: a pair takes 256 rows of the weight by 256 tokens, each
+    // block copies its 128 rows and half of the tokens, and the tensor cores of both read
+    // both halves.
+    static constexpr int kBlocks = kTokens == 256 ? 2 : 1;
+    static constexpr int kStages = kTokens == 256 ? 5 : 6;
     static constexpr int kSums = kTokens == 256 ? 1 : 2;  // accumulators in turn
     static constexpr int kBAt = kW4Tile;                  // tokens' codes in a stage
-    static constexpr int kBScalesAt = kBAt + kTokens * 128;
+    static constexpr int kBScalesAt = kBAt + kTokens / kBlocks * 128;
     static constexpr int kStageBytes = kBScalesAt + kTokens * 16;
     static constexpr int kShared = 1024 + kStages * kStageBytes;
     // tensor memory: accumulators, then each stage's scales
@@ -51,6 +56,12 @@ struct Shape {
     static constexpr int kScaleColumns = 16 + kTokens / 8;  // per stage
     static_assert(kScalesAt + kStages * kScaleColumns <= 512, "tensor memory");
     static constexpr int kPartial = kW4Rows * kTokens;  // floats
+    // K blocks that a range of a cut tile has at least.
+    static constexpr int kLeastRange = kBlocks > 1 ? 16 : 2;
+    // Columns of a tile's products: a pair's halves are whole tiles, or those of one.
+    static __device__ __forceinline__ int columns(int tokens) {
+        return kBlocks == 1 ? (tokens + 15) / 16 * 16 : tokens > 128 ? 256 : 128;
+    }
 };
 
 struct Args {
@@ -62,7 +73,7 @@ struct Args {
     const float* scales_a;
     const float* scales_b;
     float scale_a, scale_b;
-    int M, N, k_blocks, row_blocks, experts, act;
+    int M, N, k_blocks, row_blocks, experts, act;  // row_blocks: of a tile's rows
     int* status;
     int* counters;
     float* partials;
@@ -70,41 +81,55 @@ struct Args {
     int stall;
 };
 
+// Tiles as tensors of kilobytes, [block][K block][18][256 x 4 bytes], for the copies of
+// pairs: what one block copies is reported to the other's barrier, which the plain bulk
+// copies cannot.  Boxes: a whole tile, a tile's codes, the scales of two tiles.
+struct Maps {
+    CUtensorMap weight, codes, scales;
+};
+
 // A range of K blocks of one tile.
 struct Item {
     int expert, weight, token0, tokens;  // row block of the weight; first row, rows
     long long block;                     // first tile of the rows
     int kb0, kb1;
-    int parts, first_part, left_over;    // parts > 1: blocks first_part .. + parts - 1
+    int parts, first_part, left_over;    // parts > 1: sharers first_part .. + parts - 1
 };
 
-// The block's list of work.  prefix[e]: token tiles of the experts in front of e.
+// The list of work of a block, or of a pair.  prefix[e]: token tiles of the experts in front of e.
 template <int kTokens>
 struct Schedule {
+    using S = Shape<kTokens>;
     const Args& a;
     const int* prefix;
     int tiles, whole, sharers;
-    long long left;  // K blocks of the tiles that are left over
+    int left;  // K blocks of the tiles that are left over: fewer than blocks of up to 256
     int next, range0, range1;
 
     __device__ Schedule(const Args& args, const int* tile_prefix) : a(args), prefix(tile_prefix) {
-        const int P = gridDim.x;
+        const int P = gridDim.x / S::kBlocks, me = blockIdx.x / S::kBlocks;
         tiles = prefix[a.experts] * a.row_blocks;
         whole = tiles / P * P;
-        left = (long long)(tiles - whole) * a.k_blocks;
-        const long long most = left / min(kLeastRange, a.k_blocks);
-        sharers = most < P ? (most > 0 ? (int)most : (left > 0 ? 1 : 0)) : P;
-        next = blockIdx.x;
+        left = (tiles - whole) * a.k_blocks;
+        const int over = tiles - whole;
+        if (S::kBlocks > 1) {
+            // equal parts of each tile, as many as are worth their join
+            sharers = over ? over * max(1, min(P / over, a.k_blocks / S::kLeastRange)) : 0;
+        } else {
+            // equal shares of them all
+            sharers = min(P, left / min(S::kLeastRange, a.k_blocks));
+        }
+        next = me;
         range0 = range1 = 0;
-        if ((int)blockIdx.x < sharers) {
-            range0 = (int)(left * blockIdx.x / sharers);
-            range1 = (int)(left * (blockIdx.x + 1) / sharers);
+        if (me < sharers) {
+            range0 = left * me / sharers;
+            range1 = left * (me + 1) / sharers;
         }
     }
 
     // The sharer whose range holds K block p of the left-over tiles.
     __device__ int sharer(int p) const {
-        return (int)(((long long)(p + 1) * sharers + left - 1) / left) - 1;
+        return ((p + 1) * sharers + left - 1) / left - 1;
     }
 
     __device__ void place(int tile, Item& it) const {
@@ -129,13 +154,13 @@ struct Schedule {
         it.block = first / kW4Rows + lo + (long long)t * (kTokens / kW4Rows);
     }
 
-    // Where a block's sums of a cut tile lie.  Of a block's ranges only the first and
-    // the last can be parts of tiles; the last begins in front of its tile's share.
-    __device__ float4* part(int block, const Item& it) const {
-        const int begin = it.left_over * a.k_blocks;
-        const bool second = (int)(left * block / sharers) < begin;
-        return reinterpret_cast<float4*>(a.partials +
-                                         ((size_t)block * 2 + second) * Shape<kTokens>::kPartial);
+    // Where the sums of part i of a cut tile lie.  Of a sharer's ranges only the first and
+    // the last can be parts of tiles, and the last begins its tile, so it is part 0 there.
+    __device__ float4* part(const Item& it, int i) const {
+        const int sharer = it.first_part + i;
+        const bool second = i == 0 && left * sharer / sharers < it.left_over * a.k_blocks;
+        const size_t block = (size_t)sharer * S::kBlocks + blockIdx.x % S::kBlocks;
+        return reinterpret_cast<float4*>(a.partials + (block * 2 + second) * S::kPartial);
     }
 
     __device__ bool take(Item& it) {
@@ -144,7 +169,7 @@ struct Schedule {
             place(next, it);
             it.kb0 = 0;
             it.kb1 = a.k_blocks;
-            next += gridDim.x;
+            next += gridDim.x / S::kBlocks;
             return true;
         }
         if (range0 >= range1) return false;
@@ -160,9 +185,11 @@ struct Schedule {
     }
 };
 
-// kind::mxf4nvf4: E2M1 by E2M1, E4M3 scales, fp32 sums, 128 rows, n columns, 64 deep.
+// kind::mxf4nvf4: E2M1 by E2M1, E4M3 scales, fp32 sums, 128 rows per block, n columns,
+// 64 deep.
+template <int kBlocks>
 __device__ __forceinline__ constexpr uint32_t instruction(int n) {
-    return 1u << 7 | 1u << 10 | (uint32_t)(n / 8) << 17 | (uint32_t)(128 / 128) << 27;
+    return 1u << 7 | 1u << 10 | (uint32_t)(n / 8) << 17 | (uint32_t)kBlocks << 27;
 }
 
 // Shared-memory descriptors: rows of 128 bytes in the 128-byte swizzle, eight to a
@@ -174,26 +201,141 @@ __device__ __forceinline__ uint64_t scale_operand(uint32_t at) {
     return (uint64_t)((at & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
 }
 
-__device__ __forceinline__ void copy_scales(uint32_t columns, uint64_t from) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(columns), "l"(from)
-                 : "memory");
+// The instructions of one block's tensor cores, and of a pair's: those are issued by the
+// first block's thread, for the same addresses in both.
+template <int kBlocks>
+__device__ __forceinline__ void tmem_alloc(uint32_t to) {
+    if constexpr (kBlocks == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
 }
 
+template <int kBlocks>
+__device__ __forceinline__ void tmem_free(uint32_t at) {
+    if constexpr (kBlocks == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(at) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(at) : "memory");
+}
+
+template <int kBlocks>
+__device__ __forceinline__ void copy_scales(uint32_t columns, uint64_t from) {
+    if constexpr (kBlocks == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(columns), "l"(from)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(columns), "l"(from)
+                     : "memory");
+}
+
+template <int kBlocks>
 __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t scales_a, uint32_t scales_b, bool add) {
+    if constexpr (kBlocks == 1)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(scales_a), "r"(scales_b), "r"(add ? 1 : 0)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(scales_a), "r"(scales_b), "r"(add ? 1 : 0)
+            : "memory");
+}
+
+// `bar`, in each block, completes when all products issued so far have.
+template <int kBlocks>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (kBlocks == 1)
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+            ".b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// The address of the pair's first block's copy of a shared variable.
+__device__ __forceinline__ uint32_t in_first(uint32_t at) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(at));
+    return r;
+}
+
+// One box of tiles (see tile_map) from kilobyte y of tile (kb, block) on, into this
+// block's memory; `bar` may be the pair's first block's.
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int y, int kb,
+                                         int block, uint32_t bar) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(scales_a), "r"(scales_b), "r"(add ? 1 : 0)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+        "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar)
         : "memory");
 }
 
-// `bar` completes when all products issued so far have.
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
+// True for one thread of the warp, which calls it together.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// Arrives at the barrier at this address in the pair's first block.  (What has to be
+// done before it is: reads of tensor memory that were waited for.  A release at cluster
+// scope would wait for the warp's stores too, which took 540 ns.)
+__device__ __forceinline__ void arrive_at_first(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
+        " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar)
+        : "memory");
+}
+
+// Waits, boundedly, for a phase that a thread of the other block may complete.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
+                                             const volatile int* abort,
+                                             unsigned long long limit_ns) {
+    if (try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!try_wait_cluster(bar, parity)) {
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > limit_ns) return false;
+    }
+    return true;
+}
+
+// All threads of a pair (of a block).
+template <int kBlocks>
+__device__ __forceinline__ void sync_blocks() {
+    if constexpr (kBlocks == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // act(g) * u for g and u in bf16: act(g) = g * sigmoid(y), y = g or the argument of GeLU's
@@ -217,7 +359,8 @@ struct Barriers {
 };
 
 template <int kTokens, bool kGated>
-__global__ void __launch_bounds__(kThreads, 1) w4a4_gemm_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    w4a4_gemm_kernel(const Args a, const __grid_constant__ Maps maps) {
     using S = Shape<kTokens>;
     extern __shared__ __align__(1024) uint8_t dynamic[];
     // the swizzle goes by address: stages begin on multiples of 1024
@@ -231,14 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4a4_gemm_kernel(const Args a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_addr(shared);
     constexpr int kCopyWarp = 0, kIssueWarp = 1;
+    const int rank = blockIdx.x % S::kBlocks;  // in the pair
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == kIssueWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         smem_addr(&tmem_at))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == kIssueWarp) tmem_alloc<S::kBlocks>(smem_addr(&tmem_at));
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(smem_addr(&bars.full[i]), 1);
@@ -246,13 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4a4_gemm_kernel(const Args a) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.sums_full[i]), 1);
-            mbar_init(smem_addr(&bars.sums_empty[i]), kEpilogueWarps);
+            mbar_init(smem_addr(&bars.sums_empty[i]), kEpilogueWarps * S::kBlocks);
         }
         mbar_init(smem_addr(&bars.drained), 1);
         abort = 0;
         fence_mbar_init();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Without lists to read, the weight's first tiles are copied before the preceding
+    // kernel is done.
+    const bool early = a.start == nullptr;
+    if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
     // token tiles of each expert; one whose rows are not all inside has none
     if (tid == 0) prefix[0] = 0;
     for (int e = tid; e < a.experts; e += kThreads) {
@@ -276,81 +418,129 @@ __global__ void __launch_bounds__(kThreads, 1) w4a4_gemm_kernel(const Args a) {
         }
     }
     tmem_fence_before();
-    __syncthreads();
+    sync_blocks<S::kBlocks>();
+    if (S::kBlocks > 1) __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
 
     // Waits for a barrier's completion number `uses` (from 0); false, with the status
     // set, when it does not come in time.
     auto wait_lane = [&](uint64_t& bar, unsigned uses) {
-        if (mbar_wait_bounded(smem_addr(&bar), uses & 1, &abort, a.wait_ns)) return true;
+        if (S::kBlocks > 1 ? wait_cluster(smem_addr(&bar), uses & 1, &abort, a.wait_ns)
+                           : mbar_wait_bounded(smem_addr(&bar), uses & 1, &abort, a.wait_ns))
+            return true;
         abort = 1;
         *a.status = kKv8Timeout;
         return false;
     };
 
+    auto wait = [&](uint64_t& bar, unsigned uses) {  // the same answer for a whole warp
+        return __all_sync(0xffffffffu, wait_lane(bar, uses)) != 0;
+    };
+
     Schedule<kTokens> schedule(a, prefix);
-    Item it;
-    if (warp == kCopyWarp && lane == 0) {
+    Item it{};
+    if (warp == kCopyWarp) {
+        const bool issuer = elect_one();
+        // The weight's part of a stage, which the stage's bytes are announced with.
+        auto copy_weight = [&](unsigned n, int kb) {
+            if (issuer) {
+                const int stage = n % S::kStages;
+                const uint32_t at = smem + stage * S::kStageBytes;
+                const uint32_t bar = smem_addr(&bars.full[stage]);
+                const int weight = (it.expert * a.row_blocks + it.weight) * S::kBlocks + rank;
+                if constexpr (S::kBlocks == 1) {
+                    mbar_arrive_expect_tx(bar, kW4Tile + S::columns(it.tokens) * 128 + kW4Scales);
+                    bulk_copy_g2s(at, a.packed + ((size_t)weight * a.k_blocks + kb) * kW4Tile,
+                                  kW4Tile, bar);
+                } else {
+                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
+                    copy_box(at, &maps.weight, 0, kb, weight, in_first(bar));
+                }
+            }
+            __syncwarp();
+        };
+        unsigned ahead = 0;
+        if (early) {
+            Schedule<kTokens> first = schedule;
+            while (ahead < S::kStages && first.take(it))
+                for (int kb = it.kb0; kb < it.kb1 && ahead < S::kStages && !(a.stall && ahead);
+                     ++kb, ++ahead)
+                    copy_weight(ahead, kb);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
         unsigned n = 0;  // stages filled
         bool ok = true;
         while (ok && schedule.take(it)) {
-            const uint8_t* w = a.packed + ((size_t)it.expert * a.row_blocks + it.weight) *
-                                              a.k_blocks * kW4Tile;
             const uint8_t* x = a.rows + (size_t)it.block * a.k_blocks * kW4Tile;
-            const size_t block_bytes = (size_t)a.k_blocks * kW4Tile;
-            // eight rows of 128 bytes at a time
-            const uint32_t codes0 = (uint32_t)((min(it.tokens, 128) + 15) / 16 * 2048);
-            const uint32_t codes1 = (uint32_t)((max(it.tokens - 128, 0) + 15) / 16 * 2048);
-            const uint32_t bytes = kW4Tile + codes0 + kW4Scales + (codes1 ? codes1 + kW4Scales : 0);
+            const int columns = S::columns(it.tokens);
+            // a pair's block has half of the columns, which are 256 or, in one tile, 128
+            const int block = (int)it.block + (columns > 128 ? rank : 0);
+            const int y = columns > 128 ? 0 : 8 * rank;
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
                 if (n >= S::kStages) {
-                    ok = wait_lane(bars.empty[stage], n / S::kStages - 1);
+                    ok = wait(bars.empty[stage], n / S::kStages - 1);
                     if (!ok) break;
                 }
                 if (a.stall && n >= 1) {  // testing: nothing comes any more
-                    wait_lane(bars.drained, 0);
+                    wait(bars.drained, 0);
                     ok = false;
                     break;
                 }
-                const uint32_t bar = smem_addr(&bars.full[stage]);
-                const uint32_t at = smem + stage * S::kStageBytes;
-                mbar_arrive_expect_tx(bar, bytes);
-                bulk_copy_g2s(at, w + (size_t)kb * kW4Tile, kW4Tile, bar);
-                const uint8_t* t = x + (size_t)kb * kW4Tile;
-                bulk_copy_g2s(at + S::kBAt, t, codes0, bar);
-                bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
-                if (codes1) {
-                    t += block_bytes;
-                    bulk_copy_g2s(at + S::kBAt + kW4Codes, t, codes1, bar);
-                    bulk_copy_g2s(at + S::kBScalesAt + kW4Scales, t + kW4Codes, kW4Scales, bar);
+                if (n >= ahead) copy_weight(n, kb);
+                if (issuer) {
+                    const uint32_t at = smem + stage * S::kStageBytes;
+                    const uint32_t bar = smem_addr(&bars.full[stage]);
+                    if constexpr (S::kBlocks == 1) {
+                        const uint8_t* t = x + (size_t)kb * kW4Tile;
+                        bulk_copy_g2s(at + S::kBAt, t, columns * 128, bar);
+                        bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
+                    } else {
+                        copy_box(at + S::kBAt, &maps.codes, y, kb, block, in_first(bar));
+                        copy_box(at + S::kBScalesAt, &maps.scales, 16, kb, (int)it.block,
+                                 in_first(bar));
+                    }
                 }
+                __syncwarp();
             }
         }
+        // the last products' word has come before the barriers that it goes to are left
+        for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n && ok; ++i)
+            ok = wait(bars.empty[i % S::kStages], i / S::kStages);
         if (abort) {
             // copies under way end before the memory that they write is left; these waits
             // heed nobody's
             const int none = 0;
-            for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-                mbar_wait_bounded(smem_addr(&bars.full[i % S::kStages]), i / S::kStages & 1, &none);
+            if (rank == 0)
+                for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
+                    mbar_wait_bounded(smem_addr(&bars.full[i % S::kStages]), i / S::kStages & 1,
+                                      &none, a.wait_ns);
+            else  // reported to the other block: time enough for any copy
+                for (const unsigned long long t0 = global_timer_ns();
+                     global_timer_ns() - t0 < 100000;)
+                    __nanosleep(1000);
         }
-    } else if (warp == kIssueWarp && lane == 0) {
+    } else if (warp == kIssueWarp && rank == 0) {
+        // The whole warp runs the loop and one thread issues: in a branch of one thread from
+        // the start, each of these instructions took about 60 cycles (their operands have to
+        // be the same for the warp), 1030 for a stage's.
+        const bool issuer = elect_one();
         unsigned n = 0, items = 0;
         bool ok = true;
         while (ok && schedule.take(it)) {
             const unsigned sums = items % S::kSums;
             if (items >= S::kSums) {
-                ok = wait_lane(bars.sums_empty[sums], items / S::kSums - 1);
+                ok = wait(bars.sums_empty[sums], items / S::kSums - 1);
                 if (!ok) break;
             }
             tmem_fence_after();
             const uint32_t d = tmem + sums * kTokens;
-            const int columns = (it.tokens + 15) / 16 * 16;
-            const uint32_t idesc = instruction(columns);
+            const int columns = S::columns(it.tokens);
+            const uint32_t idesc = instruction<S::kBlocks>(columns);
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
-                ok = wait_lane(bars.full[stage], n / S::kStages);
+                ok = wait(bars.full[stage], n / S::kStages);
                 if (!ok) break;
                 const uint32_t at = smem + stage * S::kStageBytes;
                 // the stage's own columns: what read them last has completed, as the
@@ -359,205 +549,255 @@ __global__ void __launch_bounds__(kThreads, 1) w4a4_gemm_kernel(const Args a) {
                 const uint32_t scales_b = scales_a + 16;
                 const uint64_t from_a = scale_operand(at + kW4Codes);
                 const uint64_t from_b = scale_operand(at + S::kBScalesAt);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    copy_scales(scales_a + 4 * j, from_a + j * (512 >> 4));
-                    copy_scales(scales_b + j * (kTokens / 32), from_b + j * (512 >> 4));
-                    if (kTokens == 256 && columns > 128)
-                        copy_scales(scales_b + j * (kTokens / 32) + 4,
-                                    from_b + (kW4Scales >> 4) + j * (512 >> 4));
-                }
                 const uint64_t op_a = operand(at), op_b = operand(at + S::kBAt);
+                if (issuer) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    multiply(d, op_a + j * 2, op_b + j * 2, idesc, scales_a + 4 * j,
-                             scales_b + j * (kTokens / 32), kb > it.kb0 || j > 0);
-                commit(smem_addr(&bars.empty[stage]));
+                    for (int j = 0; j < 4; ++j) {
+                        copy_scales<S::kBlocks>(scales_a + 4 * j, from_a + j * (512 >> 4));
+                        copy_scales<S::kBlocks>(scales_b + j * (kTokens / 32),
+                                                from_b + j * (512 >> 4));
+                        if (kTokens == 256 && columns > 128)
+                            copy_scales<S::kBlocks>(scales_b + j * (kTokens / 32) + 4,
+                                                    from_b + (kW4Scales >> 4) + j * (512 >> 4));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        multiply<S::kBlocks>(d, op_a + j * 2, op_b + j * 2, idesc,
+                                             scales_a + 4 * j, scales_b + j * (kTokens / 32),
+                                             kb > it.kb0 || j > 0);
+                    commit<S::kBlocks>(smem_addr(&bars.empty[stage]));
+                }
+                __syncwarp();
             }
             if (!ok) break;
-            commit(smem_addr(&bars.sums_full[sums]));
+            if (issuer) commit<S::kBlocks>(smem_addr(&bars.sums_full[sums]));
+            __syncwarp();
             ++items;
         }
         if (abort) {
             // products under way end before the memory that they read is left
             const int none = 0;
-            commit(smem_addr(&bars.drained));
+            if (issuer) commit<S::kBlocks>(smem_addr(&bars.drained));
             mbar_wait_bounded(smem_addr(&bars.drained), 0, &none);
         }
-    } else if (warp >= 2) {
-        const int quadrant = warp & 3, half = (warp - 2) >> 2, eid = tid - 64;
-        constexpr int kHalf = kTokens / 2, kChunks = kHalf / 32;
-        const int row = quadrant * 32 + lane;  // of the weight's tile
+    } else if (warp > kIssueWarp) {
+        if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
+        // a warp reads 32 rows of a share of the columns
+        const int quadrant = warp & 3, first = (warp - 2) / 4 * (kTokens * 4 / kEpilogueWarps);
+        const int eid = tid - 64;
+        constexpr int kShare = kTokens * 4 / kEpilogueWarps;
         const uint32_t lanes = tmem + ((uint32_t)(quadrant * 32) << 16);
         bool ok = true;
         for (unsigned items = 0; schedule.take(it); ++items) {
             const unsigned sums = items % S::kSums;
-            // chunks of 32 tokens that this warp has
-            const int mine = min(max((it.tokens - half * kHalf + 31) / 32, 0), kChunks);
             float* const scales = row_scale[items & 1];
-            ok = ok && __all_sync(0xffffffffu, wait_lane(bars.sums_full[sums], items / S::kSums));
-            if (ok && eid < kTokens)
-                scales[eid] = eid < it.tokens ? a.row_scales[it.token0 + eid] : 0.0f;
-            tmem_fence_after();
-            const uint32_t from = lanes + sums * kTokens + half * kHalf;
+            if (eid < kTokens) scales[eid] = eid < it.tokens ? a.row_scales[it.token0 + eid] : 0.0f;
+            const uint32_t from = lanes + sums * kTokens + first;
             const bool up = kGated && lane >= 16;
             const float scale = up ? (a.scales_b ? a.scales_b[it.expert] : a.scale_b)
                                    : (a.scales_a ? a.scales_a[it.expert] : a.scale_a);
             named_barrier_sync(1, kEpilogueThreads);  // row scales are there
-            uint32_t p[kChunks][16];  // pairs of tokens, bf16
-            auto pack = [&](int c, const float(&x)[32]) {
-                const float2* r = reinterpret_cast<const float2*>(scales + half * kHalf + 32 * c);
+            ok = ok && wait(bars.sums_full[sums], items / S::kSums);
+            tmem_fence_after();
+            const int block = it.weight * S::kBlocks + rank;
+            // of a pair of lanes that trade: the even one's
+            const int feature = kGated ? block * 64 + quadrant * 16 + (lane & 14)
+                                       : block * kW4Rows + quadrant * 32 + (lane & 30);
+            __nv_bfloat16* const out = a.out + (size_t)it.token0 * a.N + feature;
+            // Sums of two tokens, in bf16.
+            auto pack = [&](int column, float v0, float v1) {
+                const float2 r = *reinterpret_cast<const float2*>(scales + column);
+                return bf16x2(v0 * scale * r.x, v1 * scale * r.y);
+            };
+            // Stores four pairs of tokens, column on.  Neighbouring lanes trade, for two
+            // features of one token each.  Of a gate/up pair 16 lanes have gate, 16 up, of the
+            // same features: the first take the even tokens, the others the odd ones.
+            auto emit = [&](int column, const uint32_t(&v)[4]) {
+                const bool odd = lane & 1;
+                if (kGated) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    p[c][j] = bf16x2(x[2 * j] * scale * r[j].x, x[2 * j + 1] * scale * r[j].y);
+                    for (int j = 0; j < 4; j += 2) {
+                        float h[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j + k], 16);
+                            h[k] = gated(a.act, up ? bf16_hi(o) : bf16_lo(v[j + k]),
+                                         up ? bf16_hi(v[j + k]) : bf16_lo(o));
+                        }
+                        const uint32_t own = bf16x2(h[0], h[1]);
+                        const uint32_t o = __shfl_xor_sync(0xffffffffu, own, 1);
+                        const uint32_t w = odd ? prmt(o, own, 0x7632) : prmt(own, o, 0x5410);
+                        const int token = column + 2 * j + (up ? 1 : 0) + (odd ? 2 : 0);
+                        if (token < it.tokens && feature < a.N)
+                            *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N) = w;
+                    }
+                } else if (a.N & 1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (column + j < it.tokens && feature + odd < a.N)
+                            *reinterpret_cast<uint16_t*>(out + (size_t)(column + j) * a.N + odd) =
+                                (uint16_t)(j & 1 ? v[j / 2] >> 16 : v[j / 2]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j], 1);
+                        const uint32_t w = odd ? prmt(o, v[j], 0x7632) : prmt(v[j], o, 0x5410);
+                        const int token = column + 2 * j + odd;
+                        if (token < it.tokens && feature < a.N)
+                            *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N) = w;
+                    }
+                }
             };
             auto give_back = [&] {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&bars.sums_empty[sums]));
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(smem_addr(&bars.sums_empty[sums]));
+                    else arrive_at_first(smem_addr(&bars.sums_empty[sums]));
+                }
             };
-            bool store = ok;
+            // Columns that this warp has: eight at a time.
+            const int end = min(it.tokens, first + kShare);
             if (it.parts == 1) {
-                if (ok) {
+                if constexpr (S::kSums > 1) {
+                    // the other accumulator is at work meanwhile
+#pragma unroll 1
+                    for (int column = first; column < end && ok; column += 8) {
+                        float x[8];
+                        tmem_load8(from + column - first, x);
+                        const uint32_t v[4] = {
+                            pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
+                            pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
+                        emit(column, v);
+                    }
+                    give_back();
+                } else {
+                    // the only one: given back before its columns are stored
+                    uint32_t p[kShare / 8][4];
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine) {
-                            float x[32];
+                    for (int c = 0; c < kShare / 32; ++c) {
+                        float x[32];
+                        const bool some = ok && first + 32 * c < end;
+                        if (some) {
                             tmem_load32(from + 32 * c, x);
                             tmem_wait_load(x);
-                            pack(c, x);
                         }
-                }
-                give_back();
-            } else {
-                float4* to = schedule.part(blockIdx.x, it) + half * (kHalf / 4) * kW4Rows + row;
-                if (ok) {
+                        if (c + 1 == kShare / 32) give_back();
+                        if (some) {
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine) {
-                            float x[32];
-                            tmem_load32(from + 32 * c, x);
-                            tmem_wait_load(x);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                to[(8 * c + j) * kW4Rows] =
-                                    make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                            for (int j = 0; j < 16; ++j)
+                                p[4 * c + j / 4][j % 4] =
+                                    pack(first + 32 * c + 2 * j, x[2 * j], x[2 * j + 1]);
                         }
+                    }
+#pragma unroll
+                    for (int g = 0; g < kShare / 8; ++g)
+                        if (ok && first + 8 * g < end) emit(first + 8 * g, p[g]);
                 }
-                give_back();
-                __threadfence();
-                named_barrier_sync(1, kEpilogueThreads);
-                // an abandoned range is counted too: the counter is left at 0 all the same
-                if (eid == 0) {
-                    int* const counter = a.counters + it.left_over;
-                    const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
-                    if (last) *counter = 0;
-                    last_part = last;
-                }
-                named_barrier_sync(1, kEpilogueThreads);
-                store = ok && last_part;
-                if (store) {
-                    __threadfence();
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine) {
-                            float x[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-                            for (int i = 0; i < it.parts; ++i) {
-                                const float4* part = schedule.part(it.first_part + i, it) +
-                                                     half * (kHalf / 4) * kW4Rows + row;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const float4 y = __ldcg(part + (8 * c + j) * kW4Rows);
-                                    x[4 * j] += y.x;
-                                    x[4 * j + 1] += y.y;
-                                    x[4 * j + 2] += y.z;
-                                    x[4 * j + 3] += y.w;
-                                }
-                            }
-                            pack(c, x);
-                        }
+                continue;
+            }
+            // A part of a tile: [column / 4][row][4] floats.
+            const int at = quadrant * 32 + lane;
+            if (ok) {
+                float4* const to = schedule.part(it, (int)blockIdx.x / S::kBlocks - it.first_part);
+#pragma unroll 1
+                for (int column = first; column < end; column += 8) {
+                    float x[8];
+                    tmem_load8(from + column - first, x);
+                    to[column / 4 * kW4Rows + at] = make_float4(x[0], x[1], x[2], x[3]);
+                    to[(column / 4 + 1) * kW4Rows + at] = make_float4(x[4], x[5], x[6], x[7]);
                 }
             }
-            if (!store) continue;
-            const int t0 = half * kHalf;
-            if (kGated) {
-                // 16 lanes have gate, 16 up, of the same features: the first take the even
-                // tokens, the others the odd ones, then neighbours trade for two features
-                const int feature = it.weight * 64 + quadrant * 16 + (lane & 14);
-                if (feature < a.N) {
-                    __nv_bfloat16* const out = a.out + (size_t)it.token0 * a.N + feature;
+            give_back();
+            __threadfence();
+            named_barrier_sync(1, kEpilogueThreads);
+            // an abandoned part is counted too: the counter is left at 0 all the same
+            if (eid == 0) {
+                int* const counter = a.counters + it.left_over * S::kBlocks + rank;
+                const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
+                if (last) *counter = 0;
+                last_part = last;
+            }
+            named_barrier_sync(1, kEpilogueThreads);
+            if (!ok || !last_part) continue;
+            __threadfence();
+            const float4* const part0 = schedule.part(it, 0);
+            const float4* const part1 = schedule.part(it, 1);  // the others follow it
+            constexpr size_t kNext = (size_t)S::kBlocks * 2 * S::kPartial / 4;
+#pragma unroll 1
+            for (int column = first; column < end; column += 8) {
+                float x[8] = {};
+                const int here = column / 4 * kW4Rows + at;
+#pragma unroll 1
+                for (int i = 0; i < it.parts; i += kJoin) {
+                    float4 y[kJoin][2];
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine) {
+                    for (int k = 0; k < kJoin; ++k) {
+                        y[k][0] = y[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i + k < it.parts) {
+                            const float4* part =
+                                (i + k == 0 ? part0 : part1 + (i + k - 1) * kNext) + here;
+                            y[k][0] = __ldcg(part);
+                            y[k][1] = __ldcg(part + kW4Rows);
+                        }
+                    }
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                float h[2];
+                    for (int k = 0; k < kJoin; ++k)
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint32_t v = p[c][j + k];
-                                    const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 16);
-                                    h[k] = gated(a.act, up ? bf16_hi(o) : bf16_lo(v),
-                                                 up ? bf16_hi(v) : bf16_lo(o));
-                                }
-                                const uint32_t v = bf16x2(h[0], h[1]);
-                                const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
-                                const uint32_t w =
-                                    lane & 1 ? prmt(o, v, 0x7632) : prmt(v, o, 0x5410);
-                                const int token =
-                                    t0 + 32 * c + 2 * j + (up ? 1 : 0) + 2 * (lane & 1);
-                                if (token < it.tokens)
-                                    *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N) = w;
-                            }
+                        for (int j = 0; j < 2; ++j) {
+                            x[4 * j] += y[k][j].x;
+                            x[4 * j + 1] += y[k][j].y;
+                            x[4 * j + 2] += y[k][j].z;
+                            x[4 * j + 3] += y[k][j].w;
                         }
                 }
-            } else {
-                const int feature = it.weight * kW4Rows + row;
-                __nv_bfloat16* const out = a.out + (size_t)it.token0 * a.N + feature;
-                if (a.N & 1) {
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine && feature < a.N) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int token = t0 + 32 * c + j;
-                                const uint32_t v = p[c][j / 2];
-                                if (token < it.tokens)
-                                    *reinterpret_cast<uint16_t*>(out + (size_t)token * a.N) =
-                                        (uint16_t)(j & 1 ? v >> 16 : v);
-                            }
-                        }
-                } else {
-                    // neighbours trade: an even lane has both features of an even token
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        if (c < mine) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const uint32_t v = p[c][j];
-                                const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
-                                const uint32_t w =
-                                    lane & 1 ? prmt(o, v, 0x7632) : prmt(v, o, 0x5410);
-                                const int token = t0 + 32 * c + 2 * j + (lane & 1);
-                                if (token < it.tokens && feature < a.N)
-                                    *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N -
-                                                                 (lane & 1)) = w;
-                            }
-                        }
-                }
+                const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
+                                       pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
+                emit(column, v);
             }
         }
     }
+    // a pair's first block reads the other's memory and both signal each other's barriers:
+    // neither leaves before the other is done
     tmem_fence_before();
-    __syncthreads();
-    if (warp == kIssueWarp)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
-                     : "memory");
+    __syncwarp();
+    sync_blocks<S::kBlocks>();
+    if (warp == kIssueWarp) tmem_free<S::kBlocks>(tmem);
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's function, through the runtime (the library does not link the driver).
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> known{nullptr};
+    void* f = known.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        known.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// A map of `blocks` row blocks of tiles for boxes of `rows` kilobytes of `tiles` blocks.
+bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, int rows,
+              int tiles) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t size[4] = {256, kW4Tile / 1024, (cuuint64_t)k_blocks, (cuuint64_t)blocks};
+    const cuuint64_t stride[3] = {1024, kW4Tile, (cuuint64_t)k_blocks * kW4Tile};
+    const cuuint32_t box[4] = {256, (cuuint32_t)rows, 1, (cuuint32_t)tiles}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, const_cast<void*>(at), size, stride, box,
+                  step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kTokens, bool kGated>
-cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
+cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s) {
     static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -570,16 +810,19 @@ cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
         if (dev < 64) allowed[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(num_sms);
+    cfg.gridDim = dim3(num_sms / Shape<kTokens>::kBlocks * Shape<kTokens>::kBlocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Shape<kTokens>::kShared;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = Shape<kTokens>::kBlocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a);
+    cfg.numAttrs = Shape<kTokens>::kBlocks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a, maps);
 }
 
 // Tokens per tile: rows of an expert on average, as far as the host knows them.
@@ -616,9 +859,20 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
     a.partials = reinterpret_cast<float*>(partials);
     a.wait_ns = test_wait_ns();
     a.stall = test_stall();
-    if (wide(p.M, p.groups.experts))
-        return p.streams == 2 ? launch<256, true>(a, num_sms, s) : launch<256, false>(a, num_sms, s);
-    return p.streams == 2 ? launch<128, true>(a, num_sms, s) : launch<128, false>(a, num_sms, s);
+    Maps maps{};
+    if (wide(p.M, p.groups.experts)) {
+        const long long blocks = w4_token_blocks(p.M, p.groups.experts);
+        if (!tile_map(&maps.weight, p.packed, a.k_blocks, (long long)a.experts * a.row_blocks,
+                      kW4Tile / 1024, 1) ||
+            !tile_map(&maps.codes, p.rows, a.k_blocks, blocks, kW4Codes / 1024, 1) ||
+            !tile_map(&maps.scales, p.rows, a.k_blocks, blocks, kW4Scales / 1024, 2))
+            return cudaErrorInvalidValue;
+        a.row_blocks /= Shape<256>::kBlocks;
+        return p.streams == 2 ? launch<256, true>(a, maps, num_sms, s)
+                              : launch<256, false>(a, maps, num_sms, s);
+    }
+    return p.streams == 2 ? launch<128, true>(a, maps, num_sms, s)
+                          : launch<128, false>(a, maps, num_sms, s);
 }
 
 }  // namespace nvf
