@@ -41,13 +41,14 @@ constexpr int kSuper = 16;
 
 template <int kTokens>
 struct Shape {
-    // Blocks that share a tile: a pair takes 256 rows of the weight by 256 tokens, each
-    // block copies its 128 rows and half of the tokens, and the tensor cores of both read
-    // both halves.
+    // Blocks that share a tile.  One alone has 128 rows of the weight as lanes and tokens as
+    // columns, as many as there are.  A pair has 256 tokens by 256 rows of the weight: each
+    // block copies its 128 tokens, the lanes of its accumulator, and half of the weight's
+    // rows, the columns; the tensor cores of both read both halves.
     static constexpr int kBlocks = kTokens == 256 ? 2 : 1;
     static constexpr int kStages = kTokens == 256 ? 5 : 6;
     static constexpr int kSums = kTokens == 256 ? 1 : 2;  // accumulators in turn
-    static constexpr int kBAt = kW4Tile;                  // tokens' codes in a stage
+    static constexpr int kBAt = kW4Tile;                  // the columns' codes in a stage
     static constexpr int kBScalesAt = kBAt + kTokens / kBlocks * 128;
     static constexpr int kStageBytes = kBScalesAt + kTokens * 16;
     static constexpr int kShared = 1024 + kStages * kStageBytes;
@@ -58,9 +59,9 @@ struct Shape {
     static constexpr int kPartial = kW4Rows * kTokens;  // floats
     // K blocks that a range of a cut tile has at least.
     static constexpr int kLeastRange = kBlocks > 1 ? 16 : 2;
-    // Columns of a tile's products: a pair's halves are whole tiles, or those of one.
+    // Columns of a tile's products.
     static __device__ __forceinline__ int columns(int tokens) {
-        return kBlocks == 1 ? (tokens + 15) / 16 * 16 : tokens > 128 ? 256 : 128;
+        return kBlocks == 1 ? (tokens + 15) / 16 * 16 : 256;
     }
 };
 
@@ -74,6 +75,7 @@ struct Args {
     const float* scales_b;
     float scale_a, scale_b;
     int M, N, k_blocks, row_blocks, experts, act;  // row_blocks: of a tile's rows
+    int vector;  // bytes that 16 features of a row may be stored by: 32, 16, or 2
     int* status;
     int* counters;
     float* partials;
@@ -85,7 +87,7 @@ struct Args {
 // pairs: what one block copies is reported to the other's barrier, which the plain bulk
 // copies cannot.  Boxes: a whole tile, a tile's codes, the scales of two tiles.
 struct Maps {
-    CUtensorMap weight, codes, scales;
+    CUtensorMap rows, codes, scales;  // the rows' whole tiles; the weight's
 };
 
 // A range of K blocks of one tile.
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it{};
     if (warp == kCopyWarp) {
         const bool issuer = elect_one();
-        // The weight's part of a stage, which the stage's bytes are announced with.
+        // The weight's part of a stage; the stage's bytes are announced with it.
         auto copy_weight = [&](unsigned n, int kb) {
             if (issuer) {
                 const int stage = n % S::kStages;
@@ -455,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kW4Tile, bar);
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
-                    copy_box(at, &maps.weight, 0, kb, weight, in_first(bar));
+                    copy_box(at + S::kBAt, &maps.codes, 0, kb, weight, in_first(bar));
+                    copy_box(at + S::kBScalesAt, &maps.scales, 16, kb, weight - rank,
+                             in_first(bar));
                 }
             }
             __syncwarp();
@@ -474,9 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && schedule.take(it)) {
             const uint8_t* x = a.rows + (size_t)it.block * a.k_blocks * kW4Tile;
             const int columns = S::columns(it.tokens);
-            // a pair's block has half of the columns, which are 256 or, in one tile, 128
-            const int block = (int)it.block + (columns > 128 ? rank : 0);
-            const int y = columns > 128 ? 0 : 8 * rank;
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
                 if (n >= S::kStages) {
@@ -497,9 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bulk_copy_g2s(at + S::kBAt, t, columns * 128, bar);
                         bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
                     } else {
-                        copy_box(at + S::kBAt, &maps.codes, y, kb, block, in_first(bar));
-                        copy_box(at + S::kBScalesAt, &maps.scales, 16, kb, (int)it.block,
-                                 in_first(bar));
+                        copy_box(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
                     }
                 }
                 __syncwarp();
@@ -556,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         copy_scales<S::kBlocks>(scales_a + 4 * j, from_a + j * (512 >> 4));
                         copy_scales<S::kBlocks>(scales_b + j * (kTokens / 32),
                                                 from_b + j * (512 >> 4));
-                        if (kTokens == 256 && columns > 128)
+                        if (kTokens == 256)
                             copy_scales<S::kBlocks>(scales_b + j * (kTokens / 32) + 4,
                                                     from_b + (kW4Scales >> 4) + j * (512 >> 4));
                     }
@@ -582,12 +581,169 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp > kIssueWarp) {
         if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
-        // a warp reads 32 rows of a share of the columns
-        const int quadrant = warp & 3, first = (warp - 2) / 4 * (kTokens * 4 / kEpilogueWarps);
-        const int eid = tid - 64;
+        // a warp reads 32 lanes of a share of the columns
         constexpr int kShare = kTokens * 4 / kEpilogueWarps;
+        const int quadrant = warp & 3, first = (warp - 2) / 4 * kShare, eid = tid - 64;
         const uint32_t lanes = tmem + ((uint32_t)(quadrant * 32) << 16);
         bool ok = true;
+        // Counts a part of a cut tile, whose sums have been written, or which was abandoned:
+        // the counter is left at 0 all the same.  True in the block that is last.
+        auto count_part = [&] {
+            __threadfence();
+            named_barrier_sync(1, kEpilogueThreads);
+            if (eid == 0) {
+                int* const counter = a.counters + it.left_over * S::kBlocks + rank;
+                const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
+                if (last) *counter = 0;
+                last_part = last;
+            }
+            named_barrier_sync(1, kEpilogueThreads);
+            if (last_part) __threadfence();
+            return last_part != 0;
+        };
+        auto give_back = [&](unsigned sums) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(smem_addr(&bars.sums_empty[sums]));
+                else arrive_at_first(smem_addr(&bars.sums_empty[sums]));
+            }
+        };
+        // Sums of eight columns of a cut tile, parts in order, kJoin of them asked for at a
+        // time: [column / 4][lane][4] floats.
+        auto join8 = [&](int column, float(&x)[8]) {
+            const int here = column / 4 * kW4Rows + quadrant * 32 + lane;
+            const float4* const part0 = schedule.part(it, 0) + here;
+            const float4* const part1 = schedule.part(it, 1) + here;  // the others follow it
+            constexpr size_t kNext = (size_t)S::kBlocks * 2 * S::kPartial / 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < it.parts; i += kJoin) {
+                float4 y[kJoin][2];
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) {
+                    y[k][0] = y[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i + k < it.parts) {
+                        const float4* part = i + k == 0 ? part0 : part1 + (i + k - 1) * kNext;
+                        y[k][0] = __ldcg(part);
+                        y[k][1] = __ldcg(part + kW4Rows);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x[4 * j] += y[k][j].x;
+                        x[4 * j + 1] += y[k][j].y;
+                        x[4 * j + 2] += y[k][j].z;
+                        x[4 * j + 3] += y[k][j].w;
+                    }
+            }
+        };
+        if constexpr (S::kBlocks > 1) {
+            // a token per lane: its features lie side by side
+            const int token = rank * kW4Rows + quadrant * 32 + lane;
+            for (unsigned items = 0; schedule.take(it); ++items) {
+                const bool live = token < it.tokens;
+                const float r = live ? a.row_scales[it.token0 + token] : 0.0f;
+                const float scale_a = a.scales_a ? a.scales_a[it.expert] : a.scale_a;
+                const float scale_b = a.scales_b ? a.scales_b[it.expert] : a.scale_b;
+                __nv_bfloat16* const out =
+                    a.out + (size_t)(it.token0 + token) * a.N +
+                    (it.weight * 256 + first) / (kGated ? 2 : 1);
+                const int room = a.N - (it.weight * 256 + first) / (kGated ? 2 : 1);
+                auto store16 = [&](int feature, const uint32_t(&w)[8]) {
+                    if (!live || feature >= room) return;
+                    __nv_bfloat16* const to = out + feature;
+                    if (a.vector == 32 && feature + 16 <= room) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                                     "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                     : "memory");
+                    } else if (a.vector == 16 && feature + 16 <= room) {
+                        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (feature + j < room)
+                                reinterpret_cast<uint16_t*>(to)[j] =
+                                    (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+                    }
+                };
+                // 32 columns: as many features, or 16 of gate and 16 of up
+                auto emit = [&](int c, const float(&x)[32]) {
+                    uint32_t w[8];
+                    if (kGated) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t g =
+                                bf16x2(x[2 * j] * scale_a * r, x[2 * j + 1] * scale_a * r);
+                            const uint32_t u = bf16x2(x[16 + 2 * j] * scale_b * r,
+                                                      x[17 + 2 * j] * scale_b * r);
+                            w[j] = bf16x2(gated(a.act, bf16_lo(g), bf16_lo(u)),
+                                          gated(a.act, bf16_hi(g), bf16_hi(u)));
+                        }
+                        store16(16 * c, w);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                w[j] = bf16x2(x[16 * h + 2 * j] * scale_a * r,
+                                              x[16 * h + 2 * j + 1] * scale_a * r);
+                            store16(32 * c + 16 * h, w);
+                        }
+                    }
+                };
+                ok = ok && wait(bars.sums_full[0], items);
+                tmem_fence_after();
+                if (it.parts == 1) {
+                    // the accumulator is given back before its columns are looked at
+                    float x[kShare / 32][32];
+                    if (ok) {
+#pragma unroll
+                        for (int c = 0; c < kShare / 32; ++c)
+                            tmem_load32(lanes + first + 32 * c, x[c]);
+#pragma unroll
+                        for (int c = 0; c < kShare / 32; ++c) tmem_wait_load(x[c]);
+                    }
+                    give_back(0);
+                    if (ok) {
+#pragma unroll
+                        for (int c = 0; c < kShare / 32; ++c) emit(c, x[c]);
+                    }
+                    continue;
+                }
+                if (ok) {
+                    float4* const to =
+                        schedule.part(it, (int)blockIdx.x / S::kBlocks - it.first_part) +
+                        quadrant * 32 + lane;
+#pragma unroll 1
+                    for (int column = first; column < first + kShare; column += 8) {
+                        float x[8];
+                        tmem_load8(lanes + column, x);
+                        to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
+                        to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
+                    }
+                }
+                give_back(0);
+                if (!count_part() || !ok) continue;
+#pragma unroll 1
+                for (int c = 0; c < kShare / 32; ++c) {
+                    float x[32];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float y[8];
+                        join8(first + 32 * c + 8 * h, y);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[8 * h + j] = y[j];
+                    }
+                    emit(c, x);
+                }
+            }
+        } else
         for (unsigned items = 0; schedule.take(it); ++items) {
             const unsigned sums = items % S::kSums;
             float* const scales = row_scale[items & 1];
@@ -648,109 +804,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            auto give_back = [&] {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive(smem_addr(&bars.sums_empty[sums]));
-                    else arrive_at_first(smem_addr(&bars.sums_empty[sums]));
-                }
-            };
             // Columns that this warp has: eight at a time.
             const int end = min(it.tokens, first + kShare);
             if (it.parts == 1) {
-                if constexpr (S::kSums > 1) {
-                    // the other accumulator is at work meanwhile
+                // the other accumulator is at work meanwhile
 #pragma unroll 1
-                    for (int column = first; column < end && ok; column += 8) {
-                        float x[8];
-                        tmem_load8(from + column - first, x);
-                        const uint32_t v[4] = {
-                            pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
-                            pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
-                        emit(column, v);
-                    }
-                    give_back();
-                } else {
-                    // the only one: given back before its columns are stored
-                    uint32_t p[kShare / 8][4];
-#pragma unroll
-                    for (int c = 0; c < kShare / 32; ++c) {
-                        float x[32];
-                        const bool some = ok && first + 32 * c < end;
-                        if (some) {
-                            tmem_load32(from + 32 * c, x);
-                            tmem_wait_load(x);
-                        }
-                        if (c + 1 == kShare / 32) give_back();
-                        if (some) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                p[4 * c + j / 4][j % 4] =
-                                    pack(first + 32 * c + 2 * j, x[2 * j], x[2 * j + 1]);
-                        }
-                    }
-#pragma unroll
-                    for (int g = 0; g < kShare / 8; ++g)
-                        if (ok && first + 8 * g < end) emit(first + 8 * g, p[g]);
+                for (int column = first; column < end && ok; column += 8) {
+                    float x[8];
+                    tmem_load8(from + column - first, x);
+                    const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
+                                           pack(column + 4, x[4], x[5]),
+                                           pack(column + 6, x[6], x[7])};
+                    emit(column, v);
                 }
+                give_back(sums);
                 continue;
             }
-            // A part of a tile: [column / 4][row][4] floats.
-            const int at = quadrant * 32 + lane;
             if (ok) {
-                float4* const to = schedule.part(it, (int)blockIdx.x / S::kBlocks - it.first_part);
+                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part) +
+                                   quadrant * 32 + lane;
 #pragma unroll 1
                 for (int column = first; column < end; column += 8) {
                     float x[8];
                     tmem_load8(from + column - first, x);
-                    to[column / 4 * kW4Rows + at] = make_float4(x[0], x[1], x[2], x[3]);
-                    to[(column / 4 + 1) * kW4Rows + at] = make_float4(x[4], x[5], x[6], x[7]);
+                    to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
+                    to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
                 }
             }
-            give_back();
-            __threadfence();
-            named_barrier_sync(1, kEpilogueThreads);
-            // an abandoned part is counted too: the counter is left at 0 all the same
-            if (eid == 0) {
-                int* const counter = a.counters + it.left_over * S::kBlocks + rank;
-                const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
-                if (last) *counter = 0;
-                last_part = last;
-            }
-            named_barrier_sync(1, kEpilogueThreads);
-            if (!ok || !last_part) continue;
-            __threadfence();
-            const float4* const part0 = schedule.part(it, 0);
-            const float4* const part1 = schedule.part(it, 1);  // the others follow it
-            constexpr size_t kNext = (size_t)S::kBlocks * 2 * S::kPartial / 4;
+            give_back(sums);
+            if (!count_part() || !ok) continue;
 #pragma unroll 1
             for (int column = first; column < end; column += 8) {
-                float x[8] = {};
-                const int here = column / 4 * kW4Rows + at;
-#pragma unroll 1
-                for (int i = 0; i < it.parts; i += kJoin) {
-                    float4 y[kJoin][2];
-#pragma unroll
-                    for (int k = 0; k < kJoin; ++k) {
-                        y[k][0] = y[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (i + k < it.parts) {
-                            const float4* part =
-                                (i + k == 0 ? part0 : part1 + (i + k - 1) * kNext) + here;
-                            y[k][0] = __ldcg(part);
-                            y[k][1] = __ldcg(part + kW4Rows);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < kJoin; ++k)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            x[4 * j] += y[k][j].x;
-                            x[4 * j + 1] += y[k][j].y;
-                            x[4 * j + 2] += y[k][j].z;
-                            x[4 * j + 3] += y[k][j].w;
-                        }
-                }
+                float x[8];
+                join8(column, x);
                 const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
                                        pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
                 emit(column, v);
@@ -854,6 +940,8 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
     a.row_blocks = w4_row_blocks(p.N, p.streams);
     a.experts = p.groups.experts;
     a.act = p.act;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.N * 2;
+    a.vector = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 2;
     a.status = status;
     a.counters = counters;
     a.partials = reinterpret_cast<float*>(partials);
@@ -862,10 +950,10 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
     Maps maps{};
     if (wide(p.M, p.groups.experts)) {
         const long long blocks = w4_token_blocks(p.M, p.groups.experts);
-        if (!tile_map(&maps.weight, p.packed, a.k_blocks, (long long)a.experts * a.row_blocks,
-                      kW4Tile / 1024, 1) ||
-            !tile_map(&maps.codes, p.rows, a.k_blocks, blocks, kW4Codes / 1024, 1) ||
-            !tile_map(&maps.scales, p.rows, a.k_blocks, blocks, kW4Scales / 1024, 2))
+        const long long weights = (long long)a.experts * a.row_blocks;
+        if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024, 1) ||
+            !tile_map(&maps.codes, p.packed, a.k_blocks, weights, kW4Codes / 1024, 1) ||
+            !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024, 2))
             return cudaErrorInvalidValue;
         a.row_blocks /= Shape<256>::kBlocks;
         return p.streams == 2 ? launch<256, true>(a, maps, num_sms, s)
