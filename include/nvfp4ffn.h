@@ -601,11 +601,8 @@ nvfp4_status w4a4_unpack(const void* packed, int experts, int N, int K, uint8_t*
  * an expert whose rows do not lie in 0..M has none.
  */
 typedef struct {
-    const int* start;  /* (device) [experts + 1] */
-    const int* source; /* (device) [M], for w4a4_quantize: the row of x that each row is, or
-                          NULL (row m is x's row m); a source outside x is a row of zeros */
-    int experts;       /* 1..1024 */
-    int sources;       /* rows of x, where source is given */
+    const int* start; /* (device) [experts + 1] */
+    int experts;      /* 1..1024 */
 } w4a4_groups;
 
 /* Bytes of M quantised rows (0 for sizes that the calls refuse); experts as in the
@@ -613,15 +610,24 @@ typedef struct {
 size_t w4a4_rows_bytes(int M, int K, int experts);
 
 /*
- * x (device) bf16 [M, K], or [sources, K] with a source list, -> rows (device, out,
- * w4a4_rows_bytes, opaque).  groups NULL for a dense product.
+ * x (device) bf16 [M, K] -> rows (device, out, w4a4_rows_bytes, opaque).  groups NULL
+ * for a dense product.
  */
 nvfp4_status w4a4_quantize(const void* x, int M, int K, const w4a4_groups* groups, void* rows,
                            cudaStream_t stream);
 
+/*
+ * The rows of a routed batch, tokens * choices of them: x (device) bf16 [tokens, K],
+ * each token quantised once and written to the rows of its choices; ids and place
+ * (device) int32 [tokens, choices] and groups->start as experts_order has and writes
+ * them.  A pair with an id or a place out of range is left out.
+ */
+nvfp4_status w4a4_quantize_routed(const void* x, int tokens, int K, const int* ids,
+                                  const int* place, int choices, const w4a4_groups* groups,
+                                  void* rows, cudaStream_t stream);
+
 /* The values that rows stand for: out (device, out) bf16 [M, K] = code * s_b * r, which
- * bf16 holds exactly unless r is near the end of its range (a test and inspection aid;
- * groups as for w4a4_quantize, without its sources). */
+ * bf16 holds exactly unless r is near the end of its range (a test and inspection aid). */
 nvfp4_status w4a4_dequantize(const void* rows, int M, int K, const w4a4_groups* groups, void* out,
                              cudaStream_t stream);
 

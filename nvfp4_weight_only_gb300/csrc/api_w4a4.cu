@@ -37,17 +37,21 @@ bool weight_sizes(int experts, int N, int K) {
 // M = 0 rows and more than the call takes are out of range.
 bool row_count(long long M) { return M >= 1 && M <= nvf::kW4MaxTokens; }
 
-nvf::W4Groups groups_of(const w4a4_groups* g, int M) {
-    if (!g) return {nullptr, nullptr, 1, M};
-    return {g->start, g->source, g->experts, g->source ? g->sources : M};
+nvf::W4Groups groups_of(const w4a4_groups* g) {
+    if (!g) return {nullptr, 1};
+    return {g->start, g->experts};
+}
+
+bool routed_sizes(int tokens, int choices, int experts) {
+    return tokens >= 1 && choices >= 1 && choices <= kMaxChoices && experts >= 1 &&
+           experts <= nvf::kW4MaxExperts && row_count((long long)tokens * choices);
 }
 
 nvfp4_status check_groups(const w4a4_groups* g) {
     if (!g) return NVFP4_OK;
     if (!g->start) return NVFP4_ERR_NULL;
     if (g->experts < 1 || g->experts > nvf::kW4MaxExperts) return NVFP4_ERR_RANGE;
-    if (g->source && g->sources < 1) return NVFP4_ERR_RANGE;
-    return aligned(g->start, 4) && aligned(g->source, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+    return aligned(g->start, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
 size_t rows_bytes(int M, int K, int experts) {
@@ -78,7 +82,7 @@ nvfp4_status product(const Product& p, void* ws, size_t ws_bytes, cudaStream_t s
     if (p.act != NVFP4_ACT_SILU && p.act != NVFP4_ACT_GELU_TANH) return NVFP4_ERR_RANGE;
     const nvfp4_status g = check_groups(p.groups);
     if (g != NVFP4_OK) return g;
-    const nvf::W4Groups groups = groups_of(p.groups, p.M);
+    const nvf::W4Groups groups = groups_of(p.groups);
     if (!weight_sizes(groups.experts, p.N, p.K) || (p.streams == 2 && p.N % 16 != 0))
         return NVFP4_ERR_SHAPE;
     if (!aligned(p.rows, 16) || !aligned(p.packed, 16) || !aligned(p.out, 16) || !aligned(ws, 16) ||
@@ -174,12 +178,32 @@ nvfp4_status w4a4_quantize(const void* x, int M, int K, const w4a4_groups* group
     if (!row_count(M)) return NVFP4_ERR_RANGE;
     const nvfp4_status v = check_groups(groups);
     if (v != NVFP4_OK) return v;
-    const nvf::W4Groups g = groups_of(groups, M);
+    const nvf::W4Groups g = groups_of(groups);
     if (!weight_sizes(1, 1, K)) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(rows, 16)) return NVFP4_ERR_ALIGN;
-    if (overlap(x, (size_t)g.sources * K * 2, rows, rows_bytes(M, K, g.experts)))
+    if (overlap(x, (size_t)M * K * 2, rows, rows_bytes(M, K, g.experts)))
         return NVFP4_ERR_ALIAS;
     return cuda_status(nvf::launch_w4_quantize(x, M, K, g, rows, stream));
+}
+
+nvfp4_status w4a4_quantize_routed(const void* x, int tokens, int K, const int* ids,
+                                  const int* place, int choices, const w4a4_groups* groups,
+                                  void* rows, cudaStream_t stream) {
+    if (!x || !ids || !place || !groups || !rows) return NVFP4_ERR_NULL;
+    if (!routed_sizes(tokens, choices, groups->experts)) return NVFP4_ERR_RANGE;
+    const nvfp4_status v = check_groups(groups);
+    if (v != NVFP4_OK) return v;
+    if (!weight_sizes(1, 1, K)) return NVFP4_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(rows, 16) || !aligned(ids, 4) || !aligned(place, 4))
+        return NVFP4_ERR_ALIGN;
+    const nvf::W4Groups g = groups_of(groups);
+    const size_t n = rows_bytes(tokens * choices, K, g.experts);
+    const size_t lists = (size_t)tokens * choices * 4;
+    if (overlap(x, (size_t)tokens * K * 2, rows, n) || overlap(ids, lists, rows, n) ||
+        overlap(place, lists, rows, n))
+        return NVFP4_ERR_ALIAS;
+    return cuda_status(
+        nvf::launch_w4_quantize_routed(x, tokens, K, ids, place, choices, g, rows, stream));
 }
 
 nvfp4_status w4a4_dequantize(const void* rows, int M, int K, const w4a4_groups* groups, void* out,
@@ -188,7 +212,7 @@ nvfp4_status w4a4_dequantize(const void* rows, int M, int K, const w4a4_groups* 
     if (!row_count(M)) return NVFP4_ERR_RANGE;
     const nvfp4_status v = check_groups(groups);
     if (v != NVFP4_OK) return v;
-    const nvf::W4Groups g = groups_of(groups, M);
+    const nvf::W4Groups g = groups_of(groups);
     if (!weight_sizes(1, 1, K)) return NVFP4_ERR_SHAPE;
     if (!aligned(rows, 16) || !aligned(out, 16)) return NVFP4_ERR_ALIGN;
     if (overlap(out, (size_t)M * K * 2, rows, rows_bytes(M, K, g.experts))) return NVFP4_ERR_ALIAS;
@@ -269,9 +293,7 @@ nvfp4_status ffn_swiglu_w4a4(const void* x, int M, int H, int I, const void* gat
 nvfp4_status experts_order(const int* ids, int tokens, int choices, int experts, int* start,
                            int* source, int* place, cudaStream_t stream) {
     if (!ids || !start || !source || !place) return NVFP4_ERR_NULL;
-    if (tokens < 1 || choices < 1 || choices > kMaxChoices || experts < 1 ||
-        experts > nvf::kW4MaxExperts || !row_count((long long)tokens * choices))
-        return NVFP4_ERR_RANGE;
+    if (!routed_sizes(tokens, choices, experts)) return NVFP4_ERR_RANGE;
     if (!aligned(ids, 4) || !aligned(start, 4) || !aligned(source, 4) || !aligned(place, 4))
         return NVFP4_ERR_ALIGN;
     const size_t n = (size_t)tokens * choices * 4, ns = (size_t)(experts + 1) * 4;
@@ -285,9 +307,7 @@ nvfp4_status experts_order(const int* ids, int tokens, int choices, int experts,
 nvfp4_status experts_sum(const void* y, int rows, const int* place, const float* weights, int tokens,
                          int choices, int H, void* out, cudaStream_t stream) {
     if (!y || !place || !weights || !out) return NVFP4_ERR_NULL;
-    if (tokens < 1 || choices < 1 || choices > kMaxChoices || !row_count(rows) ||
-        !row_count((long long)tokens * choices))
-        return NVFP4_ERR_RANGE;
+    if (!row_count(rows) || !routed_sizes(tokens, choices, 1)) return NVFP4_ERR_RANGE;
     if (H < 16 || H % 16 != 0 || H > nvf::kW4MaxK) return NVFP4_ERR_SHAPE;
     if (!aligned(y, 16) || !aligned(out, 16) || !aligned(place, 4) || !aligned(weights, 4))
         return NVFP4_ERR_ALIGN;
@@ -300,9 +320,7 @@ nvfp4_status experts_sum(const void* y, int rows, const int* place, const float*
 }
 
 size_t experts_swiglu_w4a4_workspace_bytes(int tokens, int choices, int experts, int H, int I) {
-    if (tokens < 1 || choices < 1 || choices > kMaxChoices || experts < 1 ||
-        experts > nvf::kW4MaxExperts || !row_count((long long)tokens * choices) || !ffn_sizes(H, I))
-        return 0;
+    if (!routed_sizes(tokens, choices, experts) || !ffn_sizes(H, I)) return 0;
     return ffn_layout(tokens * choices, H, I, experts, sms_for_sizing()).total;
 }
 
@@ -315,9 +333,7 @@ nvfp4_status experts_swiglu_w4a4(const void* x, int tokens, int H, int I, const 
     if (!x || !ids || !weights || !gate_up_packed || !gate_scale2 || !up_scale2 || !down_packed ||
         !down_scale2 || !out || !ws)
         return NVFP4_ERR_NULL;
-    if (tokens < 1 || choices < 1 || choices > kMaxChoices || experts < 1 ||
-        experts > nvf::kW4MaxExperts || !row_count((long long)tokens * choices))
-        return NVFP4_ERR_RANGE;
+    if (!routed_sizes(tokens, choices, experts)) return NVFP4_ERR_RANGE;
     if (act != NVFP4_ACT_SILU && act != NVFP4_ACT_GELU_TANH) return NVFP4_ERR_RANGE;
     if (!ffn_sizes(H, I)) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(gate_up_packed, 16) || !aligned(down_packed, 16) ||
@@ -340,8 +356,8 @@ nvfp4_status experts_swiglu_w4a4(const void* x, int tokens, int H, int I, const 
     int* const place = reinterpret_cast<int*>(w + l.place);
     nvfp4_status e = experts_order(ids, tokens, choices, experts, start, source, place, stream);
     if (e != NVFP4_OK) return e;
-    const w4a4_groups gather{start, source, experts, tokens}, same{start, nullptr, experts, 0};
-    e = w4a4_quantize(x, M, H, &gather, w + l.x_rows, stream);
+    const w4a4_groups same{start, experts};
+    e = w4a4_quantize_routed(x, tokens, H, ids, place, choices, &same, w + l.x_rows, stream);
     if (e != NVFP4_OK) return e;
     e = w4a4_experts_gate_up(w + l.x_rows, M, H, &same, gate_up_packed, gate_scale2, up_scale2, I,
                              act, w + l.h, ws, l.front, stream);

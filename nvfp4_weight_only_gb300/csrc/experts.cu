@@ -6,10 +6,16 @@
 // gives its first row, and its own, which a prefix sum over the block puts in order.
 // No block needs another's result, so one launch does it, at a cost of experts * ids
 // compares.  One more block has the ids of no expert and the rows behind the last.
+// Long lists are cut into chunks of 1024 ids instead, in three launches: each chunk's
+// count by expert, first rows from the sums of these over chunks and experts, and each
+// chunk's rows.  The counts lie in the chunk's own part of `place`, which only the last
+// launch's block of that chunk reads, and then writes.
 //
 // Sum: out[t] = bf16(sum_j weights[t][j] * y[place[t][j]]), fp32, in the order of j.
 // Bound by memory: every thread has 8 columns of a token and asks for all of its
 // rows at once.
+#include <atomic>
+
 #include "kv8.cuh"
 #include "w4a4.h"
 
@@ -18,6 +24,8 @@ namespace nvf {
 namespace {
 
 constexpr int kOrderThreads = 1024;
+constexpr int kManyPairs = 24576;
+constexpr long long kManyCompares = 1 << 20;
 constexpr int kSumThreads = 256;
 constexpr int kAhead = 8;  // rows of a token asked for at once
 
@@ -90,9 +98,9 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int* __restr
         int own = 0, ahead = 0, sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned b = __ballot_sync(0xffffffffu, (unsigned)v[i] == expert);
-            ahead += __popc(b & below);
-            sum += __popc(b);
+            const unsigned same = __ballot_sync(0xffffffffu, (unsigned)v[i] == expert);
+            ahead += __popc(same & below);
+            sum += __popc(same);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -103,6 +111,145 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int* __restr
             }
         row += sum;
     }
+}
+
+// Chunk c of a long list: ids c * kChunk on, the last one with what is left (up to
+// 2 * kChunk - 1), so that each has at least as many ids as there may be experts.
+constexpr int kChunk = 1024;
+static_assert(kW4MaxExperts <= kChunk, "counts lie in the chunk's places");
+
+__device__ __forceinline__ int chunk_end(int chunk, int chunks, int pairs) {
+    return chunk + 1 < chunks ? (chunk + 1) * kChunk : pairs;
+}
+
+__global__ void __launch_bounds__(kChunk) chunk_count_kernel(const int* __restrict__ ids, int pairs,
+                                                             int experts, int* __restrict__ place) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int counts[kW4MaxExperts];
+    const int tid = threadIdx.x, begin = blockIdx.x * kChunk;
+    const int end = chunk_end(blockIdx.x, gridDim.x, pairs);
+    if (tid < experts) counts[tid] = 0;
+    __syncthreads();
+    for (int i = begin + tid; i < end; i += kChunk) {
+        const int id = ids[i];
+        if ((unsigned)id < (unsigned)experts) atomicAdd(&counts[id], 1);
+    }
+    __syncthreads();
+    if (tid < experts) place[begin + tid] = counts[tid];
+}
+
+// Turns the chunks' counts into their rows: sums over the experts and chunks in front.
+// One block, in which several threads share the chunks of an expert.
+__global__ void __launch_bounds__(1024) chunk_sum_kernel(int chunks, int experts,
+                                                         int* __restrict__ start,
+                                                         int* __restrict__ place) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int total[kW4MaxExperts], part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < experts; e += 1024) total[e] = 0;
+    __syncthreads();
+    // neighbouring threads take neighbouring experts; 1024 / group of them share one
+    const int group = (experts + 31) / 32 * 32, sharers = 1024 / group;
+    const int e = tid % group, share = tid / group;
+    const int per = (chunks + sharers - 1) / sharers;
+    const int c0 = min(share * per, chunks), c1 = min(c0 + per, chunks);
+    __shared__ int front[1024];
+    int sum = 0;
+    if (e < experts && share < sharers)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += place[(size_t)c * kChunk + e];
+    front[tid] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
+    if (e < experts && share < sharers) {
+        for (int s = 0; s < sharers; ++s) {
+            const int n = front[s * group + e];
+            if (s < share) before += n;
+            all += n;
+        }
+        if (share == 0) total[e] = all;
+    }
+    __syncthreads();
+    // first rows: a sum over the experts in front (thread t has expert t)
+    int mine = tid < experts ? total[tid] : 0, upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    int warps_before = lane < warp ? part[lane] : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        warps_before += __shfl_xor_sync(0xffffffffu, warps_before, d);
+    upto += warps_before;
+    __syncthreads();
+    if (tid < experts) {
+        start[tid] = upto - mine;
+        total[tid] = upto - mine;
+        if (tid == experts - 1) start[experts] = upto;
+    }
+    __syncthreads();
+    if (e < experts && share < sharers) {
+        int row = total[e] + before;
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) {
+            const int n = place[(size_t)c * kChunk + e];
+            place[(size_t)c * kChunk + e] = row;
+            row += n;
+        }
+    }
+}
+
+// A chunk's rows: each warp's 32 ids are ranked among themselves, its counts by expert
+// summed over the warps in front.  counts: [32 warps][experts].
+__global__ void __launch_bounds__(kChunk) chunk_place_kernel(const int* __restrict__ ids, int pairs,
+                                                             int choices, int experts,
+                                                             const int* __restrict__ start,
+                                                             int* __restrict__ source,
+                                                             int* __restrict__ place) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    extern __shared__ int counts[];
+    __shared__ int first[kW4MaxExperts];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int begin = blockIdx.x * kChunk, end = chunk_end(blockIdx.x, gridDim.x, pairs);
+    if (tid < experts) first[tid] = place[begin + tid];
+    for (int at = begin; at < end; at += kChunk) {
+        for (int i = tid; i < 32 * experts; i += kChunk) counts[i] = 0;
+        __syncthreads();
+        const int i = at + tid;
+        int id = i < end ? ids[i] : -1;
+        if ((unsigned)id >= (unsigned)experts) id = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, id);
+        if (id >= 0 && lane == __ffs(same) - 1) counts[warp * experts + id] = __popc(same);
+        __syncthreads();
+        if (tid < experts) {
+            int row = first[tid];
+#pragma unroll 8
+            for (int w = 0; w < 32; ++w) {
+                const int n = counts[w * experts + tid];
+                counts[w * experts + tid] = row;
+                row += n;
+            }
+            first[tid] = row;
+        }
+        __syncthreads();
+        int row = -1;
+        if (id >= 0) {
+            row = counts[warp * experts + id] + __popc(same & ((1u << lane) - 1));
+            source[row] = i / choices;
+        }
+        if (i < end) place[i] = row;
+        __syncthreads();
+    }
+    // rows behind the last expert's
+    for (long long r = start[experts] + (long long)blockIdx.x * kChunk + tid; r < pairs;
+         r += (long long)gridDim.x * kChunk)
+        source[r] = -1;
 }
 
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restrict__ y, int rows,
@@ -147,11 +294,12 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restric
 }
 
 template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), unsigned blocks, int threads, cudaStream_t s,
-                   Args... args) {
+cudaError_t launch(void (*kernel)(Args...), unsigned blocks, int threads, size_t shared,
+                   cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -166,15 +314,34 @@ cudaError_t launch(void (*kernel)(Args...), unsigned blocks, int threads, cudaSt
 cudaError_t launch_experts_order(const int* ids, int tokens, int choices, int experts, int* start,
                                  int* source, int* place, cudaStream_t s) {
     const int pairs = tokens * choices, groups = (pairs + 127) / 128;
+    if (pairs >= kManyPairs && (long long)pairs * experts >= kManyCompares) {
+        static std::atomic<bool> allowed[64];  // per device: the shared memory limit is set
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= 64 || !allowed[dev].load(std::memory_order_acquire)) {
+            e = cudaFuncSetAttribute(chunk_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     32 * kW4MaxExperts * (int)sizeof(int));
+            if (e != cudaSuccess) return e;
+            if (dev < 64) allowed[dev].store(true, std::memory_order_release);
+        }
+        const int chunks = pairs / kChunk;
+        e = launch(chunk_count_kernel, (unsigned)chunks, kChunk, 0, s, ids, pairs, experts, place);
+        if (e != cudaSuccess) return e;
+        e = launch(chunk_sum_kernel, 1u, 1024, 0, s, chunks, experts, start, place);
+        if (e != cudaSuccess) return e;
+        return launch(chunk_place_kernel, (unsigned)chunks, kChunk, 32 * experts * sizeof(int), s,
+                      ids, pairs, choices, experts, (const int*)start, source, place);
+    }
     const int threads = groups < kOrderThreads / 32 ? groups * 32 : kOrderThreads;
-    return launch(order_kernel, (unsigned)experts + 1, threads, s, ids, pairs, choices, experts,
+    return launch(order_kernel, (unsigned)experts + 1, threads, 0, s, ids, pairs, choices, experts,
                   start, source, place);
 }
 
 cudaError_t launch_experts_sum(const void* y, int rows, const int* place, const float* weights,
                                int tokens, int choices, int H, void* out, cudaStream_t s) {
     const long long vectors = (long long)tokens * (H / 8);
-    return launch(sum_kernel, (unsigned)((vectors + kSumThreads - 1) / kSumThreads), kSumThreads, s,
+    return launch(sum_kernel, (unsigned)((vectors + kSumThreads - 1) / kSumThreads), kSumThreads, 0, s,
                   reinterpret_cast<const uint4*>(y), rows, place, weights, vectors, choices, H / 8,
                   reinterpret_cast<uint4*>(out));
 }

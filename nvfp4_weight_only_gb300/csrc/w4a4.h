@@ -50,9 +50,8 @@ inline __host__ __device__ int w4_scale_at(int r, int c) {
 // first tile of expert e is start[e] / 128 + e, so that a row's place needs no sum
 // over the experts.  start null: one expert with all rows.
 struct W4Groups {
-    const int* start;   // [experts + 1]
-    const int* source;  // row of x that each row is, or null
-    int experts, sources;
+    const int* start;  // [experts + 1]
+    int experts;
 };
 
 // Quantised rows: row blocks of tiles, then one fp32 scale per row.
@@ -71,6 +70,10 @@ cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, u
                              uint8_t* scales, cudaStream_t s);
 cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
                                cudaStream_t s);
+// Each token's row, at the places of its choices (ids, place [tokens, choices]).
+cudaError_t launch_w4_quantize_routed(const void* x, int tokens, int K, const int* ids,
+                                      const int* place, int choices, const W4Groups& g, void* rows,
+                                      cudaStream_t s);
 cudaError_t launch_w4_dequantize(const void* rows, int M, int K, const W4Groups& g, void* out,
                                  cudaStream_t s);
 

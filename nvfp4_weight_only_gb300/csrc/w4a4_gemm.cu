@@ -32,7 +32,7 @@ namespace nvf {
 namespace {
 
 constexpr int kEpilogueWarps = 16;
-constexpr int kJoin = 4;  // parts of a cut tile that are read at a time
+constexpr int kJoin = 4;  // parts of a cut tile that are asked for at a time
 constexpr int kThreads = (2 + kEpilogueWarps) * 32;
 constexpr int kEpilogueThreads = kEpilogueWarps * 32;
 // Token tiles that take turns with one weight tile before the next one: their tiles
@@ -58,7 +58,7 @@ struct Shape {
     static_assert(kScalesAt + kStages * kScaleColumns <= 512, "tensor memory");
     static constexpr int kPartial = kW4Rows * kTokens;  // floats
     // K blocks that a range of a cut tile has at least.
-    static constexpr int kLeastRange = kBlocks > 1 ? 16 : 2;
+    static constexpr int kLeastRange = kBlocks > 1 ? 8 : 2;
     // Columns of a tile's products.
     static __device__ __forceinline__ int columns(int tokens) {
         return kBlocks == 1 ? (tokens + 15) / 16 * 16 : 256;
@@ -75,6 +75,7 @@ struct Args {
     const float* scales_b;
     float scale_a, scale_b;
     int M, N, k_blocks, row_blocks, experts, act;  // row_blocks: of a tile's rows
+    int cut;     // K blocks of a tile that may be cut, 0 for none
     int vector;  // bytes that 16 features of a row may be stored by: 32, 16, or 2
     int* status;
     int* counters;
@@ -108,15 +109,17 @@ struct Schedule {
     int left;  // K blocks of the tiles that are left over: fewer than blocks of up to 256
     int next, range0, range1;
 
-    __device__ Schedule(const Args& args, const int* tile_prefix) : a(args), prefix(tile_prefix) {
-        const int P = gridDim.x / S::kBlocks, me = blockIdx.x / S::kBlocks;
+    int P;  // blocks, or pairs
+
+    __device__ Schedule(const Args& args, const int* tile_prefix, int pairs, int me)
+        : a(args), prefix(tile_prefix), P(pairs) {
         tiles = prefix[a.experts] * a.row_blocks;
         whole = tiles / P * P;
         left = (tiles - whole) * a.k_blocks;
         const int over = tiles - whole;
         if (S::kBlocks > 1) {
-            // equal parts of each tile, as many as are worth their join
-            sharers = over ? over * max(1, min(P / over, a.k_blocks / S::kLeastRange)) : 0;
+            // equal parts of each tile
+            sharers = over ? over * max(1, min(P / over, a.cut / S::kLeastRange)) : 0;
         } else {
             // equal shares of them all
             sharers = min(P, left / min(S::kLeastRange, a.k_blocks));
@@ -158,10 +161,10 @@ struct Schedule {
 
     // Where the sums of part i of a cut tile lie.  Of a sharer's ranges only the first and
     // the last can be parts of tiles, and the last begins its tile, so it is part 0 there.
-    __device__ float4* part(const Item& it, int i) const {
+    __device__ float4* part(const Item& it, int i, int rank) const {
         const int sharer = it.first_part + i;
         const bool second = i == 0 && left * sharer / sharers < it.left_over * a.k_blocks;
-        const size_t block = (size_t)sharer * S::kBlocks + blockIdx.x % S::kBlocks;
+        const size_t block = (size_t)sharer * S::kBlocks + rank;
         return reinterpret_cast<float4*>(a.partials + (block * 2 + second) * S::kPartial);
     }
 
@@ -171,19 +174,24 @@ struct Schedule {
             place(next, it);
             it.kb0 = 0;
             it.kb1 = a.k_blocks;
-            next += gridDim.x / S::kBlocks;
+            next += P;
             return true;
         }
         if (range0 >= range1) return false;
-        const int tile = range0 / a.k_blocks, begin = tile * a.k_blocks, end = begin + a.k_blocks;
-        place(whole + tile, it);
+        const int tile = range0 / a.k_blocks, begin = tile * a.k_blocks;
+        left_over(tile, it);
         it.kb0 = range0 - begin;
-        it.kb1 = min(range1, end) - begin;
-        it.left_over = tile;
-        it.first_part = sharer(begin);
-        it.parts = sharer(end - 1) - it.first_part + 1;
-        range0 = min(range1, end);
+        it.kb1 = min(range1 - begin, a.k_blocks);
+        range0 = min(range1, begin + a.k_blocks);
         return true;
+    }
+
+    // A tile that is cut, without a range of it.
+    __device__ void left_over(int tile, Item& it) const {
+        place(whole + tile, it);
+        it.left_over = tile;
+        it.first_part = sharer(tile * a.k_blocks);
+        it.parts = sharer((tile + 1) * a.k_blocks - 1) - it.first_part + 1;
     }
 };
 
@@ -354,6 +362,108 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
     return p == t && (bits & 0xffffu) == 0x8000u ? __uint_as_float(bits - 1) : p;
 }
 
+// Sums of kColumns columns of a cut tile in one lane, parts in order, kJoin of them asked
+// for at a time: a part is [column / 4][lane][4] floats.
+template <int kTokens, int kColumns>
+__device__ __forceinline__ void join(const Schedule<kTokens>& schedule, const Item& it, int rank,
+                                     int column, int lane, float (&x)[kColumns]) {
+    using S = Shape<kTokens>;
+    const int here = column / 4 * kW4Rows + lane;
+    const float4* const part0 = schedule.part(it, 0, rank) + here;
+    const float4* const part1 = schedule.part(it, 1, rank) + here;  // the others follow it
+    constexpr size_t kNext = (size_t)S::kBlocks * 2 * S::kPartial / 4;
+#pragma unroll
+    for (int j = 0; j < kColumns; ++j) x[j] = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < it.parts; i += kJoin) {
+        float4 y[kJoin][kColumns / 4];
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k)
+#pragma unroll
+            for (int j = 0; j < kColumns / 4; ++j) {
+                y[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i + k < it.parts)
+                    y[k][j] = __ldcg((i + k == 0 ? part0 : part1 + (i + k - 1) * kNext) +
+                                     j * kW4Rows);
+            }
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k)
+#pragma unroll
+            for (int j = 0; j < kColumns / 4; ++j) {
+                x[4 * j] += y[k][j].x;
+                x[4 * j + 1] += y[k][j].y;
+                x[4 * j + 2] += y[k][j].z;
+                x[4 * j + 3] += y[k][j].w;
+            }
+    }
+}
+
+// A pair's lane: one token, whose features lie side by side.
+template <bool kGated>
+struct TokenRow {
+    bool live;
+    float r, scale_a, scale_b;
+    __nv_bfloat16* out;  // from the lane's first column on
+    int room;            // features of the output from there on
+    int act, vector;
+
+    __device__ __forceinline__ TokenRow(const Args& a, const Item& it, int token, int first) {
+        live = token < it.tokens;
+        r = live ? a.row_scales[it.token0 + token] : 0.0f;
+        scale_a = a.scales_a ? a.scales_a[it.expert] : a.scale_a;
+        scale_b = a.scales_b ? a.scales_b[it.expert] : a.scale_b;
+        const int feature = (it.weight * 256 + first) / (kGated ? 2 : 1);
+        out = a.out + (size_t)(it.token0 + token) * a.N + feature;
+        room = a.N - feature;
+        act = a.act;
+        vector = a.vector;
+    }
+
+    __device__ __forceinline__ void store16(int feature, const uint32_t (&w)[8]) const {
+        if (!live || feature >= room) return;
+        __nv_bfloat16* const to = out + feature;
+        if (vector == 32 && feature + 16 <= room) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                         "r"(w[6]), "r"(w[7])
+                         : "memory");
+        } else if (vector == 16 && feature + 16 <= room) {
+            reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (feature + j < room)
+                    reinterpret_cast<uint16_t*>(to)[j] =
+                        (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+        }
+    }
+
+    // 32 columns, the c-th ones: as many features, or 16 of gate and 16 of up.
+    __device__ __forceinline__ void emit(int c, const float (&x)[32]) const {
+        uint32_t w[8];
+        if (kGated) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t g = bf16x2(x[2 * j] * scale_a * r, x[2 * j + 1] * scale_a * r);
+                const uint32_t u =
+                    bf16x2(x[16 + 2 * j] * scale_b * r, x[17 + 2 * j] * scale_b * r);
+                w[j] = bf16x2(gated(act, bf16_lo(g), bf16_lo(u)), gated(act, bf16_hi(g), bf16_hi(u)));
+            }
+            store16(16 * c, w);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = bf16x2(x[16 * h + 2 * j] * scale_a * r,
+                                  x[16 * h + 2 * j + 1] * scale_a * r);
+                store16(32 * c + 16 * h, w);
+            }
+        }
+    }
+};
+
 struct Barriers {
     uint64_t full[8], empty[8];        // stages
     uint64_t sums_full[2], sums_empty[2];
@@ -440,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, wait_lane(bar, uses)) != 0;
     };
 
-    Schedule<kTokens> schedule(a, prefix);
+    Schedule<kTokens> schedule(a, prefix, gridDim.x / S::kBlocks, blockIdx.x / S::kBlocks);
     Item it{};
     if (warp == kCopyWarp) {
         const bool issuer = elect_one();
@@ -583,7 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
         // a warp reads 32 lanes of a share of the columns
         constexpr int kShare = kTokens * 4 / kEpilogueWarps;
-        const int quadrant = warp & 3, first = (warp - 2) / 4 * kShare, eid = tid - 64;
+        const int quadrant = warp & 3, eid = tid - 64;
+        // a pair's warp has as many columns in a run; of one block's, eight of every 32
+        const int first = (warp - 2) / 4 * (S::kBlocks > 1 ? kShare : 8);
         const uint32_t lanes = tmem + ((uint32_t)(quadrant * 32) << 16);
         bool ok = true;
         // Counts a part of a cut tile, whose sums have been written, or which was abandoned:
@@ -592,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __threadfence();
             named_barrier_sync(1, kEpilogueThreads);
             if (eid == 0) {
-                int* const counter = a.counters + it.left_over * S::kBlocks + rank;
+                int* const counter = a.counters + it.left_over;
                 const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
                 if (last) *counter = 0;
                 last_part = last;
@@ -609,138 +721,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else arrive_at_first(smem_addr(&bars.sums_empty[sums]));
             }
         };
-        // Sums of eight columns of a cut tile, parts in order, kJoin of them asked for at a
-        // time: [column / 4][lane][4] floats.
-        auto join8 = [&](int column, float(&x)[8]) {
-            const int here = column / 4 * kW4Rows + quadrant * 32 + lane;
-            const float4* const part0 = schedule.part(it, 0) + here;
-            const float4* const part1 = schedule.part(it, 1) + here;  // the others follow it
-            constexpr size_t kNext = (size_t)S::kBlocks * 2 * S::kPartial / 4;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-#pragma unroll 1
-            for (int i = 0; i < it.parts; i += kJoin) {
-                float4 y[kJoin][2];
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k) {
-                    y[k][0] = y[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (i + k < it.parts) {
-                        const float4* part = i + k == 0 ? part0 : part1 + (i + k - 1) * kNext;
-                        y[k][0] = __ldcg(part);
-                        y[k][1] = __ldcg(part + kW4Rows);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x[4 * j] += y[k][j].x;
-                        x[4 * j + 1] += y[k][j].y;
-                        x[4 * j + 2] += y[k][j].z;
-                        x[4 * j + 3] += y[k][j].w;
-                    }
-            }
-        };
         if constexpr (S::kBlocks > 1) {
-            // a token per lane: its features lie side by side
             const int token = rank * kW4Rows + quadrant * 32 + lane;
             for (unsigned items = 0; schedule.take(it); ++items) {
-                const bool live = token < it.tokens;
-                const float r = live ? a.row_scales[it.token0 + token] : 0.0f;
-                const float scale_a = a.scales_a ? a.scales_a[it.expert] : a.scale_a;
-                const float scale_b = a.scales_b ? a.scales_b[it.expert] : a.scale_b;
-                __nv_bfloat16* const out =
-                    a.out + (size_t)(it.token0 + token) * a.N +
-                    (it.weight * 256 + first) / (kGated ? 2 : 1);
-                const int room = a.N - (it.weight * 256 + first) / (kGated ? 2 : 1);
-                auto store16 = [&](int feature, const uint32_t(&w)[8]) {
-                    if (!live || feature >= room) return;
-                    __nv_bfloat16* const to = out + feature;
-                    if (a.vector == 32 && feature + 16 <= room) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                                     "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                     : "memory");
-                    } else if (a.vector == 16 && feature + 16 <= room) {
-                        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (feature + j < room)
-                                reinterpret_cast<uint16_t*>(to)[j] =
-                                    (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
-                    }
-                };
-                // 32 columns: as many features, or 16 of gate and 16 of up
-                auto emit = [&](int c, const float(&x)[32]) {
-                    uint32_t w[8];
-                    if (kGated) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t g =
-                                bf16x2(x[2 * j] * scale_a * r, x[2 * j + 1] * scale_a * r);
-                            const uint32_t u = bf16x2(x[16 + 2 * j] * scale_b * r,
-                                                      x[17 + 2 * j] * scale_b * r);
-                            w[j] = bf16x2(gated(a.act, bf16_lo(g), bf16_lo(u)),
-                                          gated(a.act, bf16_hi(g), bf16_hi(u)));
-                        }
-                        store16(16 * c, w);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                w[j] = bf16x2(x[16 * h + 2 * j] * scale_a * r,
-                                              x[16 * h + 2 * j + 1] * scale_a * r);
-                            store16(32 * c + 16 * h, w);
-                        }
-                    }
-                };
+                const TokenRow<kGated> row(a, it, token, first);
                 ok = ok && wait(bars.sums_full[0], items);
                 tmem_fence_after();
-                if (it.parts == 1) {
-                    // the accumulator is given back before its columns are looked at
-                    float x[kShare / 32][32];
-                    if (ok) {
-#pragma unroll
-                        for (int c = 0; c < kShare / 32; ++c)
-                            tmem_load32(lanes + first + 32 * c, x[c]);
-#pragma unroll
-                        for (int c = 0; c < kShare / 32; ++c) tmem_wait_load(x[c]);
-                    }
-                    give_back(0);
-                    if (ok) {
-#pragma unroll
-                        for (int c = 0; c < kShare / 32; ++c) emit(c, x[c]);
-                    }
-                    continue;
-                }
+                // the accumulator is given back before its columns are looked at
+                float x[kShare / 32][32];
                 if (ok) {
-                    float4* const to =
-                        schedule.part(it, (int)blockIdx.x / S::kBlocks - it.first_part) +
-                        quadrant * 32 + lane;
-#pragma unroll 1
-                    for (int column = first; column < first + kShare; column += 8) {
-                        float x[8];
-                        tmem_load8(lanes + column, x);
-                        to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
-                        to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
-                    }
+#pragma unroll
+                    for (int c = 0; c < kShare / 32; ++c)
+                        tmem_load32(lanes + first + 32 * c, x[c]);
+#pragma unroll
+                    for (int c = 0; c < kShare / 32; ++c) tmem_wait_load(x[c]);
                 }
                 give_back(0);
-                if (!count_part() || !ok) continue;
-#pragma unroll 1
-                for (int c = 0; c < kShare / 32; ++c) {
-                    float x[32];
+                if (!ok) continue;
+                if (it.parts == 1) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        float y[8];
-                        join8(first + 32 * c + 8 * h, y);
+                    for (int c = 0; c < kShare / 32; ++c) row.emit(c, x[c]);
+                } else {
+                    float4* const to =
+                        schedule.part(it, (int)blockIdx.x / S::kBlocks - it.first_part, rank) +
+                        first / 4 * kW4Rows + quadrant * 32 + lane;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[8 * h + j] = y[j];
-                    }
-                    emit(c, x);
+                    for (int j = 0; j < kShare / 4; ++j)
+                        to[j * kW4Rows] =
+                            make_float4(x[j / 8][j % 8 * 4], x[j / 8][j % 8 * 4 + 1],
+                                        x[j / 8][j % 8 * 4 + 2], x[j / 8][j % 8 * 4 + 3]);
                 }
             }
         } else
@@ -748,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned sums = items % S::kSums;
             float* const scales = row_scale[items & 1];
             if (eid < kTokens) scales[eid] = eid < it.tokens ? a.row_scales[it.token0 + eid] : 0.0f;
-            const uint32_t from = lanes + sums * kTokens + first;
+            const uint32_t from = lanes + sums * kTokens;
             const bool up = kGated && lane >= 16;
             const float scale = up ? (a.scales_b ? a.scales_b[it.expert] : a.scale_b)
                                    : (a.scales_a ? a.scales_a[it.expert] : a.scale_a);
@@ -804,14 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            // Columns that this warp has: eight at a time.
-            const int end = min(it.tokens, first + kShare);
             if (it.parts == 1) {
                 // the other accumulator is at work meanwhile
 #pragma unroll 1
-                for (int column = first; column < end && ok; column += 8) {
+                for (int column = first; column < it.tokens && ok; column += 32) {
                     float x[8];
-                    tmem_load8(from + column - first, x);
+                    tmem_load8(from + column, x);
                     const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
                                            pack(column + 4, x[4], x[5]),
                                            pack(column + 6, x[6], x[7])};
@@ -821,12 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (ok) {
-                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part) +
+                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part, 0) +
                                    quadrant * 32 + lane;
 #pragma unroll 1
-                for (int column = first; column < end; column += 8) {
+                for (int column = first; column < it.tokens; column += 32) {
                     float x[8];
-                    tmem_load8(from + column - first, x);
+                    tmem_load8(from + column, x);
                     to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
                     to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
                 }
@@ -834,9 +841,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             give_back(sums);
             if (!count_part() || !ok) continue;
 #pragma unroll 1
-            for (int column = first; column < end; column += 8) {
+            for (int column = first; column < it.tokens; column += 32) {
                 float x[8];
-                join8(column, x);
+                join<kTokens, 8>(schedule, it, 0, column, quadrant * 32 + lane, x);
                 const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
                                        pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
                 emit(column, v);
@@ -849,6 +856,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     sync_blocks<S::kBlocks>();
     if (warp == kIssueWarp) tmem_free<S::kBlocks>(tmem);
+}
+
+// Joins the cut tiles of a dense product of pairs: a block has 32 columns of 128 tokens.
+// (In the product's kernel the block that came last took 14 us for the four parts of its
+// tile, 512 KB through one SM.)
+template <bool kGated>
+__global__ void __launch_bounds__(kW4Rows) w4a4_join_kernel(const Args a, int pairs) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int prefix[2] = {0, (a.M + 255) / 256};
+    const Schedule<256> schedule(a, prefix, pairs, 0);
+    Item it{};
+    schedule.left_over(blockIdx.x, it);
+    const int rank = blockIdx.y / 8, first = blockIdx.y % 8 * 32;
+    const TokenRow<kGated> row(a, it, rank * kW4Rows + threadIdx.x, first);
+    float x[32];
+    join<256, 32>(schedule, it, rank, first, threadIdx.x, x);
+    row.emit(0, x);
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -908,8 +933,20 @@ cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = Shape<kTokens>::kBlocks > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a, maps);
+    e = cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a, maps);
+    if (kTokens == 128 || !a.cut || e != cudaSuccess) return e;
+    const int pairs = num_sms / 2;
+    const int over = (int)((long long)((a.M + 255) / 256) * a.row_blocks % pairs);
+    if (over == 0 || pairs / over < 2) return e;
+    cfg.gridDim = dim3(over, 16);
+    cfg.blockDim = dim3(kW4Rows);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, w4a4_join_kernel<kGated>, a, pairs);
 }
+
+// K blocks from which a pair's tile is cut.
+constexpr int kLeastCut = 32;
 
 // Tokens per tile: rows of an expert on average, as far as the host knows them.
 bool wide(int M, int experts) { return M > 128LL * experts; }
@@ -942,6 +979,8 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
     a.act = p.act;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.N * 2;
     a.vector = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 2;
+    // A join costs about 6 us beside the cut tile's parts, 18 K blocks' products.
+    a.cut = !p.groups.start && a.k_blocks >= kLeastCut ? a.k_blocks : 0;
     a.status = status;
     a.counters = counters;
     a.partials = reinterpret_cast<float*>(partials);

@@ -3,12 +3,14 @@
 //
 // A row of x becomes r (2^e with the smallest e that keeps max|x| <= 2688 r, in
 // -100..117), per 16 values s = E4M3(max|x| / 6 / r), and codes E2M1(x / (s r)).
-// x / r is exact, so the two roundings are of quotients of a bf16 value: by 6,
-// where fp32 division cannot reach a tie of E4M3 that the quotient is not (they
-// are 2^-10 apart), and by s.  The latter is a product with 1/s, off by 2^-23 of
-// itself, brought to multiples of 2^-14 by adding and taking away 768: a quotient
-// that is a tie of E2M1 lands on it, any other is 2^-10 or more away and stays on
-// its side.  So codes are those of the exact quotients, without a division each.
+// x / r is exact, so the two roundings are of quotients of bf16 values: by 6, and by s.
+// Both are products with a rounded reciprocal, off by 2^-22 of themselves at most, which
+// are then rounded to a grid that the ties of the codes lie on: a quotient that is a tie
+// lands on it, and one that is not stays on its side.  For E4M3 (ties of 5 bits) max|x|
+// and 6 times a tie are both 8-bit numbers, so unequal ones are 2^-8 apart; the grid has
+// 13 bits.  For E2M1 (ties are multiples of 1/4 up to 5) a quotient is 2^-10 or more away
+// from a tie that it is not; the grid is 2^-14 (768 is added and taken away).  So codes
+// are those of the exact quotients, without a division.
 #include "kv8.cuh"
 #include "w4a4.h"
 
@@ -18,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinExp = -100, kMaxExp = 117;
+constexpr int kQuantizeWarps = 2;
 
 // One thread per 16 code bytes of a tile (two scale bytes with them).
 __global__ void __launch_bounds__(kThreads) repack_kernel(
@@ -82,6 +85,13 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restr
     }
 }
 
+// The place of a row of an expert whose rows begin at `first`.
+__device__ __forceinline__ void place_of(int row, int expert, int first, long long& block, int& r) {
+    const int i = row - first;
+    block = first / kW4Rows + expert + i / kW4Rows;
+    r = i % kW4Rows;
+}
+
 // The expert of a row and its place; false for a row of none.  All threads of the
 // block call it.
 __device__ __forceinline__ bool find_place(const W4Groups& g, int row, long long& block, int& r) {
@@ -99,9 +109,7 @@ __device__ __forceinline__ bool find_place(const W4Groups& g, int row, long long
         first = g.start[expert];
         if (first < 0 || first > row || row >= g.start[expert + 1]) return false;
     }
-    const int i = row - first;
-    block = first / kW4Rows + expert + i / kW4Rows;
-    r = i % kW4Rows;
+    place_of(row, expert, first, block, r);
     return true;
 }
 
@@ -117,6 +125,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
     return w;
 }
 
+// 1 / v, off by one unit of the last place at most.
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // The larger of two pairs of bf16, NaN if either is.
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -124,30 +139,37 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     return r;
 }
 
-// One block per row; a warp takes 256 values at a time, 8 per lane, which stay in
-// registers between the row's maximum and the codes, so x is read once.
+// Where a row goes: its expert's place for it, or those of a token's choices.
+struct Places {
+    W4Groups groups;
+    const int* ids;    // routed: [tokens, choices], with each pair's row in `place`
+    const int* place;
+    int choices;       // 0: not routed
+    int rows;
+};
+
+// One block per row of x; a warp takes 256 values at a time, 8 per lane, which stay in
+// registers between the row's maximum and the codes, so x is read once.  A token's codes
+// are written to the places of all of its choices.
 template <int kIter>
 __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict__ x, int K,
-                                                        int k_blocks, const W4Groups g,
+                                                        int k_blocks, const Places to,
                                                         uint8_t* __restrict__ rows,
                                                         float* __restrict__ row_scales) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int row = blockIdx.x;
-    long long block;
-    int r;
-    if (!find_place(g, row, block, r)) return;
-    const int from = g.source ? g.source[row] : row;
-    // a row without a source is a row of zeros
-    const int vecs = K / 8, have = from >= 0 && from < g.sources ? vecs : 0;
-    const uint4* src = x + (have ? (size_t)from * vecs : 0);
+    const int row = blockIdx.x, vecs = K / 8;
+    const uint4* src = x + (size_t)row * vecs;
     uint4 v[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
         const int c = (warp + i * warps) * 32 + lane;
-        v[i] = c < have ? src[c] : make_uint4(0, 0, 0, 0);
+        v[i] = c < vecs ? src[c] : make_uint4(0, 0, 0, 0);
     }
+    long long block = 0;
+    int r = 0;
+    if (to.choices == 0 && !find_place(to.groups, row, block, r)) return;
     uint32_t top[kIter];  // the largest of each block of 16, as bf16
     uint32_t most = 0;
 #pragma unroll
@@ -175,33 +197,58 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
         e = exponent - 11 + ((amax & 0x7f) > (0x3fa8 & 0x7f) ? 1 : 0);
         e = min(max(e, kMinExp), kMaxExp);
     }
-    if (tid == 0)
-        row_scales[row] = amax >= 0x7f80 ? __uint_as_float(0x7fffffffu)
-                                         : __uint_as_float((uint32_t)(e + 127) << 23);
+    const float scale = amax >= 0x7f80 ? __uint_as_float(0x7fffffffu)
+                                       : __uint_as_float((uint32_t)(e + 127) << 23);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 1 / r
-    uint8_t* const out = rows + (size_t)block * k_blocks * kW4Tile;
+    // codes in place of x, scales of 64 values in every eighth lane
+    uint32_t scales[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int kb = warp + i * warps;
-        if (kb >= k_blocks) break;
         const float largest = __uint_as_float(max(top[i] & 0xffffu, top[i] >> 16) << 16) * down;
-        const uint32_t code = f32_to_e4m3(__fdiv_rn(largest, 6.0f));
-        const float s = e4m3_to_f32(code);
-        const float by = code ? __frcp_rn(s) * down : 0.0f;
+        const uint32_t sixth = __float_as_uint(largest * (1.0f / 6.0f));
+        const uint32_t code = f32_to_e4m3(__uint_as_float((sixth + 0x400u) & ~0x7ffu));
+        const float by = code ? reciprocal(e4m3_to_f32(code)) * down : 0.0f;
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint64_t by2 = pair(by, by), grid = pair(768.0f, 768.0f), back = pair(-768.0f, -768.0f);
         float q[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            q[2 * p] = __fmaf_rn(bf16_lo(w[p]), by, 768.0f) - 768.0f;
-            q[2 * p + 1] = __fmaf_rn(bf16_hi(w[p]), by, 768.0f) - 768.0f;
+            const float2 y =
+                unpair(add2(fma2(pair(bf16_lo(w[p]), bf16_hi(w[p])), by2, grid), back));
+            q[2 * p] = y.x;
+            q[2 * p + 1] = y.y;
         }
-        uint8_t* const tile = out + (size_t)kb * kW4Tile;
-        *reinterpret_cast<uint32_t*>(tile + w4_code_at(r, lane * 4)) = e2m1x8(q);
-        // the four scales of 64 values: lanes 8j, 8j + 2, 8j + 4, 8j + 6
+        v[i].x = e2m1x8(q);
         uint32_t sc = code;
         sc |= __shfl_down_sync(0xffffffffu, sc, 2) << 8;
         sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 16;
-        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile + w4_scale_at(r, lane / 2)) = sc;
+        scales[i] = sc;
+    }
+    auto write = [&](int at_row) {
+        if (tid == 0) row_scales[at_row] = scale;
+        uint8_t* const out = rows + (size_t)block * k_blocks * kW4Tile;
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const int kb = warp + i * warps;
+            if (kb >= k_blocks) break;
+            uint8_t* const tile = out + (size_t)kb * kW4Tile;
+            *reinterpret_cast<uint32_t*>(tile + w4_code_at(r, lane * 4)) = v[i].x;
+            if ((lane & 7) == 0)
+                *reinterpret_cast<uint32_t*>(tile + w4_scale_at(r, lane / 2)) = scales[i];
+        }
+    };
+    if (to.choices == 0) {
+        write(row);
+        return;
+    }
+    for (int j = 0; j < to.choices; ++j) {
+        const size_t pair_at = (size_t)row * to.choices + j;
+        const int expert = to.ids[pair_at], at_row = to.place[pair_at];
+        if (expert < 0 || expert >= to.groups.experts || at_row < 0 || at_row >= to.rows) continue;
+        const int first = to.groups.start[expert];
+        if (first < 0 || first > at_row) continue;
+        place_of(at_row, expert, first, block, r);
+        write(at_row);
     }
 }
 
@@ -274,12 +321,15 @@ cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, u
     return cudaGetLastError();
 }
 
-cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
-                               cudaStream_t s) {
+namespace {
+
+cudaError_t quantize(const void* x, int blocks, int M, int K, const Places& to, void* rows,
+                     cudaStream_t s) {
     const int k_blocks = w4_k_blocks(K);
-    // 8 warps and up to 8 vectors per lane, then more warps
+    // Two warps per row as long as 8 vectors per lane hold it: small blocks, whose loads and
+    // stores overlap others' (16384 rows of 2048: 18.1 us, with 4 warps 20.1, with 8 28.9).
     int iter = 1;
-    while (iter < 8 && (k_blocks + iter - 1) / iter > 8) iter *= 2;
+    while (iter < 8 && k_blocks > kQuantizeWarps * iter) iter *= 2;
     const int warps = (k_blocks + iter - 1) / iter;
     auto kernel = iter == 1   ? quantize_kernel<1>
                   : iter == 2 ? quantize_kernel<2>
@@ -287,9 +337,23 @@ cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, v
                               : quantize_kernel<8>;
     uint8_t* const base = reinterpret_cast<uint8_t*>(rows);
     float* const scales =
-        reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, g.experts));
-    return launch(kernel, M, warps * 32, s, reinterpret_cast<const uint4*>(x), K, k_blocks, g, base,
-                  scales);
+        reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, to.groups.experts));
+    return launch(kernel, blocks, warps * 32, s, reinterpret_cast<const uint4*>(x), K, k_blocks, to,
+                  base, scales);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
+                               cudaStream_t s) {
+    return quantize(x, M, M, K, Places{g, nullptr, nullptr, 0, M}, rows, s);
+}
+
+cudaError_t launch_w4_quantize_routed(const void* x, int tokens, int K, const int* ids,
+                                      const int* place, int choices, const W4Groups& g, void* rows,
+                                      cudaStream_t s) {
+    const int M = tokens * choices;
+    return quantize(x, tokens, M, K, Places{g, ids, place, choices, M}, rows, s);
 }
 
 cudaError_t launch_w4_dequantize(const void* rows, int M, int K, const W4Groups& g, void* out,

@@ -45,7 +45,8 @@ EXPORTS = [
     "add_rmsnorm_bf16", "add_rmsnorm_e4m3", "rope_table", "kv8_batch_status", "kv8_append",
     "kv8_read", "kv8_attention_workspace_bytes", "kv8_attention",
     "w4a4_repacked_bytes", "w4a4_repacked_gate_up_bytes", "w4a4_repack", "w4a4_repack_gate_up",
-    "w4a4_unpack", "w4a4_rows_bytes", "w4a4_quantize", "w4a4_dequantize",
+    "w4a4_unpack", "w4a4_rows_bytes", "w4a4_quantize", "w4a4_quantize_routed",
+    "w4a4_dequantize",
     "w4a4_gemm_workspace_bytes", "w4a4_gemm", "w4a4_gate_up", "w4a4_experts_gemm",
     "w4a4_experts_gate_up", "ffn_swiglu_w4a4_workspace_bytes", "ffn_swiglu_w4a4", "experts_order",
     "experts_sum", "experts_swiglu_w4a4_workspace_bytes", "experts_swiglu_w4a4",
@@ -130,6 +131,7 @@ def load(build_if_missing: bool = False):
         "w4a4_unpack": (i32, [vp, i32, i32, i32, vp, vp, vp]),
         "w4a4_rows_bytes": (sz, [i32, i32, i32]),
         "w4a4_quantize": (i32, [vp, i32, i32, vp, vp, vp]),
+        "w4a4_quantize_routed": (i32, [vp, i32, i32, vp, vp, i32, vp, vp, vp]),
         "w4a4_dequantize": (i32, [vp, i32, i32, vp, vp, vp]),
         "w4a4_gemm_workspace_bytes": (sz, [i32, i32, i32, i32]),
         "w4a4_gemm": (i32, [vp, i32, i32, vp, f32, i32, vp, vp, sz, vp]),
@@ -727,8 +729,15 @@ def kv8_attention(q: torch.Tensor, cache: Kv8Cache, batch: Kv8Batch, softmax_sca
 # ------------------------------------------------------------------ 4-bit activations (w4a4)
 
 class _GroupsStruct(ctypes.Structure):
-    _fields_ = [("start", ctypes.c_void_p), ("source", ctypes.c_void_p), ("experts", ctypes.c_int),
-                ("sources", ctypes.c_int)]
+    _fields_ = [("start", ctypes.c_void_p), ("experts", ctypes.c_int)]
+
+
+def _matrix(x, name):
+    """(rows, width, device) of a contiguous bf16 CUDA matrix."""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
+                         f"{list(x.shape)} on {x.device}")
+    return (*x.shape, x.get_device())
 
 
 def _stacked(codes, scales, name):
@@ -796,8 +805,8 @@ class W4a4Rows:
         self.at = _plain(data, "data", _U8, (size,), self.device)
         self.struct = self.groups = None
         if start is not None:
-            self.struct = _GroupsStruct(_plain(start, "start", _I32, start.shape, self.device), None,
-                                        self.experts, 0)
+            self.struct = _GroupsStruct(_plain(start, "start", _I32, (self.experts + 1,),
+                                               self.device), self.experts)
             self.groups = ctypes.addressof(self.struct)
 
     @classmethod
@@ -808,33 +817,46 @@ class W4a4Rows:
         return cls(torch.empty(size, dtype=_U8, device=device), M, K, start)
 
 
-def w4a4_quantize(x: torch.Tensor, start: torch.Tensor = None, source: torch.Tensor = None,
-                  out: W4a4Rows = None) -> W4a4Rows:
-    """x bf16 [M, K] in 4 bits.  With start (see W4a4Rows) the rows are an expert product's; with
-    source int32 [M] as well, row m is x's row source[m]."""
-    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"x must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
-                         f"{list(x.shape)} on {x.device}")
-    n, K = x.shape
-    device = x.get_device()
-    M = n if source is None else source.numel()
+def _rows_for(out, M, K, start, like):
+    """Rows to write M quantised rows of K to: `out`, checked, or new ones."""
     if out is None:
-        out = W4a4Rows.empty(M, K, x.device, start)
-    elif start is not None and start is not out.start:
+        return W4a4Rows.empty(M, K, like.device, start)
+    if start is not None and start is not out.start:
         raise ValueError("start is not that of out")
-    if out.M != M or out.K != K or out.device != device:
+    if out.M != M or out.K != K or out.device != like.get_device():
         raise ValueError(f"out holds {out.M} rows of {out.K} on device {out.device}, "
-                         f"got {M} of {K} on {device}")
-    groups, struct = out.groups, None
-    if source is not None:
-        if groups is None:
-            raise ValueError("a source list needs start")
-        struct = _GroupsStruct(out.struct.start, _plain(source, "source", _I32, (M,), device),
-                               out.experts, n)
-        groups = ctypes.addressof(struct)
-    code = (_lib or load()).w4a4_quantize(x.data_ptr(), M, K, groups, out.at, _raw_stream(device))
+                         f"got {M} of {K} on {like.device}")
+    return out
+
+
+def w4a4_quantize(x: torch.Tensor, start: torch.Tensor = None, out: W4a4Rows = None) -> W4a4Rows:
+    """x bf16 [M, K] in 4 bits.  With start (see W4a4Rows) the rows are an expert product's."""
+    M, K, device = _matrix(x, "x")
+    out = _rows_for(out, M, K, start, x)
+    code = (_lib or load()).w4a4_quantize(x.data_ptr(), M, K, out.groups, out.at,
+                                          _raw_stream(device))
     if code:
         _check("w4a4_quantize", code)
+    return out
+
+
+def w4a4_quantize_routed(x: torch.Tensor, ids: torch.Tensor, place: torch.Tensor,
+                         start: torch.Tensor = None, out: W4a4Rows = None) -> W4a4Rows:
+    """The rows of a routed batch: x bf16 [tokens, K], each token quantised once and written to the
+    rows of its choices; ids, place int32 [tokens, choices] and start as experts_order has them."""
+    T, K, device = _matrix(x, "x")
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"ids must be [{T}, choices], got {list(shape)}")
+    out = _rows_for(out, T * shape[1], K, start, x)
+    if out.groups is None:
+        raise ValueError("routed rows need start")
+    code = (_lib or load()).w4a4_quantize_routed(
+        x.data_ptr(), T, K, _plain(ids, "ids", _I32, shape, device),
+        _plain(place, "place", _I32, shape, device), shape[1], out.groups, out.at,
+        _raw_stream(device))
+    if code:
+        _check("w4a4_quantize_routed", code)
     return out
 
 
@@ -911,14 +933,6 @@ def w4a4_gate_up(rows: W4a4Rows, gate_up_packed: torch.Tensor, gate_scale2, up_s
 
 def ffn_swiglu_w4a4_workspace_bytes(M: int, H: int, I: int) -> int:
     return load().ffn_swiglu_w4a4_workspace_bytes(M, H, I)
-
-
-def _matrix(x, name):
-    """(rows, width, device) of a contiguous bf16 CUDA matrix."""
-    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bfloat16 CUDA matrix, got {x.dtype} "
-                         f"{list(x.shape)} on {x.device}")
-    return (*x.shape, x.get_device())
 
 
 def ffn_swiglu_w4a4(x: torch.Tensor, gate_up_packed: torch.Tensor, gate_scale2: float,
