@@ -560,10 +560,13 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
  * w4a4_gemm), dense or grouped by expert.  Other numerics than the calls above,
  * which keep activations in bf16: a user chooses.  These calls take any number of
  * rows up to 2^22 (RANGE beyond), K, H and I multiples of 16 up to 65536, N up to
- * 2^20.  They are asynchronous, use programmatic dependent launch, read no input
- * before the preceding kernel on `stream` has completed, and their results are
- * bit-reproducible.  Blocks do not wait for one another, so calls on different
- * streams may overlap if their workspaces (and rows buffers) differ.
+ * 2^20.  They are asynchronous and use programmatic dependent launch; their results
+ * are bit-reproducible.  The dense products (without groups) begin to read their
+ * packed weight while the preceding kernel on `stream` is still finishing, so that
+ * kernel must not write it (the repack calls may precede them); nothing else is read
+ * before it has completed.  Blocks of different pairs do not wait for one another, so
+ * calls on different streams may overlap if their workspaces (and rows buffers)
+ * differ.
  *
  * A row of x [M, K] becomes a scale r per row, one E4M3 scale per 16 values and
  * E2M1 codes (all to nearest, ties to even, saturating):
@@ -571,8 +574,9 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
  *          of zeros, NaN for a row that holds an infinity or a NaN
  *   s_b  = E4M3(max|x_b| / 6 / r)        per block b of 16
  *   code = E2M1(x / (s_b * r))           0 where s_b is 0
- * A row's result depends on that row alone.  A row that is not finite gives an
- * output row of NaN and leaves the others as they are.
+ * A row that is not finite gives an output row of NaN and leaves the others as they
+ * are.  Sums may be cut along K in another way for another number of rows, so a row's
+ * product may differ in the last place between calls of different sizes.
  */
 
 /*

@@ -98,9 +98,8 @@ nvfp4_status product(const Product& p, void* ws, size_t ws_bytes, cudaStream_t s
     char* const w = reinterpret_cast<char*>(ws);
     const nvf::W4Product q{p.rows,    p.packed,  p.out,      p.M,        p.N,   p.K, p.streams,
                            p.act,     p.scale_a, p.scale_b,  p.scales_a, p.scales_b, groups};
-    return cuda_status(nvf::launch_w4_gemm(q, reinterpret_cast<int*>(w),
-                                           reinterpret_cast<int*>(w + nvf::kStatusBytes),
-                                           w + nvf::kDataOffset, sms, stream));
+    return cuda_status(nvf::launch_w4_gemm(q, reinterpret_cast<int*>(w), w + nvf::kDataOffset, sms,
+                                           stream));
 }
 
 // The FFN's workspace: [status][counters][partial sums][x's rows][h][h's rows], for

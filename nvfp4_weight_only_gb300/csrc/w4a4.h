@@ -91,8 +91,8 @@ struct W4Product {
     W4Groups groups;
 };
 size_t w4_partial_bytes(int M, int experts, int num_sms);
-cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void* partials,
-                           int num_sms, cudaStream_t s);
+cudaError_t launch_w4_gemm(const W4Product& p, int* status, void* partials, int num_sms,
+                           cudaStream_t s);
 
 // experts.cu
 cudaError_t launch_experts_order(const int* ids, int tokens, int choices, int experts, int* start,

@@ -20,6 +20,7 @@
 // waits for another.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "internal.h"
@@ -32,6 +33,10 @@ namespace nvf {
 namespace {
 
 constexpr int kEpilogueWarps = 16;
+// K blocks that a cut has to save for its join (8 rows of 4096 x 4096, which it would save
+// 10: cut 7.9 us, whole 7.3; 1 row of 17408 x 5120, 53: 14.7, 23.5; 300 rows of 8192 x
+// 4096, 16: 18.9, 14.9; 2048 rows of 17408 x 5120, 51: 66.8, 71.0).
+constexpr int kJoinCost = 16;
 constexpr int kJoin = 4;  // parts of a cut tile that are asked for at a time
 constexpr int kThreads = (2 + kEpilogueWarps) * 32;
 constexpr int kEpilogueThreads = kEpilogueWarps * 32;
@@ -78,7 +83,6 @@ struct Args {
     int cut;     // K blocks of a tile that may be cut, 0 for none
     int vector;  // bytes that 16 features of a row may be stored by: 32, 16, or 2
     int* status;
-    int* counters;
     float* partials;
     unsigned long long wait_ns;
     int stall;
@@ -122,7 +126,7 @@ struct Schedule {
             sharers = over ? over * max(1, min(P / over, a.cut / S::kLeastRange)) : 0;
         } else {
             // equal shares of them all
-            sharers = min(P, left / min(S::kLeastRange, a.k_blocks));
+            sharers = a.cut ? min(P, left / S::kLeastRange) : over;
         }
         next = me;
         range0 = range1 = 0;
@@ -163,7 +167,8 @@ struct Schedule {
     // the last can be parts of tiles, and the last begins its tile, so it is part 0 there.
     __device__ float4* part(const Item& it, int i, int rank) const {
         const int sharer = it.first_part + i;
-        const bool second = i == 0 && left * sharer / sharers < it.left_over * a.k_blocks;
+        const bool second =
+            i == 0 && sharers > 0 && left * sharer / sharers < it.left_over * a.k_blocks;
         const size_t block = (size_t)sharer * S::kBlocks + rank;
         return reinterpret_cast<float4*>(a.partials + (block * 2 + second) * S::kPartial);
     }
@@ -398,6 +403,74 @@ __device__ __forceinline__ void join(const Schedule<kTokens>& schedule, const It
     }
 }
 
+// The lanes of one block alone: a row of the weight each, tokens as columns.
+template <bool kGated>
+struct FeatureLane {
+    bool odd, up;
+    float scale;
+    int feature, N, tokens, act;
+    __nv_bfloat16* out;
+
+    __device__ __forceinline__ FeatureLane(const Args& a, const Item& it, int quadrant) {
+        const int lane = threadIdx.x & 31;
+        odd = lane & 1;
+        up = kGated && lane >= 16;
+        scale = up ? (a.scales_b ? a.scales_b[it.expert] : a.scale_b)
+                   : (a.scales_a ? a.scales_a[it.expert] : a.scale_a);
+        // of a pair of lanes that trade: the even one's
+        feature = kGated ? it.weight * 64 + quadrant * 16 + (lane & 14)
+                         : it.weight * kW4Rows + quadrant * 32 + (lane & 30);
+        N = a.N;
+        tokens = it.tokens;
+        act = a.act;
+        out = a.out + (size_t)it.token0 * a.N + feature;
+    }
+
+    // Scales and stores eight tokens, column on (r: their rows' scales).  Neighbouring lanes
+    // trade, for two features of one token each.  Of a gate/up pair 16 lanes have gate, 16 up,
+    // of the same features: the first take the even tokens, the others the odd ones.
+    __device__ __forceinline__ void emit(int column, const float (&x)[8],
+                                         const float* r) const {
+        uint32_t v[4];  // pairs of tokens, in bf16
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = bf16x2(x[2 * j] * scale * r[2 * j], x[2 * j + 1] * scale * r[2 * j + 1]);
+        if (kGated) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                float h[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j + k], 16);
+                    h[k] = gated(act, up ? bf16_hi(o) : bf16_lo(v[j + k]),
+                                 up ? bf16_hi(v[j + k]) : bf16_lo(o));
+                }
+                const uint32_t own = bf16x2(h[0], h[1]);
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, own, 1);
+                const uint32_t w = odd ? prmt(o, own, 0x7632) : prmt(own, o, 0x5410);
+                const int token = column + 2 * j + (up ? 1 : 0) + (odd ? 2 : 0);
+                if (token < tokens && feature < N)
+                    *reinterpret_cast<uint32_t*>(out + (size_t)token * N) = w;
+            }
+        } else if (N & 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (column + j < tokens && feature + odd < N)
+                    *reinterpret_cast<uint16_t*>(out + (size_t)(column + j) * N + odd) =
+                        (uint16_t)(j & 1 ? v[j / 2] >> 16 : v[j / 2]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j], 1);
+                const uint32_t w = odd ? prmt(o, v[j], 0x7632) : prmt(v[j], o, 0x5410);
+                const int token = column + 2 * j + odd;
+                if (token < tokens && feature < N)
+                    *reinterpret_cast<uint32_t*>(out + (size_t)token * N) = w;
+            }
+        }
+    }
+};
+
 // A pair's lane: one token, whose features lie side by side.
 template <bool kGated>
 struct TokenRow {
@@ -480,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Barriers bars;
     __shared__ int prefix[kW4MaxExperts + 1];
     __shared__ alignas(16) float row_scale[2][kTokens];  // of two tiles in turn, read in pairs
-    __shared__ int last_part;
     __shared__ volatile int abort;
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -698,21 +770,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = (warp - 2) / 4 * (S::kBlocks > 1 ? kShare : 8);
         const uint32_t lanes = tmem + ((uint32_t)(quadrant * 32) << 16);
         bool ok = true;
-        // Counts a part of a cut tile, whose sums have been written, or which was abandoned:
-        // the counter is left at 0 all the same.  True in the block that is last.
-        auto count_part = [&] {
-            __threadfence();
-            named_barrier_sync(1, kEpilogueThreads);
-            if (eid == 0) {
-                int* const counter = a.counters + it.left_over;
-                const bool last = atom_add_acq_rel_gpu(counter, 1) == it.parts - 1;
-                if (last) *counter = 0;
-                last_part = last;
-            }
-            named_barrier_sync(1, kEpilogueThreads);
-            if (last_part) __threadfence();
-            return last_part != 0;
-        };
         auto give_back = [&](unsigned sums) {
             tmem_fence_before();
             __syncwarp();
@@ -752,101 +809,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         x[j / 8][j % 8 * 4 + 2], x[j / 8][j % 8 * 4 + 3]);
                 }
             }
-        } else
-        for (unsigned items = 0; schedule.take(it); ++items) {
-            const unsigned sums = items % S::kSums;
-            float* const scales = row_scale[items & 1];
-            if (eid < kTokens) scales[eid] = eid < it.tokens ? a.row_scales[it.token0 + eid] : 0.0f;
-            const uint32_t from = lanes + sums * kTokens;
-            const bool up = kGated && lane >= 16;
-            const float scale = up ? (a.scales_b ? a.scales_b[it.expert] : a.scale_b)
-                                   : (a.scales_a ? a.scales_a[it.expert] : a.scale_a);
-            named_barrier_sync(1, kEpilogueThreads);  // row scales are there
-            ok = ok && wait(bars.sums_full[sums], items / S::kSums);
-            tmem_fence_after();
-            const int block = it.weight * S::kBlocks + rank;
-            // of a pair of lanes that trade: the even one's
-            const int feature = kGated ? block * 64 + quadrant * 16 + (lane & 14)
-                                       : block * kW4Rows + quadrant * 32 + (lane & 30);
-            __nv_bfloat16* const out = a.out + (size_t)it.token0 * a.N + feature;
-            // Sums of two tokens, in bf16.
-            auto pack = [&](int column, float v0, float v1) {
-                const float2 r = *reinterpret_cast<const float2*>(scales + column);
-                return bf16x2(v0 * scale * r.x, v1 * scale * r.y);
-            };
-            // Stores four pairs of tokens, column on.  Neighbouring lanes trade, for two
-            // features of one token each.  Of a gate/up pair 16 lanes have gate, 16 up, of the
-            // same features: the first take the even tokens, the others the odd ones.
-            auto emit = [&](int column, const uint32_t(&v)[4]) {
-                const bool odd = lane & 1;
-                if (kGated) {
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        float h[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j + k], 16);
-                            h[k] = gated(a.act, up ? bf16_hi(o) : bf16_lo(v[j + k]),
-                                         up ? bf16_hi(v[j + k]) : bf16_lo(o));
-                        }
-                        const uint32_t own = bf16x2(h[0], h[1]);
-                        const uint32_t o = __shfl_xor_sync(0xffffffffu, own, 1);
-                        const uint32_t w = odd ? prmt(o, own, 0x7632) : prmt(own, o, 0x5410);
-                        const int token = column + 2 * j + (up ? 1 : 0) + (odd ? 2 : 0);
-                        if (token < it.tokens && feature < a.N)
-                            *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N) = w;
-                    }
-                } else if (a.N & 1) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (column + j < it.tokens && feature + odd < a.N)
-                            *reinterpret_cast<uint16_t*>(out + (size_t)(column + j) * a.N + odd) =
-                                (uint16_t)(j & 1 ? v[j / 2] >> 16 : v[j / 2]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t o = __shfl_xor_sync(0xffffffffu, v[j], 1);
-                        const uint32_t w = odd ? prmt(o, v[j], 0x7632) : prmt(v[j], o, 0x5410);
-                        const int token = column + 2 * j + odd;
-                        if (token < it.tokens && feature < a.N)
-                            *reinterpret_cast<uint32_t*>(out + (size_t)token * a.N) = w;
-                    }
-                }
-            };
-            if (it.parts == 1) {
+        } else {
+            for (unsigned items = 0; schedule.take(it); ++items) {
+                const unsigned sums = items % S::kSums;
+                float* const scales = row_scale[items & 1];
+                if (eid < kTokens)
+                    scales[eid] = eid < it.tokens ? a.row_scales[it.token0 + eid] : 0.0f;
+                const FeatureLane<kGated> feature(a, it, quadrant);
+                named_barrier_sync(1, kEpilogueThreads);  // row scales are there
+                ok = ok && wait(bars.sums_full[sums], items / S::kSums);
+                tmem_fence_after();
+                const uint32_t from = lanes + sums * kTokens;
+                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part, 0) +
+                                   quadrant * 32 + lane;
                 // the other accumulator is at work meanwhile
 #pragma unroll 1
                 for (int column = first; column < it.tokens && ok; column += 32) {
                     float x[8];
                     tmem_load8(from + column, x);
-                    const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
-                                           pack(column + 4, x[4], x[5]),
-                                           pack(column + 6, x[6], x[7])};
-                    emit(column, v);
+                    if (it.parts == 1) {
+                        feature.emit(column, x, scales + column);
+                    } else {
+                        to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
+                        to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
+                    }
                 }
                 give_back(sums);
-                continue;
-            }
-            if (ok) {
-                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part, 0) +
-                                   quadrant * 32 + lane;
-#pragma unroll 1
-                for (int column = first; column < it.tokens; column += 32) {
-                    float x[8];
-                    tmem_load8(from + column, x);
-                    to[column / 4 * kW4Rows] = make_float4(x[0], x[1], x[2], x[3]);
-                    to[(column / 4 + 1) * kW4Rows] = make_float4(x[4], x[5], x[6], x[7]);
-                }
-            }
-            give_back(sums);
-            if (!count_part() || !ok) continue;
-#pragma unroll 1
-            for (int column = first; column < it.tokens; column += 32) {
-                float x[8];
-                join<kTokens, 8>(schedule, it, 0, column, quadrant * 32 + lane, x);
-                const uint32_t v[4] = {pack(column, x[0], x[1]), pack(column + 2, x[2], x[3]),
-                                       pack(column + 4, x[4], x[5]), pack(column + 6, x[6], x[7])};
-                emit(column, v);
             }
         }
     }
@@ -858,22 +846,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kIssueWarp) tmem_free<S::kBlocks>(tmem);
 }
 
-// Joins the cut tiles of a dense product of pairs: a block has 32 columns of 128 tokens.
-// (In the product's kernel the block that came last took 14 us for the four parts of its
-// tile, 512 KB through one SM.)
-template <bool kGated>
+// Joins the cut tiles of a dense product: a block has 128 lanes of a tile, and 8 columns
+// of one block's or 32 of a pair's.  (Joined by the block that came last, in the
+// product's kernel, the four parts of a pair's tile, 512 KB through one SM, took 14 us;
+// those of one block's tile of 1 token 7 us, of 128 tokens 15 us.)
+template <int kTokens, bool kGated>
 __global__ void __launch_bounds__(kW4Rows) w4a4_join_kernel(const Args a, int pairs) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int prefix[2] = {0, (a.M + 255) / 256};
-    const Schedule<256> schedule(a, prefix, pairs, 0);
+    const int prefix[2] = {0, (a.M + kTokens - 1) / kTokens};
+    const Schedule<kTokens> schedule(a, prefix, pairs, 0);
     Item it{};
     schedule.left_over(blockIdx.x, it);
-    const int rank = blockIdx.y / 8, first = blockIdx.y % 8 * 32;
-    const TokenRow<kGated> row(a, it, rank * kW4Rows + threadIdx.x, first);
-    float x[32];
-    join<256, 32>(schedule, it, rank, first, threadIdx.x, x);
-    row.emit(0, x);
+    if (it.parts < 2) return;  // one range had all of it
+    const int lane = threadIdx.x;
+    if constexpr (kTokens == 256) {
+        const int rank = blockIdx.y / 8, first = blockIdx.y % 8 * 32;
+        const TokenRow<kGated> row(a, it, rank * kW4Rows + lane, first);
+        float x[32];
+        join<kTokens, 32>(schedule, it, rank, first, lane, x);
+        row.emit(0, x);
+    } else {
+        const int column = blockIdx.y * 8;
+        if (column >= it.tokens) return;
+        const FeatureLane<kGated> feature(a, it, lane / 32);
+        float x[8], r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            r[j] = column + j < it.tokens ? a.row_scales[it.token0 + column + j] : 0.0f;
+        join<kTokens, 8>(schedule, it, 0, column, lane, x);
+        feature.emit(column, x, r);
+    }
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -907,6 +910,26 @@ bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tiles of a dense product behind the last whole turn.
+template <int kTokens>
+int left_over(const Args& a, int pairs) {
+    return (int)((long long)((a.M + kTokens - 1) / kTokens) * a.row_blocks % pairs);
+}
+
+// Whether they are cut along K: where that saves more K blocks of time (0.3 us each) than
+// the join costs.
+template <int kTokens>
+bool cuts(const Args& a, int num_sms) {
+    const int pairs = num_sms / Shape<kTokens>::kBlocks, over = left_over<kTokens>(a, pairs);
+    if (a.start || over == 0) return false;
+    // one range of a cut tile
+    const int range = kTokens == 256
+                          ? a.k_blocks / std::max(1, std::min(pairs / over,
+                                                              a.k_blocks / Shape<256>::kLeastRange))
+                          : std::max(over * a.k_blocks / pairs, Shape<128>::kLeastRange);
+    return a.k_blocks - range > kJoinCost;
+}
+
 template <int kTokens, bool kGated>
 cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s) {
     static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory limit is set
@@ -934,19 +957,14 @@ cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = Shape<kTokens>::kBlocks > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a, maps);
-    if (kTokens == 128 || !a.cut || e != cudaSuccess) return e;
-    const int pairs = num_sms / 2;
-    const int over = (int)((long long)((a.M + 255) / 256) * a.row_blocks % pairs);
-    if (over == 0 || pairs / over < 2) return e;
-    cfg.gridDim = dim3(over, 16);
+    if (!a.cut || e != cudaSuccess) return e;
+    const int pairs = num_sms / Shape<kTokens>::kBlocks;
+    cfg.gridDim = dim3(left_over<kTokens>(a, pairs), kTokens == 256 ? 16 : (a.M + 7) / 8);
     cfg.blockDim = dim3(kW4Rows);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w4a4_join_kernel<kGated>, a, pairs);
+    return cudaLaunchKernelEx(&cfg, w4a4_join_kernel<kTokens, kGated>, a, pairs);
 }
-
-// K blocks from which a pair's tile is cut.
-constexpr int kLeastCut = 32;
 
 // Tokens per tile: rows of an expert on average, as far as the host knows them.
 bool wide(int M, int experts) { return M > 128LL * experts; }
@@ -957,8 +975,8 @@ size_t w4_partial_bytes(int M, int experts, int num_sms) {
     return (size_t)num_sms * 2 * kW4Rows * (wide(M, experts) ? 256 : 128) * sizeof(float);
 }
 
-cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void* partials,
-                           int num_sms, cudaStream_t s) {
+cudaError_t launch_w4_gemm(const W4Product& p, int* status, void* partials, int num_sms,
+                           cudaStream_t s) {
     const uint8_t* const rows = reinterpret_cast<const uint8_t*>(p.rows);
     Args a;
     a.rows = rows;
@@ -979,10 +997,7 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
     a.act = p.act;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.N * 2;
     a.vector = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 2;
-    // A join costs about 6 us beside the cut tile's parts, 18 K blocks' products.
-    a.cut = !p.groups.start && a.k_blocks >= kLeastCut ? a.k_blocks : 0;
     a.status = status;
-    a.counters = counters;
     a.partials = reinterpret_cast<float*>(partials);
     a.wait_ns = test_wait_ns();
     a.stall = test_stall();
@@ -995,9 +1010,11 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, int* counters, void*
             !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024, 2))
             return cudaErrorInvalidValue;
         a.row_blocks /= Shape<256>::kBlocks;
+        a.cut = cuts<256>(a, num_sms) ? a.k_blocks : 0;
         return p.streams == 2 ? launch<256, true>(a, maps, num_sms, s)
                               : launch<256, false>(a, maps, num_sms, s);
     }
+    a.cut = cuts<128>(a, num_sms) ? a.k_blocks : 0;
     return p.streams == 2 ? launch<128, true>(a, maps, num_sms, s)
                           : launch<128, false>(a, maps, num_sms, s);
 }

@@ -148,6 +148,22 @@ struct Places {
     int rows;
 };
 
+// A choice of a token: its expert (-1 for none, or one out of range), its row and the
+// expert's first.
+struct Choice {
+    int expert, row, first;
+};
+
+__device__ __forceinline__ Choice choice_of(const Places& to, int token, int j) {
+    const size_t at = (size_t)token * to.choices + j;
+    Choice c{to.ids[at], to.place[at], 0};
+    if (c.expert < 0 || c.expert >= to.groups.experts || c.row < 0 || c.row >= to.rows)
+        return {-1, 0, 0};
+    c.first = to.groups.start[c.expert];
+    if (c.first < 0 || c.first > c.row) c.expert = -1;
+    return c;
+}
+
 // One block per row of x; a warp takes 256 values at a time, 8 per lane, which stay in
 // registers between the row's maximum and the codes, so x is read once.  A token's codes
 // are written to the places of all of its choices.
@@ -167,6 +183,9 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
         const int c = (warp + i * warps) * 32 + lane;
         v[i] = c < vecs ? src[c] : make_uint4(0, 0, 0, 0);
     }
+    // the lists are read beside x: lane j looks up choice j
+    Choice choice{-1, 0, 0};
+    if (lane < to.choices) choice = choice_of(to, row, lane);
     long long block = 0;
     int r = 0;
     if (to.choices == 0 && !find_place(to.groups, row, block, r)) return;
@@ -242,11 +261,12 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
         return;
     }
     for (int j = 0; j < to.choices; ++j) {
-        const size_t pair_at = (size_t)row * to.choices + j;
-        const int expert = to.ids[pair_at], at_row = to.place[pair_at];
-        if (expert < 0 || expert >= to.groups.experts || at_row < 0 || at_row >= to.rows) continue;
-        const int first = to.groups.start[expert];
-        if (first < 0 || first > at_row) continue;
+        const Choice c = j < 32 ? choice : choice_of(to, row, j);
+        const int from_lane = j < 32 ? j : lane;
+        const int expert = __shfl_sync(0xffffffffu, c.expert, from_lane);
+        const int at_row = __shfl_sync(0xffffffffu, c.row, from_lane);
+        const int first = __shfl_sync(0xffffffffu, c.first, from_lane);
+        if (expert < 0) continue;
         place_of(at_row, expert, first, block, r);
         write(at_row);
     }

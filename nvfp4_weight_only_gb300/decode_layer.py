@@ -14,6 +14,10 @@ which the next layer's first norm adds.  Buffers are allocated once, the sequenc
 the device, and every call goes to the current stream, so a step can be captured in a CUDA graph
 and replayed while the lengths advance.
 
+Prompts of any length go through `prompt`, in which the projections and the FFN run on activations
+quantised to 4 bits (w4a4_quantize, w4a4_gemm, ffn_swiglu_w4a4); a layer made with prompt_tokens
+keeps the weights in that layout too, and buffers for so many rows.
+
 `python -m nvfp4_weight_only_gb300.decode_layer` runs steps of a layer with synthetic weights and
 prints the time of one.
 """
@@ -32,7 +36,7 @@ class DecodeLayer:
 
     def __init__(self, qkv, out, gate, up, down, norm_in, norm_ffn, heads, kv_heads, head_dim,
                  rope=None, interleaved=False, window=0, sinks=0, eps=1e-6, act=ffi.NVFP4_ACT_SILU,
-                 softmax_scale=None):
+                 softmax_scale=None, prompt_tokens=0):
         self.H, self.I = norm_in.numel(), gate[0].shape[0]
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.rope, self.interleaved = rope, interleaved
@@ -61,6 +65,58 @@ class DecodeLayer:
         self.attention_ws = ffi.workspace(
             max(ffi.kv8_attention_workspace_size(kv_heads, head_dim, 1024, 1, heads),
                 ffi.kv8_attention_workspace_size(kv_heads, head_dim, 1, M, heads)), dev)
+        self.prompt_tokens = prompt_tokens
+        if prompt_tokens:
+            self._prepare_prompts(qkv, out, gate, up, down, dev)
+
+    def _prepare_prompts(self, qkv, out, gate, up, down, dev):
+        M, H, I = self.prompt_tokens, self.H, self.I
+        heads, kv_heads, dim = self.heads, self.kv_heads, self.head_dim
+        self.p_qkv, self.p_out = ffi.w4a4_repack(*qkv[:2]), ffi.w4a4_repack(*out[:2])
+        self.p_gate_up = ffi.w4a4_repack_gate_up(*gate[:2], *up[:2])
+        self.p_down = ffi.w4a4_repack(*down[:2])
+        new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.p_normed, self.p_fused = new(M, H), new(M, self.rows)
+        self.p_turned, self.p_attended = new(M, heads, dim), new(M, heads, dim)
+        self.p_projected, self.p_residual, self.p_result = new(M, H), new(M, H), new(M, H)
+        # rows of the norm and of attention; a call has fewer rows and takes their front
+        size = ffi.load().w4a4_rows_bytes(M, max(H, heads * dim), 1)
+        self.p_quantized = torch.empty(size, dtype=torch.uint8, device=dev)
+        self.p_ws = ffi.workspace(max(
+            ffi.w4a4_gemm_workspace_bytes(M, self.rows, H), ffi.w4a4_gemm_workspace_bytes(M, H, heads * dim),
+            ffi.ffn_swiglu_w4a4_workspace_bytes(M, H, I)), dev)
+        self.p_attention_ws = ffi.workspace(
+            max(ffi.kv8_attention_workspace_size(kv_heads, dim, 1 << s, n, heads)
+                for s in range(11) for n in {1 << s, max(M, 1 << s)}), dev)
+
+    def _quantized(self, x):
+        M, K = x.shape
+        size = ffi.load().w4a4_rows_bytes(M, K, 1)
+        return ffi.w4a4_quantize(x, out=ffi.W4a4Rows(self.p_quantized[:size], M, K))
+
+    def prompt(self, x: torch.Tensor, residual: torch.Tensor, cache: ffi.Kv8Cache,
+               batch: ffi.Kv8Batch):
+        """x, residual bf16 [tokens, H], up to prompt_tokens of one or more sequences -> (out,
+        residual), views of the layer's buffers.  As step, with the products on 4-bit activations."""
+        M = x.shape[0]
+        if not 1 <= M <= self.prompt_tokens:
+            raise ValueError(f"this layer's prompts have 1..{self.prompt_tokens} tokens, got {M}")
+        s, heads, kv_heads, dim = self.scales, self.heads, self.kv_heads, self.head_dim
+        n, r = self.p_normed[:M], self.p_residual[:M]
+        ffi.add_rmsnorm_bf16(x, self.norm_in, self.eps, residual=residual, sum_out=r, out=n)
+        fused = ffi.w4a4_gemm(self._quantized(n), self.p_qkv, s["qkv"], self.rows, ws=self.p_ws,
+                              out=self.p_fused[:M])
+        q, k, v = fused.view(M, -1, dim).split((heads, kv_heads, kv_heads), 1)
+        q = ffi.kv8_append(cache, batch, k, v, q=q, q_out=self.p_turned[:M], rope=self.rope,
+                           interleaved=self.interleaved)
+        a = ffi.kv8_attention(q, cache, batch, self.softmax_scale, window=self.window,
+                              sinks=self.sinks, ws=self.p_attention_ws, out=self.p_attended[:M])
+        p = ffi.w4a4_gemm(self._quantized(a.view(M, -1)), self.p_out, s["out"], self.H,
+                          ws=self.p_ws, out=self.p_projected[:M])
+        ffi.add_rmsnorm_bf16(p, self.norm_ffn, self.eps, residual=r, sum_out=r, out=n)
+        out = ffi.ffn_swiglu_w4a4(n, self.p_gate_up, s["gate"], s["up"], self.p_down, s["down"],
+                                  self.I, self.act, ws=self.p_ws, out=self.p_result[:M])
+        return out, r
 
     def step(self, x: torch.Tensor, residual: torch.Tensor, cache: ffi.Kv8Cache,
              batch: ffi.Kv8Batch):
@@ -102,7 +158,7 @@ def main():
     dev = torch.device("cuda:0")
     ffi.load(build_if_missing=True)
     H, I, heads, kv_heads, dim, page, sequences, length = 5120, 17408, 40, 8, 128, 64, 16, 4096
-    layer = DecodeLayer.synthetic(H, I, heads, kv_heads, dim, dev,
+    layer = DecodeLayer.synthetic(H, I, heads, kv_heads, dim, dev, prompt_tokens=length,
                                   rope=ffi.rope_table(length + 64, dim, 500000.0, dev))
     width = (length + 64) // page
     cache = ffi.Kv8Cache.empty(sequences * width, kv_heads, page, dim, dev)
@@ -112,22 +168,36 @@ def main():
     batch = ffi.Kv8Batch(torch.arange(sequences + 1, dtype=torch.int32, device=dev),
                          torch.full((sequences,), length, dtype=torch.int32, device=dev), table)
     x, residual = [synth.activations_bf16(sequences, H, seed=i, device=dev) for i in range(2)]
-    layer.step(x, residual, cache, batch)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    prompt = ffi.Kv8Batch(ints(0, length), ints(length), table[:1].contiguous())
+    px, presidual = [synth.activations_bf16(length, H, seed=i, device=dev) for i in (2, 3)]
+
+    def token():
         batch.kv_len += 1  # the next token's position
         layer.step(x, residual, cache, batch)
+
+    what = (f"decoder layer H={H} I={I}, {heads}/{kv_heads} heads of {dim}")
+    us = _replayed(lambda: layer.prompt(px, presidual, cache, prompt))
+    print(f"{what}, a prompt of {length} tokens: {us:.1f} us")
+    us = _replayed(token)
+    print(f"{what}, {sequences} sequences of {length} tokens: {us:.1f} us per step")
+    assert ffi.kv8_batch_status(batch) == 0 and ffi.kv8_batch_status(prompt) == 0
+
+
+def _replayed(step, steps=40):
+    """Microseconds of one replay of a captured step."""
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
     graph.replay()
     begin, end = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
-    steps = 40
     begin.record()
     for _ in range(steps):
         graph.replay()
     end.record()
     torch.cuda.synchronize()
-    assert ffi.kv8_batch_status(batch) == 0
-    print(f"decoder layer H={H} I={I}, {heads}/{kv_heads} heads of {dim}, {sequences} sequences of "
-          f"{length} tokens: {begin.elapsed_time(end) / steps * 1e3:.1f} us per step")
+    return begin.elapsed_time(end) / steps * 1e3
 
 
 if __name__ == "__main__":
