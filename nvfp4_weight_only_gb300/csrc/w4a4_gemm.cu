@@ -4,20 +4,34 @@
 //   out[m][n] = bf16(r_m * (scale2 * sum_k x[m][k] w[n][k]))
 //   or, of a gate/up pair, bf16(act(g) * u) with g and u such sums in bf16.
 //
-// The weight's rows are the 128 lanes of an accumulator, tokens its columns, up to
-// kTokens of them, so that a few tokens cost few columns and a tile of the weight
-// is read once for all of them.  One thread copies tiles into a ring of stages (a
-// bulk copy each, see w4a4.h), one issues products: per stage the scales go to
-// tensor memory (the tensor cores read them there) and four products of 64 elements
-// follow.  Eight warps read the sums out, a weight row per lane.  They pack them to
-// bf16 and give the accumulator back before they store, so a tile's stores run
-// beside the next one's products.
+// Two shapes, by the rows of an expert (of the call, without experts) on average.
 //
-// Work: whole tiles in turn, then the tiles that are left over (fewer than blocks)
-// are cut along K into equal ranges, one per block.  A range that is not all of its
-// tile leaves its sums in the workspace; the block that comes last adds all parts
-// up in the order of their ranges, so results do not depend on timing, and no block
-// waits for another.
+// Up to 128: a block has 128 rows of the weight as the lanes of its accumulators and the
+// tokens as columns, as many as there are, so a few tokens cost few columns.  Bound by
+// the weight's bytes; two accumulators take turns.
+//
+// More: a pair of blocks (two SMs, one product of 256 x 256 x 64 at a time) has tokens as
+// lanes, so that the epilogue stores 32 bytes of a token's features per lane; with
+// features as lanes, 64 bytes per warp, its stores took 3.8 us a tile.  Each block copies
+// half of either operand.  Bound by the copies: a K block of 256 takes the tensor cores
+// 264 ns and the copies of 36 KB to each SM, out of L2, 333; without the half of them
+// that brings the rows it took 290.  Between tiles the accumulator is idle for about
+// 950 ns: the products' completion, the epilogue's reads, word of them to the first block,
+// copies that compete with the stores of the tile before.  A second accumulator would
+// need half of the columns.
+//
+// Both: one warp copies tiles into a ring of stages (a bulk copy or a box each, see
+// w4a4.h), one issues products: per stage the scales go to tensor memory, into columns of
+// that stage, and four products of 64 elements follow.  Sixteen warps read the sums out.
+//
+// Work: whole tiles in turn, then the tiles that are left over (fewer than blocks), which
+// a dense product may cut along K: a range that is not all of its tile leaves its sums in
+// the workspace, and a second launch adds them up in the order of the ranges.  So results
+// do not depend on timing, and no block waits for one that is not of its pair.
+//
+// Measured (us, of it the rate): 4096 x 17408 x 5120 109 (6.7 Pflop/s), 2048 x 5120 x
+// 34816 with SiLU 115 (6.3), 59 rows of 64 experts, 4096 x 4096 with SiLU 83.5 (7.2 TB/s
+// of weights), 1 x 5120 x 7168 8.5 (2.4 TB/s: start, first copies and end take 6 of it).
 #include <cuda.h>
 
 #include <algorithm>
@@ -90,7 +104,8 @@ struct Args {
 
 // Tiles as tensors of kilobytes, [block][K block][18][256 x 4 bytes], for the copies of
 // pairs: what one block copies is reported to the other's barrier, which the plain bulk
-// copies cannot.  Boxes: a whole tile, a tile's codes, the scales of two tiles.
+// copies cannot.  (With a thread that passed the word on, a stage took 545 ns or more.)
+// Boxes: a whole tile, a tile's codes, a tile's scales.
 struct Maps {
     CUtensorMap rows, codes, scales;  // the rows' whole tiles; the weight's
 };
@@ -290,15 +305,24 @@ __device__ __forceinline__ uint32_t in_first(uint32_t at) {
     return r;
 }
 
-// One box of tiles (see tile_map) from kilobyte y of tile (kb, block) on, into this
-// block's memory; `bar` may be the pair's first block's.
+// One box of a tile (see Maps) from kilobyte y of tile (kb, block) on, into this block's
+// memory, or to the same place in both blocks of the pair; `bar` is the first block's, to
+// which the copies into either are reported.
+template <bool kBoth>
 __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int y, int kb,
                                          int block, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
-        "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar)
-        : "memory");
+    if constexpr (kBoth)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".multicast::cluster.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(to),
+            "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar), "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+            "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar)
+            : "memory");
 }
 
 // True for one thread of the warp, which calls it together.
@@ -639,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kW4Tile, bar);
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
-                    copy_box(at + S::kBAt, &maps.codes, 0, kb, weight, in_first(bar));
-                    copy_box(at + S::kBScalesAt, &maps.scales, 16, kb, weight - rank,
-                             in_first(bar));
+                    copy_box<false>(at + S::kBAt, &maps.codes, 0, kb, weight, in_first(bar));
+                    copy_box<true>(at + S::kBScalesAt + rank * kW4Scales, &maps.scales,
+                                   kW4Codes / 1024, kb, weight, in_first(bar));
                 }
             }
             __syncwarp();
@@ -680,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bulk_copy_g2s(at + S::kBAt, t, columns * 128, bar);
                         bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
                     } else {
-                        copy_box(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
+                        copy_box<false>(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
                     }
                 }
                 __syncwarp();
@@ -848,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the cut tiles of a dense product: a block has 128 lanes of a tile, and 8 columns
 // of one block's or 32 of a pair's.  (Joined by the block that came last, in the
-// product's kernel, the four parts of a pair's tile, 512 KB through one SM, took 14 us;
-// those of one block's tile of 1 token 7 us, of 128 tokens 15 us.)
+// product's kernel, four parts of a pair's tile, 512 KB through one SM, took 14 us; those
+// of one block's tile of 1 token 7 us, of 128 tokens 15 us.)
 template <int kTokens, bool kGated>
 __global__ void __launch_bounds__(kW4Rows) w4a4_join_kernel(const Args a, int pairs) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -896,14 +920,13 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A map of `blocks` row blocks of tiles for boxes of `rows` kilobytes of `tiles` blocks.
-bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, int rows,
-              int tiles) {
+// A map of `blocks` row blocks of tiles for boxes of `rows` kilobytes.
+bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, int rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const cuuint64_t size[4] = {256, kW4Tile / 1024, (cuuint64_t)k_blocks, (cuuint64_t)blocks};
     const cuuint64_t stride[3] = {1024, kW4Tile, (cuuint64_t)k_blocks * kW4Tile};
-    const cuuint32_t box[4] = {256, (cuuint32_t)rows, 1, (cuuint32_t)tiles}, step[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {256, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, const_cast<void*>(at), size, stride, box,
                   step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1005,9 +1028,9 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, void* partials, int 
     if (wide(p.M, p.groups.experts)) {
         const long long blocks = w4_token_blocks(p.M, p.groups.experts);
         const long long weights = (long long)a.experts * a.row_blocks;
-        if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024, 1) ||
-            !tile_map(&maps.codes, p.packed, a.k_blocks, weights, kW4Codes / 1024, 1) ||
-            !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024, 2))
+        if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024) ||
+            !tile_map(&maps.codes, p.packed, a.k_blocks, weights, kW4Codes / 1024) ||
+            !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024))
             return cudaErrorInvalidValue;
         a.row_blocks /= Shape<256>::kBlocks;
         a.cut = cuts<256>(a, num_sms) ? a.k_blocks : 0;
