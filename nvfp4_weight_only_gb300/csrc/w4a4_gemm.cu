@@ -380,7 +380,8 @@ __device__ __forceinline__ void sync_blocks() {
 // act(g) * u for g and u in bf16: act(g) = g * sigmoid(y), y = g or the argument of GeLU's
 // tanh, doubled.  g * u is exact in fp32, and for y > 0 what sigmoid takes away from
 // it is subtracted, with one rounding.  Where that is too little for fp32, g * u itself
-// may be a tie of bf16 (it has 16 bits); the result is below it, so it goes towards 0.
+// may be a tie of bf16 (it has 16 bits): then the result, below it, goes towards 0, unless
+// sigmoid(y) is 1 in 64 bits too (a loss below 2^-54), where the tie goes to even.
 __device__ __forceinline__ float gated(int act, float g, float u) {
     const float y = act == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float e = __expf(-fabsf(y)), s = __fdividef(e, 1.0f + e);  // sigmoid(-|y|)
@@ -388,7 +389,8 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
     const float t = g * u;
     const float p = fabsf(t) < INFINITY ? fmaf(-t, s, t) : t;
     const uint32_t bits = __float_as_uint(p);
-    return p == t && (bits & 0xffffu) == 0x8000u ? __uint_as_float(bits - 1) : p;
+    const bool below = p == t && s > 5.5511151e-17f && (bits & 0xffffu) == 0x8000u;
+    return below ? __uint_as_float(bits - 1) : p;
 }
 
 // Sums of kColumns columns of a cut tile in one lane, parts in order, kJoin of them asked

@@ -962,19 +962,27 @@ def experts_order(ids: torch.Tensor, experts: int, start: torch.Tensor = None,
                   source: torch.Tensor = None, place: torch.Tensor = None):
     """ids int32 [tokens, choices] sorted by expert: (start [experts + 1], source [tokens *
     choices], place [tokens, choices]), int32."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be [tokens, choices]")
     shape, device = ids.shape, ids.get_device()
+    if len(shape) != 2:
+        raise ValueError("ids must be [tokens, choices]")
     at = _plain(ids, "ids", _I32, shape, device)
     pairs = shape[0] * shape[1]
-    new = lambda *n: torch.empty(n, dtype=_I32, device=ids.device)  # noqa: E731
-    start = new(experts + 1) if start is None else start
-    source = new(pairs) if source is None else source
-    place = new(*shape) if place is None else place
-    code = (_lib or load()).experts_order(
-        at, shape[0], shape[1], experts, _plain(start, "start", _I32, (experts + 1,), device),
-        _plain(source, "source", _I32, (pairs,), device),
-        _plain(place, "place", _I32, shape, device), _raw_stream(device))
+    # lists made here need no checks
+    if start is None:
+        start = torch.empty(experts + 1, dtype=_I32, device=ids.device)
+    else:
+        _plain(start, "start", _I32, (experts + 1,), device)
+    if source is None:
+        source = torch.empty(pairs, dtype=_I32, device=ids.device)
+    else:
+        _plain(source, "source", _I32, (pairs,), device)
+    if place is None:
+        place = torch.empty(shape, dtype=_I32, device=ids.device)
+    else:
+        _plain(place, "place", _I32, shape, device)
+    code = (_lib or load()).experts_order(at, shape[0], shape[1], experts, start.data_ptr(),
+                                          source.data_ptr(), place.data_ptr(),
+                                          _raw_stream(device))
     if code:
         _check("experts_order", code)
     return start, source, place

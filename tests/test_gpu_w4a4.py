@@ -186,7 +186,8 @@ def test_gate_up(dev, M, H, I, kind):
 
 
 def test_gated_products_that_are_ties_of_bf16(dev):
-    """Large g: the sigmoid's loss decides a product that lies between two bf16 values."""
+    """Large g: the sigmoid's loss decides a product that lies between two bf16 values, as long as
+    64 bits have it; else the tie goes to even."""
     I, H = 16, 256
     codes = torch.zeros((I, H // 2), dtype=torch.uint8, device=dev)
     codes[:, 0] = 2  # weight 1 at element 0
@@ -195,10 +196,11 @@ def test_gated_products_that_are_ties_of_bf16(dev):
     x = torch.zeros((300, H), device=dev)
     x[:, 0] = 6.0
     few, many = [ffi.w4a4_quantize(x[:n].to(BF)) for n in (20, 300)]
-    # g * u = 64 * 323, 128 * 315, 128 * 325, 64 * 323: half a step from both neighbours; act(g)
-    # is below g, by too little for 32 bits
-    for g, u, want in ((136, 152, 20608), (168, 240, 40192), (200, 208, 41472), (152, -136, -20608)):
-        for kind in (0, 1):
+    # g * u = 8 * 315, 16 * 323, 64 * 323, 128 * 315, 128 * 325: half a step from both neighbours
+    for g, u, silu, gelu in ((20, 126, 2512, 2528), (34, 152, 5152, 5184), (34, -152, -5152, -5184),
+                             (136, 152, 20736, 20736), (168, 240, 40448, 40448),
+                             (200, 208, 41472, 41472)):
+        for kind, want in ((0, silu), (1, gelu)):
             for rows in few, many:
                 got = ffi.w4a4_gate_up(rows, packed, g / 6, u / 6, I, kind)
                 assert bool((got == want).all()), (g, u, kind)
