@@ -20,7 +20,7 @@
 // copies that compete with the stores of the tile before.  A second accumulator would
 // need half of the columns.
 //
-// Both: one warp copies tiles into a ring of stages (a bulk copy or a box each, see
+// Both: two warps copy tiles into a ring of stages (a bulk copy or a box each, see
 // w4a4.h), one issues products: per stage the scales go to tensor memory, into columns of
 // that stage, and four products of 64 elements follow.  Sixteen warps read the sums out.
 //
@@ -52,7 +52,7 @@ constexpr int kEpilogueWarps = 16;
 // 4096, 16: 18.9, 14.9; 2048 rows of 17408 x 5120, 51: 66.8, 71.0).
 constexpr int kJoinCost = 16;
 constexpr int kJoin = 4;  // parts of a cut tile that are asked for at a time
-constexpr int kThreads = (2 + kEpilogueWarps) * 32;
+constexpr int kThreads = (3 + kEpilogueWarps) * 32;
 constexpr int kEpilogueThreads = kEpilogueWarps * 32;
 // Token tiles that take turns with one weight tile before the next one: their tiles
 // (16 x 256 tokens of K = 17408: 40 MB) stay in L2 for it.
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_addr(shared);
-    constexpr int kCopyWarp = 0, kIssueWarp = 1;
+    constexpr int kWeightWarp = 0, kIssueWarp = 1, kRowsWarp = 2 + kEpilogueWarps;
     const int rank = blockIdx.x % S::kBlocks;  // in the pair
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort = 0;
         fence_mbar_init();
     }
-    // Without lists to read, the weight's first tiles are copied before the preceding
-    // kernel is done.
+    // Without lists to read, the weight's first tiles are copied while the preceding kernel
+    // is still at work.
     const bool early = a.start == nullptr;
     if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
     // token tiles of each expert; one whose rows are not all inside has none
@@ -650,42 +650,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     Schedule<kTokens> schedule(a, prefix, gridDim.x / S::kBlocks, blockIdx.x / S::kBlocks);
     Item it{};
-    if (warp == kCopyWarp) {
-        const bool issuer = elect_one();
-        // The weight's part of a stage; the stage's bytes are announced with it.
-        auto copy_weight = [&](unsigned n, int kb) {
-            if (issuer) {
-                const int stage = n % S::kStages;
-                const uint32_t at = smem + stage * S::kStageBytes;
-                const uint32_t bar = smem_addr(&bars.full[stage]);
-                const int weight = (it.expert * a.row_blocks + it.weight) * S::kBlocks + rank;
-                if constexpr (S::kBlocks == 1) {
-                    mbar_arrive_expect_tx(bar, kW4Tile + S::columns(it.tokens) * 128 + kW4Scales);
-                    bulk_copy_g2s(at, a.packed + ((size_t)weight * a.k_blocks + kb) * kW4Tile,
-                                  kW4Tile, bar);
-                } else {
-                    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
-                    copy_box<false>(at + S::kBAt, &maps.codes, 0, kb, weight, in_first(bar));
-                    copy_box<true>(at + S::kBScalesAt + rank * kW4Scales, &maps.scales,
-                                   kW4Codes / 1024, kb, weight, in_first(bar));
-                }
-            }
-            __syncwarp();
-        };
-        unsigned ahead = 0;
-        if (early) {
-            Schedule<kTokens> first = schedule;
-            while (ahead < S::kStages && first.take(it))
-                for (int kb = it.kb0; kb < it.kb1 && ahead < S::kStages && !(a.stall && ahead);
-                     ++kb, ++ahead)
-                    copy_weight(ahead, kb);
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-        }
+    if (warp == kWeightWarp || warp == kRowsWarp) {
+        // Two warps, since a copy takes its thread about 80 cycles.
+        const bool issuer = elect_one(), rows = warp == kRowsWarp;
+        if (rows && early) asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned n = 0;  // stages filled
         bool ok = true;
         while (ok && schedule.take(it)) {
-            const uint8_t* x = a.rows + (size_t)it.block * a.k_blocks * kW4Tile;
-            const int columns = S::columns(it.tokens);
+            const int weight = (it.expert * a.row_blocks + it.weight) * S::kBlocks + rank;
+            const uint8_t* const from = rows ? a.rows + (size_t)it.block * a.k_blocks * kW4Tile
+                                             : a.packed + (size_t)weight * a.k_blocks * kW4Tile;
+            const int codes = S::columns(it.tokens) * 128;  // of the rows, to one block alone
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
                 if (n >= S::kStages) {
@@ -697,16 +672,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (n >= ahead) copy_weight(n, kb);
                 if (issuer) {
                     const uint32_t at = smem + stage * S::kStageBytes;
-                    const uint32_t bar = smem_addr(&bars.full[stage]);
+                    uint32_t bar = smem_addr(&bars.full[stage]);
+                    // the weight's warp announces the bytes of all of the stage's copies
                     if constexpr (S::kBlocks == 1) {
-                        const uint8_t* t = x + (size_t)kb * kW4Tile;
-                        bulk_copy_g2s(at + S::kBAt, t, columns * 128, bar);
-                        bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
-                    } else {
+                        const uint8_t* const t = from + (size_t)kb * kW4Tile;
+                        if (rows) {
+                            bulk_copy_g2s(at + S::kBAt, t, codes, bar);
+                            bulk_copy_g2s(at + S::kBScalesAt, t + kW4Codes, kW4Scales, bar);
+                        } else {
+                            mbar_arrive_expect_tx(bar, kW4Tile + codes + kW4Scales);
+                            bulk_copy_g2s(at, t, kW4Tile, bar);
+                        }
+                    } else if (rows) {
                         copy_box<false>(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
+                        bar = in_first(bar);
+                        copy_box<false>(at + S::kBAt, &maps.codes, 0, kb, weight, bar);
+                        copy_box<true>(at + S::kBScalesAt + rank * kW4Scales, &maps.scales,
+                                       kW4Codes / 1024, kb, weight, bar);
                     }
                 }
                 __syncwarp();
@@ -717,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bars.empty[i % S::kStages], i / S::kStages);
         if (abort) {
             // copies under way end before the memory that they write is left; these waits
-            // heed nobody's
+            // heed nobody's, and end for stages that lack the other warp's
             const int none = 0;
             if (rank == 0)
                 for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
@@ -787,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issuer) commit<S::kBlocks>(smem_addr(&bars.drained));
             mbar_wait_bounded(smem_addr(&bars.drained), 0, &none);
         }
-    } else if (warp > kIssueWarp) {
+    } else if (warp > kIssueWarp) {  // the epilogue
         if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
         // a warp reads 32 lanes of a share of the columns
         constexpr int kShare = kTokens * 4 / kEpilogueWarps;
