@@ -7,9 +7,10 @@
  *   x, out BF16;  gate [I, H], up [I, H], down [H, I] NVFP4;  act = SiLU | GeLU-tanh.
  *
  * Beside it: a LoRA delta overlay on the same FFN, the FFN and GEMV on
- * block-scaled FP8 weights (the w8a16 calls), and the attention side of a
- * decode layer (norm, rotary positions, 8-bit paged cache, attention; near
- * the end of this header).
+ * block-scaled FP8 weights (the w8a16 calls), the attention side of a
+ * decode layer (norm, rotary positions, 8-bit paged cache, attention), and
+ * products for many rows on activations quantised to 4 bits, dense and by
+ * expert (the w4a4 and experts calls; near the end of this header).
  *
  * What the calls restate (Atlas engine pages):
  *  - "spark_model/layers/dense_ffn.rs", module doc comment: the dense SwiGLU

@@ -21,7 +21,8 @@ extern "C" {
  * returns, and the call's outputs are left unwritten.  kv8_attention with more
  * than 32 rows (new tokens times query heads per kv head) per sequence on
  * average, and heads of at most 128 values, copies half of a block's pages and
- * then none, and leaves wrong outputs.  The kernel still ends
+ * then none, and leaves wrong outputs.  The w4a4 products copy one stage of a
+ * block's tiles, and leave wrong outputs.  The kernel still ends
  * every wait and leaves no copy in flight.  enable == 0 restores normal
  * operation (1 s limit).  Not synchronised with launches on other threads.
  */

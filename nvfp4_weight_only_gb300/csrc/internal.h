@@ -83,7 +83,8 @@ bool gemv_plan_aligned(int streams, int M, int N, int K, int num_sms, bool f8 = 
 // Testing only: with stall != 0 every later GEMV/FFN launch runs with a
 // producer that issues no copies and bounded waits of wait_ns, so each
 // launch abandons its first wait and reports NVFP4_ERR_TIMEOUT.  The attention
-// kernel for many rows copies half of a block's tiles before it does so.
+// kernel for many rows copies half of a block's tiles before it does so, the 4-bit
+// products one stage.
 void set_test_stall(int stall, unsigned long long wait_ns);
 
 // Host-side argument checks of ffn_swiglu_nvfp4 that do not involve the
