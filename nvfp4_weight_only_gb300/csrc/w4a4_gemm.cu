@@ -182,8 +182,7 @@ struct Schedule {
     // the last can be parts of tiles, and the last begins its tile, so it is part 0 there.
     __device__ float4* part(const Item& it, int i, int rank) const {
         const int sharer = it.first_part + i;
-        const bool second =
-            i == 0 && sharers > 0 && left * sharer / sharers < it.left_over * a.k_blocks;
+        const bool second = i == 0 && left * sharer / sharers < it.left_over * a.k_blocks;
         const size_t block = (size_t)sharer * S::kBlocks + rank;
         return reinterpret_cast<float4*>(a.partials + (block * 2 + second) * S::kPartial);
     }
@@ -664,6 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
                 if (n >= S::kStages) {
+                    // a limited wait does not begin before the preceding kernel is done
+                    if (n == S::kStages && early && !rows)
+                        asm volatile("griddepcontrol.wait;" ::: "memory");
                     ok = wait(bars.empty[stage], n / S::kStages - 1);
                     if (!ok) break;
                 }
@@ -699,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // the last products' word has come before the barriers that it goes to are left
+        if (early && !rows) asm volatile("griddepcontrol.wait;" ::: "memory");
         for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n && ok; ++i)
             ok = wait(bars.empty[i % S::kStages], i / S::kStages);
         if (abort) {
@@ -719,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the start, each of these instructions took about 60 cycles (their operands have to
         // be the same for the warp), 1030 for a stage's.
         const bool issuer = elect_one();
+        if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned n = 0, items = 0;
         bool ok = true;
         while (ok && schedule.take(it)) {
@@ -832,8 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && wait(bars.sums_full[sums], items / S::kSums);
                 tmem_fence_after();
                 const uint32_t from = lanes + sums * kTokens;
-                float4* const to = schedule.part(it, (int)blockIdx.x - it.first_part, 0) +
-                                   quadrant * 32 + lane;
+                float4* const to =
+                    it.parts == 1 ? nullptr
+                                  : schedule.part(it, (int)blockIdx.x - it.first_part, 0) +
+                                        quadrant * 32 + lane;
                 // the other accumulator is at work meanwhile
 #pragma unroll 1
                 for (int column = first; column < it.tokens && ok; column += 32) {
@@ -870,7 +876,6 @@ __global__ void __launch_bounds__(kW4Rows) w4a4_join_kernel(const Args a, int pa
     const Schedule<kTokens> schedule(a, prefix, pairs, 0);
     Item it{};
     schedule.left_over(blockIdx.x, it);
-    if (it.parts < 2) return;  // one range had all of it
     const int lane = threadIdx.x;
     if constexpr (kTokens == 256) {
         const int rank = blockIdx.y / 8, first = blockIdx.y % 8 * 32;
@@ -983,6 +988,7 @@ bool wide(int M, int experts) { return M > 128LL * experts; }
 }  // namespace
 
 size_t w4_partial_bytes(int M, int experts, int num_sms) {
+    if (experts > 1) return 0;  // their tiles are not cut
     return (size_t)num_sms * 2 * kW4Rows * (wide(M, experts) ? 256 : 128) * sizeof(float);
 }
 

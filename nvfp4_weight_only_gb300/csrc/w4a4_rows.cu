@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
     for (int i = 0; i < kIter; ++i) {
         const float largest = __uint_as_float(max(top[i] & 0xffffu, top[i] >> 16) << 16) * down;
         const uint32_t sixth = __float_as_uint(largest * (1.0f / 6.0f));
-        const uint32_t code = f32_to_e4m3(__uint_as_float((sixth + 0x400u) & ~0x7ffu));
+        // (of a row with a NaN anything without a sign)
+        const uint32_t code = f32_to_e4m3(__uint_as_float((sixth + 0x400u) & ~0x7ffu)) & 0x7fu;
         const float by = code ? reciprocal(e4m3_to_f32(code)) * down : 0.0f;
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         const uint64_t by2 = pair(by, by), grid = pair(768.0f, 768.0f), back = pair(-768.0f, -768.0f);

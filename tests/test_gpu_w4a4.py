@@ -159,6 +159,9 @@ SIZES = [(1, 256, 128), (1, 16, 1), (2, 272, 77), (15, 512, 128), (16, 512, 130)
          (1000, 1024, 1000), (2048, 2048, 2056), (1025, 16384, 3000), (513, 8992, 2432)]
 
 
+SIZES += [(5, 17408, 130), (128, 8192, 264), (77, 65536, 48), (300, 65536, 48), (40, 21504, 5376)]
+
+
 @pytest.mark.parametrize("M,K,N", SIZES)
 def test_gemm(dev, M, K, N):
     x, w = draw(M, K, M, dev), draw_weight(N, K, N, dev)
@@ -176,7 +179,8 @@ def test_gemm(dev, M, K, N):
 @pytest.mark.parametrize("kind", [0, 1])
 @pytest.mark.parametrize("M,H,I", [(1, 16, 16), (1, 5120, 512), (20, 272, 208), (48, 4096, 1024),
                                    (128, 512, 4000), (129, 256, 64), (200, 1040, 336),
-                                   (600, 8192, 1040), (2000, 512, 1024)])
+                                   (600, 8192, 1040), (2000, 512, 1024), (128, 12288, 272),
+                                   (300, 16384, 528)])
 def test_gate_up(dev, M, H, I, kind):
     x, gate, up = draw(M, H, M, dev), draw_weight(I, H, 1, dev), draw_weight(I, H, 2, dev)
     packed = ffi.w4a4_repack_gate_up(*gate[:2], *up[:2])
@@ -315,6 +319,70 @@ def test_lists_that_do_not_fit(dev, list_):
             mine = slice(list_[e], list_[e + 1])
             check(y[1:M + 1][mine], *ref.product(ref.values(x[mine]), of_expert(w, e)))
         assert bool((y[41:M + 1] == -7).all())
+
+
+def test_a_thousand_experts(dev):
+    E, K, N = 1024, 256, 48
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 4, (E,), generator=g).tolist()
+    lens[700] = 300
+    M, start = sum(lens), starts(lens, 0, dev)
+    x, w = draw(M, K, 1, dev), draw_weight(N, K, 2, dev, E)
+    y = ffi.w4a4_gemm(ffi.w4a4_quantize(x, start=start), ffi.w4a4_repack(*w[:2]), w[2], N)
+    v, at = ref.values(x), start.tolist()
+    for e in range(E):
+        if lens[e]:
+            mine = slice(at[e], at[e + 1])
+            check(y[mine], *ref.product(v[mine], of_expert(w, e)))
+
+
+def test_rows_that_are_not_finite_by_expert(dev):
+    x, E, I, H = draw(200, 256, 1, dev), 2, 64, 256
+    x[3, 5], x[150, 7] = math.nan, math.inf
+    gate, up = draw_weight(I, H, 2, dev, E), draw_weight(I, H, 3, dev, E)
+    s = torch.full((E,), 1e-4, device=dev)
+    rows = ffi.w4a4_quantize(x, start=starts([100, 100], 0, dev))
+    h = ffi.w4a4_gate_up(rows, ffi.w4a4_repack_gate_up(*gate[:2], *up[:2]), s, s, I)
+    assert bool(torch.isnan(h[[3, 150]]).all())
+    fine = [r for r in range(200) if r not in (3, 150)]
+    assert bool(torch.isfinite(h[fine]).all())
+
+
+def test_offsets_beyond_32_bits(dev):
+    """An output, an experts' weight and quantised rows of more than 2^32 bytes: their last rows."""
+    M, K, N = 65600, 16, 33000
+    x, w = draw(M, K, 1, dev), draw_weight(N, K, 2, dev)
+    y = ffi.w4a4_gemm(ffi.w4a4_quantize(x), ffi.w4a4_repack(*w[:2]), w[2], N)
+    for rows in (slice(0, 3), slice(M - 300, M)):
+        check(y[rows], *ref.product(ref.values(x[rows]), ref.weight(*w)))
+    del y
+    E, K, N = 300, 16384, 2048
+    codes = torch.zeros((E, N, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.zeros((E, N, K // 16), dtype=torch.uint8, device=dev)
+    last = draw_weight(N, K, 3, dev)
+    codes[E - 1], scales[E - 1] = last[0], last[1]
+    packed = ffi.w4a4_repack(codes, scales)
+    assert packed.numel() > 2 ** 32
+    del codes, scales
+    x = draw(70, K, 4, dev)
+    s = torch.full((E,), last[2], device=dev)
+    start = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    start[E] = 70  # all rows are the last expert's
+    for n in (70, 70 * 600):  # both kernels
+        x = draw(n, K, 4, dev)
+        start[E] = n
+        y = ffi.w4a4_gemm(ffi.w4a4_quantize(x, start=start), packed, s, N)
+        check(y[-70:], *ref.product(ref.values(x[-70:]), ref.weight(*last)))
+    del packed, y
+    M, K = 150000, 65536  # 5.5 GB of tiles, 19.7 GB of x
+    x = torch.zeros((M, K), dtype=BF, device=dev)
+    x[-200:] = draw(200, K, 5, dev)
+    rows = ffi.w4a4_quantize(x)
+    assert rows.data.numel() > 2 ** 32
+    w = draw_weight(32, K, 6, dev)
+    y = ffi.w4a4_gemm(rows, ffi.w4a4_repack(*w[:2]), w[2], 32)
+    check(y[-200:], *ref.product(ref.values(x[-200:]), ref.weight(*w)))
+    assert bool((y[:-200] == 0).all())
 
 
 # ------------------------------------------------------------------ routing

@@ -41,7 +41,8 @@ def test_sizes(lib):
     assert lib.w4a4_repacked_gate_up_bytes(1, 24, 16) == 0
     assert lib.w4a4_rows_bytes(0, 16, 1) == lib.w4a4_rows_bytes((1 << 22) + 1, 16, 1) == 0
     assert lib.w4a4_gemm_workspace_bytes(0, 16, 16, 1) == 0
-    assert lib.w4a4_gemm_workspace_bytes(1, 16, 16, 1) > 1 << 17
+    assert lib.w4a4_gemm_workspace_bytes(1, 16, 16, 1) > lib.w4a4_gemm_workspace_bytes(1, 16, 16, 2)
+    assert lib.w4a4_gemm_workspace_bytes(1, 16, 16, 2) > 1 << 17
     assert lib.ffn_swiglu_w4a4_workspace_bytes(1, 16, 24) == 0
     assert lib.ffn_swiglu_w4a4_workspace_bytes(70, 256, 512) > 70 * 512 * 2
     assert lib.experts_swiglu_w4a4_workspace_bytes(4, 65, 80, 256, 512) == 0
