@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinExp = -100, kMaxExp = 117;
-constexpr int kQuantizeWarps = 2;
+constexpr int kFewRows = 152;  // blocks that there is an SM for each
 
 // One thread per 16 code bytes of a tile (two scale bytes with them).
 __global__ void __launch_bounds__(kThreads) repack_kernel(
@@ -349,8 +349,11 @@ cudaError_t quantize(const void* x, int blocks, int M, int K, const Places& to, 
     const int k_blocks = w4_k_blocks(K);
     // Two warps per row as long as 8 vectors per lane hold it: small blocks, whose loads and
     // stores overlap others' (16384 rows of 2048: 18.1 us, with 4 warps 20.1, with 8 28.9).
+    // Few rows leave room for eight, each with less to write (64 tokens of 4096 values for 8
+    // experts each: 3.2 us, with two warps 4.1; 300 for 2: 3.0, 2.8).
+    const int most = blocks <= kFewRows ? 8 : 2;
     int iter = 1;
-    while (iter < 8 && k_blocks > kQuantizeWarps * iter) iter *= 2;
+    while (iter < 8 && k_blocks > most * iter) iter *= 2;
     const int warps = (k_blocks + iter - 1) / iter;
     auto kernel = iter == 1   ? quantize_kernel<1>
                   : iter == 2 ? quantize_kernel<2>
