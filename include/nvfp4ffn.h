@@ -602,8 +602,9 @@ nvfp4_status w4a4_unpack(const void* packed, int experts, int N, int K, uint8_t*
  * Rows that belong to experts: rows start[e] .. start[e+1] - 1 of the call's M to
  * expert e.  start does not decrease; rows in front of start[0] and from
  * start[experts] on belong to none: nothing is read or written for them.  The
- * lists live on the device and are not read by the host.  The kernels check them:
- * an expert whose rows do not lie in 0..M has none.
+ * lists live on the device and are not read by the host.  The products check them:
+ * an expert whose rows do not lie in 0..M has none, and where start decreases no
+ * expert has any; w4a4_quantize leaves rows out that have no place.
  */
 typedef struct {
     const int* start; /* (device) [experts + 1] */

@@ -118,7 +118,8 @@ struct Item {
     int parts, first_part, left_over;    // parts > 1: sharers first_part .. + parts - 1
 };
 
-// The list of work of a block, or of a pair.  prefix[e]: token tiles of the experts in front of e.
+// The list of work of a block, or of a pair.  prefix[e]: token tiles of the experts in
+// front of e.
 template <int kTokens>
 struct Schedule {
     using S = Shape<kTokens>;
@@ -127,7 +128,6 @@ struct Schedule {
     int tiles, whole, sharers;
     int left;  // K blocks of the tiles that are left over: fewer than blocks of up to 256
     int next, range0, range1;
-
     int P;  // blocks, or pairs
 
     __device__ Schedule(const Args& args, const int* tile_prefix, int pairs, int me)
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const shared = dynamic + (-smem_addr(dynamic) & 1023u);
     __shared__ Barriers bars;
     __shared__ int prefix[kW4MaxExperts + 1];
-    __shared__ alignas(16) float row_scale[2][kTokens];  // of two tiles in turn, read in pairs
+    __shared__ alignas(16) float row_scale[2][kTokens];  // one block's: of two tiles in turn
     __shared__ volatile int abort;
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -604,16 +604,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // is still at work.
     const bool early = a.start == nullptr;
     if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    // token tiles of each expert; one whose rows are not all inside has none
+    // token tiles of each expert; one whose rows are not all inside has none, and none has
+    // any where the list decreases (shares that overlap could be more than tiles are counted)
     if (tid == 0) prefix[0] = 0;
+    bool decreases = false;
     for (int e = tid; e < a.experts; e += kThreads) {
         const int first = a.start ? a.start[e] : 0, end = a.start ? a.start[e + 1] : a.M;
+        decreases |= end < first;
         prefix[e + 1] = first >= 0 && end <= a.M && end > first
                             ? (end - first + kTokens - 1) / kTokens
                             : 0;
     }
-    __syncthreads();
-    if (warp == 2 && a.experts > 1) {
+    if (__syncthreads_or(decreases)) {
+        for (int e = tid; e < a.experts; e += kThreads) prefix[e + 1] = 0;
+    } else if (warp == 2 && a.experts > 1) {
         int sum = 0;
         for (int base = 1; base <= a.experts; base += 32) {
             int v = base + lane <= a.experts ? prefix[base + lane] : 0;
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Schedule<kTokens> schedule(a, prefix, gridDim.x / S::kBlocks, blockIdx.x / S::kBlocks);
     Item it{};
     if (warp == kWeightWarp || warp == kRowsWarp) {
-        // Two warps, since a copy takes its thread about 80 cycles.
+        // Two warps, since a copy takes its thread about 200 cycles.
         const bool issuer = elect_one(), rows = warp == kRowsWarp;
         if (rows && early) asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned n = 0;  // stages filled

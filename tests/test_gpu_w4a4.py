@@ -385,6 +385,17 @@ def test_offsets_beyond_32_bits(dev):
     assert bool((y[:-200] == 0).all())
 
 
+@pytest.mark.parametrize("M", [100, 9000])
+def test_a_list_that_decreases_leaves_every_row_out(dev, M):
+    E, K, N = 64, 256, 64
+    x, w = draw(M, K, 1, dev), draw_weight(N, K, 2, dev, E)
+    start = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32, device=dev)
+    rows = ffi.w4a4_quantize(x, start=start)
+    y = torch.full((M, N), -7.0, dtype=BF, device=dev)
+    ffi.w4a4_gemm(rows, ffi.w4a4_repack(*w[:2]), w[2], N, out=y)
+    assert bool((y == -7).all())
+
+
 # ------------------------------------------------------------------ routing
 
 def draw_ids(T, k, E, seed, dev, outside=True):
