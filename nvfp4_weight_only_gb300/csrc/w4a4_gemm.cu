@@ -13,12 +13,13 @@
 // More: a pair of blocks (two SMs, one product of 256 x 256 x 64 at a time) has tokens as
 // lanes, so that the epilogue stores 32 bytes of a token's features per lane; with
 // features as lanes, 64 bytes per warp, its stores took 3.8 us a tile.  Each block copies
-// half of either operand.  Bound by the copies: a K block of 256 takes the tensor cores
-// 264 ns and the copies of 36 KB to each SM, out of L2, 333; without the half of them
-// that brings the rows it took 290.  Between tiles the accumulator is idle for about
-// 950 ns: the products' completion, the epilogue's reads, word of them to the first block,
-// copies that compete with the stores of the tile before.  A second accumulator would
-// need half of the columns.
+// half of either operand.  Bound by what an SM takes in: a K block of 256 takes the
+// tensor cores 264 ns, and its 38 KB, out of L2, 333 (59 bytes a cycle); without the rows'
+// 18 it took 290, with a sixth stage as long.  A tile that needs less of them per product
+// needs more columns of sums than the scales leave.  Between tiles the accumulator is idle
+// for about 950 ns: the products' completion, the epilogue's reads, word of them to the
+// first block, copies that compete with the stores of the tile before.  A second
+// accumulator would need half of the columns.
 //
 // Both: two warps copy tiles into a ring of stages (a bulk copy or a box each, see
 // w4a4.h), one issues products: per stage the scales go to tensor memory, into columns of
