@@ -15,11 +15,12 @@
 // features as lanes, 64 bytes per warp, its stores took 3.8 us a tile.  Each block copies
 // half of either operand.  Bound by what an SM takes in: a K block of 256 takes the
 // tensor cores 264 ns, and its 38 KB, out of L2, 333 (59 bytes a cycle); without the rows'
-// 18 it took 290, with a sixth stage as long.  A tile that needs less of them per product
-// needs more columns of sums than the scales leave.  Between tiles the accumulator is idle
-// for about 950 ns: the products' completion, the epilogue's reads, word of them to the
-// first block, copies that compete with the stores of the tile before.  A second
-// accumulator would need half of the columns.
+// 18 it took 290, with a sixth stage as long.  Tiles of 256 x 384, which need fewer bytes
+// per product, came to 6.0 Pflop/s against 6.7: their 48 KB took 500 ns without the third
+// 128 columns' products, 570 with them.  Between tiles the accumulator is idle for about
+// 950 ns: the products' completion, the epilogue's reads, word of them to the first block,
+// copies that compete with the stores of the tile before.  A second accumulator would need
+// half of the columns.
 //
 // Both: two warps copy tiles into a ring of stages (a bulk copy or a box each, see
 // w4a4.h), one issues products: per stage the scales go to tensor memory, into columns of
