@@ -12,8 +12,9 @@
 // launch's block of that chunk reads, and then writes.
 //
 // Sum: out[t] = bf16(sum_j weights[t][j] * y[place[t][j]]), fp32, in the order of j.
-// Bound by memory: every thread has 8 columns of a token and asks for all of its
-// rows at once.
+// Bound by memory: every thread has 8 columns of a token and asks for its rows four or
+// eight at once (8192 tokens of 8 rows of 4096: 91 us, 6.6 TB/s; 4096 of 4: 27.4 us, 6.1,
+// with eight asked for there too 33.6).
 #include <atomic>
 
 #include "kv8.cuh"
@@ -27,7 +28,6 @@ constexpr int kOrderThreads = 1024;
 constexpr int kManyPairs = 24576;
 constexpr long long kManyCompares = 1 << 20;
 constexpr int kSumThreads = 256;
-constexpr int kAhead = 8;  // rows of a token asked for at once
 
 // Ids base + 4 lane .. + 3 of a warp's 128, -1 beyond the end.
 __device__ __forceinline__ void load4(const int* ids, long long at, long long end, int (&v)[4]) {
@@ -252,18 +252,21 @@ __global__ void __launch_bounds__(kChunk) chunk_place_kernel(const int* __restri
         source[r] = -1;
 }
 
+// `share` threads, a power of two, have a token's next 8 * share columns.
+template <int kAhead>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restrict__ y, int rows,
                                                           const int* __restrict__ place,
                                                           const float* __restrict__ weights,
-                                                          long long vectors, int choices, int vecs,
-                                                          uint4* __restrict__ out) {
+                                                          int tokens, int choices, int vecs,
+                                                          int share, uint4* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long at = blockIdx.x * (long long)kSumThreads + threadIdx.x;
-    if (at >= vectors) return;
-    const long long token = at / vecs;
-    const int c = (int)(at - token * vecs);
-    float sum[8] = {};
+    const int token = blockIdx.x * (kSumThreads / share) + threadIdx.x / share;
+    const int c = blockIdx.y * share + threadIdx.x % share;
+    if (token >= tokens || c >= vecs) return;
+    place += (size_t)token * choices;
+    weights += (size_t)token * choices;
+    uint64_t sum[4] = {};  // pairs
     for (int base = 0; base < choices; base += kAhead) {
         uint4 v[kAhead];
         float w[kAhead];
@@ -272,9 +275,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restric
             v[j] = make_uint4(0, 0, 0, 0);
             w[j] = 0.0f;
             if (base + j < choices) {
-                const int p = place[token * choices + base + j];
+                const int p = place[base + j];
                 if (p >= 0 && p < rows) {
-                    w[j] = weights[token * choices + base + j];
+                    w[j] = weights[base + j];
                     v[j] = y[(size_t)p * vecs + c];
                 }
             }
@@ -282,22 +285,25 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restric
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            const uint64_t w2 = pair(w[j], w[j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[2 * i] = fmaf(w[j], bf16_lo(u[i]), sum[2 * i]);
-                sum[2 * i + 1] = fmaf(w[j], bf16_hi(u[i]), sum[2 * i + 1]);
-            }
+            for (int i = 0; i < 4; ++i) sum[i] = fma2(w2, pair(bf16_lo(u[i]), bf16_hi(u[i])), sum[i]);
         }
     }
-    out[at] = make_uint4(bf16x2(sum[0], sum[1]), bf16x2(sum[2], sum[3]), bf16x2(sum[4], sum[5]),
-                         bf16x2(sum[6], sum[7]));
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 s = unpair(sum[i]);
+        o[i] = bf16x2(s.x, s.y);
+    }
+    out[(size_t)token * vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), unsigned blocks, int threads, size_t shared,
+cudaError_t launch(void (*kernel)(Args...), dim3 blocks, int threads, size_t shared,
                    cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = blocks;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = s;
@@ -326,24 +332,31 @@ cudaError_t launch_experts_order(const int* ids, int tokens, int choices, int ex
             if (dev < 64) allowed[dev].store(true, std::memory_order_release);
         }
         const int chunks = pairs / kChunk;
-        e = launch(chunk_count_kernel, (unsigned)chunks, kChunk, 0, s, ids, pairs, experts, place);
+        e = launch(chunk_count_kernel, dim3(chunks), kChunk, 0, s, ids, pairs, experts, place);
         if (e != cudaSuccess) return e;
-        e = launch(chunk_sum_kernel, 1u, 1024, 0, s, chunks, experts, start, place);
+        e = launch(chunk_sum_kernel, dim3(1), 1024, 0, s, chunks, experts, start, place);
         if (e != cudaSuccess) return e;
-        return launch(chunk_place_kernel, (unsigned)chunks, kChunk, 32 * experts * sizeof(int), s,
+        return launch(chunk_place_kernel, dim3(chunks), kChunk, 32 * experts * sizeof(int), s,
                       ids, pairs, choices, experts, (const int*)start, source, place);
     }
     const int threads = groups < kOrderThreads / 32 ? groups * 32 : kOrderThreads;
-    return launch(order_kernel, (unsigned)experts + 1, threads, 0, s, ids, pairs, choices, experts,
+    return launch(order_kernel, dim3(experts + 1), threads, 0, s, ids, pairs, choices, experts,
                   start, source, place);
 }
 
 cudaError_t launch_experts_sum(const void* y, int rows, const int* place, const float* weights,
                                int tokens, int choices, int H, void* out, cudaStream_t s) {
-    const long long vectors = (long long)tokens * (H / 8);
-    return launch(sum_kernel, (unsigned)((vectors + kSumThreads - 1) / kSumThreads), kSumThreads, 0, s,
-                  reinterpret_cast<const uint4*>(y), rows, place, weights, vectors, choices, H / 8,
-                  reinterpret_cast<uint4*>(out));
+    const int vecs = H / 8;
+    // as many threads as leave an eighth of them idle at most (rows of 250 vectors: 256
+    // threads; 672: 64), or a warp of them, and of a short row what it takes
+    int share = kSumThreads;
+    while (share > 32 && (vecs + share - 1) / share * share - vecs > vecs / 8) share /= 2;
+    while (share / 2 >= vecs) share /= 2;
+    const int at_once = kSumThreads / share;
+    const dim3 grid((tokens + at_once - 1) / at_once, (vecs + share - 1) / share);
+    return launch(choices <= 4 ? sum_kernel<4> : sum_kernel<8>, grid, kSumThreads, 0, s,
+                  reinterpret_cast<const uint4*>(y), rows, place, weights, tokens, choices, vecs,
+                  share, reinterpret_cast<uint4*>(out));
 }
 
 }  // namespace nvf

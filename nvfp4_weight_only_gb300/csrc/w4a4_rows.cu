@@ -132,11 +132,25 @@ __device__ __forceinline__ float reciprocal(float v) {
     return r;
 }
 
-// The larger of two pairs of bf16, NaN if either is.
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+// The larger magnitudes of two pairs of bf16 (of either sign), NaN if either is.
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// 16 values, 32 bytes; whole says that they are aligned so.
+__device__ __forceinline__ void load16(const uint4* at, bool whole, uint32_t (&v)[8]) {
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                       "=r"(v[6]), "=r"(v[7])
+                     : "l"(at));
+    } else {
+        const uint4 a = at[0], b = at[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
 }
 
 // Where a row goes: its expert's place for it, or those of a token's choices.
@@ -164,24 +178,35 @@ __device__ __forceinline__ Choice choice_of(const Places& to, int token, int j) 
     return c;
 }
 
-// One block per row of x; a warp takes 256 values at a time, 8 per lane, which stay in
-// registers between the row's maximum and the codes, so x is read once.  A token's codes
-// are written to the places of all of its choices.
+// One block per row of x; a warp takes 512 values at a time, 16 per lane (a block with its
+// scale), which stay in registers between the row's maximum and the codes, so x is read
+// once.  A token's codes are written to the places of all of its choices.
+//
+// Bound by memory (4096 rows of 17408: 29.5 us, 6.2 TB/s; 16384 of 2048: 17.1, 5.0).  With
+// 8 values per lane, two lanes to a scale, it issued 96 instructions for them, in two of
+// three cycles, and took 35.5 and 18.5 us.  56 registers let four blocks of 9 warps share
+// an SM (30.5 us without).
 template <int kIter>
-__global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict__ x, int K,
+__global__ void __maxnreg__(56) quantize_kernel(const uint4* __restrict__ x, int K,
                                                         int k_blocks, const Places to,
                                                         uint8_t* __restrict__ rows,
                                                         float* __restrict__ row_scales) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int row = blockIdx.x, vecs = K / 8;
-    const uint4* src = x + (size_t)row * vecs;
-    uint4 v[kIter];
+    const int row = blockIdx.x, vecs = K / 16;
+    const uint4* const src = x + (size_t)row * (K / 8);
+    const bool whole = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
+    uint32_t v[kIter][8];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
         const int c = (warp + i * warps) * 32 + lane;
-        v[i] = c < vecs ? src[c] : make_uint4(0, 0, 0, 0);
+        if (c < vecs) {
+            load16(src + 2 * c, whole, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0;
+        }
     }
     // the lists are read beside x: lane j looks up choice j
     Choice choice{-1, 0, 0};
@@ -189,26 +214,21 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
     long long block = 0;
     int r = 0;
     if (to.choices == 0 && !find_place(to.groups, row, block, r)) return;
-    uint32_t top[kIter];  // the largest of each block of 16, as bf16
-    uint32_t most = 0;
+    // the largest of each block, as bf16: as integers, magnitudes keep their order, NaN on top
+    uint32_t top[kIter], most = 0;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        constexpr uint32_t kAbs = 0x7fff7fffu;
-        const uint32_t m = max2_nan(max2_nan(v[i].x & kAbs, v[i].y & kAbs),
-                                    max2_nan(v[i].z & kAbs, v[i].w & kAbs));
-        top[i] = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        most = max2_nan(most, top[i]);
+        const uint32_t m =
+            max2_abs(max2_abs(max2_abs(v[i][0], v[i][1]), max2_abs(v[i][2], v[i][3])),
+                     max2_abs(max2_abs(v[i][4], v[i][5]), max2_abs(v[i][6], v[i][7])));
+        top[i] = max(m & 0x7fffu, m >> 16 & 0x7fffu);
+        most = max(most, top[i]);
     }
-#pragma unroll
-    for (int d = 16; d > 1; d >>= 1) most = max2_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
     __shared__ uint32_t part[32];
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) part[warp] = most;
     __syncthreads();
-    most = lane < warps ? part[lane] : 0;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) most = max2_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
-    // as integers, bf16 magnitudes keep their order, NaN on top
-    const uint32_t amax = max(most & 0xffffu, most >> 16);
+    const uint32_t amax = __reduce_max_sync(0xffffffffu, lane < warps ? part[lane] : 0);
     int e = 0;  // of r
     if (amax) {
         // 2688 = 1.3125 * 2^11, and 0x3fa8 is 1.3125
@@ -219,42 +239,46 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const uint4* __restrict_
     const float scale = amax >= 0x7f80 ? __uint_as_float(0x7fffffffu)
                                        : __uint_as_float((uint32_t)(e + 127) << 23);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 1 / r
-    // codes in place of x, scales of 64 values in every eighth lane
+    const float sixth_down = down * (1.0f / 6.0f);
+    // codes in place of x, scales of 64 values in every fourth lane
     uint32_t scales[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const float largest = __uint_as_float(max(top[i] & 0xffffu, top[i] >> 16) << 16) * down;
-        const uint32_t sixth = __float_as_uint(largest * (1.0f / 6.0f));
+        const uint32_t sixth = __float_as_uint(__uint_as_float(top[i] << 16) * sixth_down);
         // (of a row with a NaN anything without a sign)
         const uint32_t code = f32_to_e4m3(__uint_as_float((sixth + 0x400u) & ~0x7ffu)) & 0x7fu;
         const float by = code ? reciprocal(e4m3_to_f32(code)) * down : 0.0f;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         const uint64_t by2 = pair(by, by), grid = pair(768.0f, 768.0f), back = pair(-768.0f, -768.0f);
-        float q[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float2 y =
-                unpair(add2(fma2(pair(bf16_lo(w[p]), bf16_hi(w[p])), by2, grid), back));
-            q[2 * p] = y.x;
-            q[2 * p + 1] = y.y;
+        for (int h = 0; h < 2; ++h) {
+            float q[8];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t w = v[i][4 * h + p];
+                const float2 y = unpair(add2(fma2(pair(bf16_lo(w), bf16_hi(w)), by2, grid), back));
+                q[2 * p] = y.x;
+                q[2 * p + 1] = y.y;
+            }
+            v[i][h] = e2m1x8(q);
         }
-        v[i].x = e2m1x8(q);
         uint32_t sc = code;
-        sc |= __shfl_down_sync(0xffffffffu, sc, 2) << 8;
-        sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 16;
+        sc |= __shfl_down_sync(0xffffffffu, sc, 1) << 8;
+        sc |= __shfl_down_sync(0xffffffffu, sc, 2) << 16;
         scales[i] = sc;
     }
     auto write = [&](int at_row) {
         if (tid == 0) row_scales[at_row] = scale;
-        uint8_t* const out = rows + (size_t)block * k_blocks * kW4Tile;
+        // a warp's values are those of two tiles
+        const int kb0 = 2 * warp + lane / 16;
+        uint8_t* tile = rows + ((size_t)block * k_blocks + kb0) * kW4Tile;
+        const int code_at = w4_code_at(r, lane % 16 * 8), scale_at = w4_scale_at(r, lane % 16);
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int kb = warp + i * warps;
-            if (kb >= k_blocks) break;
-            uint8_t* const tile = out + (size_t)kb * kW4Tile;
-            *reinterpret_cast<uint32_t*>(tile + w4_code_at(r, lane * 4)) = v[i].x;
-            if ((lane & 7) == 0)
-                *reinterpret_cast<uint32_t*>(tile + w4_scale_at(r, lane / 2)) = scales[i];
+            if (kb0 + 2 * i * warps < k_blocks) {
+                *reinterpret_cast<uint2*>(tile + code_at) = make_uint2(v[i][0], v[i][1]);
+                if (lane % 4 == 0) *reinterpret_cast<uint32_t*>(tile + scale_at) = scales[i];
+            }
+            tile += (size_t)2 * warps * kW4Tile;
         }
     };
     if (to.choices == 0) {
@@ -347,18 +371,17 @@ namespace {
 cudaError_t quantize(const void* x, int blocks, int M, int K, const Places& to, void* rows,
                      cudaStream_t s) {
     const int k_blocks = w4_k_blocks(K);
-    // Two warps per row as long as 8 vectors per lane hold it: small blocks, whose loads and
-    // stores overlap others' (16384 rows of 2048: 18.1 us, with 4 warps 20.1, with 8 28.9).
+    // Two warps per row as long as 4 vectors per lane hold it: small blocks, whose loads and
+    // stores overlap others'.
     // Few rows leave room for eight, each with less to write (64 tokens of 4096 values for 8
-    // experts each: 3.2 us, with two warps 4.1; 300 for 2: 3.0, 2.8).
-    const int most = blocks <= kFewRows ? 8 : 2;
+    // experts each: 3.0 us, with two warps 4.1).
+    const int passes = (K + 511) / 512, most = blocks <= kFewRows ? 8 : 2;
     int iter = 1;
-    while (iter < 8 && k_blocks > most * iter) iter *= 2;
-    const int warps = (k_blocks + iter - 1) / iter;
+    while (iter < 4 && passes > most * iter) iter *= 2;
+    const int warps = (passes + iter - 1) / iter;
     auto kernel = iter == 1   ? quantize_kernel<1>
                   : iter == 2 ? quantize_kernel<2>
-                  : iter == 4 ? quantize_kernel<4>
-                              : quantize_kernel<8>;
+                              : quantize_kernel<4>;
     uint8_t* const base = reinterpret_cast<uint8_t*>(rows);
     float* const scales =
         reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, to.groups.experts));

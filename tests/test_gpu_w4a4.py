@@ -82,6 +82,24 @@ def test_quantize_every_magnitude(dev, lo, hi):
     assert torch.equal(ffi.w4a4_dequantize(ffi.w4a4_quantize(x)).double(), ref.values(x))
 
 
+@pytest.mark.parametrize("M,K", [(1, 16), (37, 528), (160, 4112), (3, 17408)])
+def test_quantize_rows_that_begin_on_16_bytes(dev, M, K):
+    x = draw(M * K + 8, 1, K, dev).flatten()[8:].view(M, K)
+    assert x.data_ptr() % 32 == 16
+    assert torch.equal(ffi.w4a4_dequantize(ffi.w4a4_quantize(x)).double(), ref.values(x))
+
+
+@pytest.mark.parametrize("at", [0, 15, 16, 511, 512, 1037])
+@pytest.mark.parametrize("bad", [0x7f80, 0xff80, 0x7fc0, 0xffc0, 0x7f81, 0xffff])
+def test_quantize_rows_with_any_value_that_is_not_finite(dev, at, bad):
+    """Infinities and NaN of both signs and any payload, in every place of a lane's values."""
+    x = draw(3, 1040, at, dev)
+    x[1].view(torch.int16)[at] = bad - 65536 if bad > 32767 else bad
+    got = ffi.w4a4_dequantize(ffi.w4a4_quantize(x))
+    assert bool(torch.isnan(got[1]).all())
+    assert torch.equal(got[[0, 2]].double(), ref.values(x[[0, 2]]))
+
+
 def test_quantize_every_tie(dev):
     """x = tie * s for every scale s that a block can get, beside a value that gives it."""
     s = torch.tensor(ref.E4M3[1:], dtype=torch.float64)
@@ -445,6 +463,21 @@ def test_sum(dev, T, k, H):
     v = y.double()[place.clamp(0, rows - 1).long()] * torch.where(live, w.double(), 0.0)[..., None]
     # k products added in fp32, a fused one each
     check(got, v.sum(1), k * 2.0 ** -24 * v.abs().sum(1))
+
+
+@pytest.mark.parametrize("k", [1, 4, 5, 9])
+@pytest.mark.parametrize("T,H", [(9, 16), (40, 48), (17, 240), (5, 272), (3, 2000), (2, 2064),
+                                 (2, 5376), (1, 65536)])
+def test_sum_of_rows_of_any_length(dev, T, H, k):
+    y = draw(T * k, H, T + k, dev)
+    g = torch.Generator(device=dev).manual_seed(H)
+    place = torch.randperm(T * k, generator=g, device=dev).view(T, k).int()
+    w = torch.rand((T, k), generator=g, device=dev) - 0.5
+    buf = torch.full((T * H + 64,), 7.0, dtype=BF, device=dev)
+    ffi.experts_sum(y, place, w, out=buf[:T * H].view(T, H))
+    v = y.double()[place.long()] * w.double()[..., None]
+    check(buf[:T * H].view(T, H), v.sum(1), k * 2.0 ** -24 * v.abs().sum(1))
+    assert bool((buf[T * H:] == 7.0).all())
 
 
 def test_sum_with_the_same_row_twice(dev):
