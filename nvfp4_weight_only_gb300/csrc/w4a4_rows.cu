@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinExp = -100, kMaxExp = 117;
-constexpr int kFewRows = 152;  // blocks that there is an SM for each
+constexpr int kFewRows = 152;   // as many as SMs
+constexpr int kRowsAtOnce = 4;  // of a block, a warp each, that are short
 
 // One thread per 16 code bytes of a tile (two scale bytes with them).
 __global__ void __launch_bounds__(kThreads) repack_kernel(
@@ -92,17 +93,16 @@ __device__ __forceinline__ void place_of(int row, int expert, int first, long lo
     r = i % kW4Rows;
 }
 
-// The expert of a row and its place; false for a row of none.  All threads of the
-// block call it.
+// The expert of a row and its place; false for a row of none.  A whole warp calls it.
 __device__ __forceinline__ bool find_place(const W4Groups& g, int row, long long& block, int& r) {
     int expert = 0, first = 0;
     if (g.start) {
         // the last expert that starts at or before the row: empty ones in front of it
         // start there too
         int before = 0;
-        for (int base = 0; base < g.experts; base += blockDim.x) {
-            const int e = base + threadIdx.x;
-            before += __syncthreads_count(e < g.experts && g.start[e] <= row);
+        for (int base = 0; base < g.experts; base += 32) {
+            const int e = base + (threadIdx.x & 31);
+            before += __popc(__ballot_sync(0xffffffffu, e < g.experts && g.start[e] <= row));
         }
         expert = before - 1;
         if (expert < 0) return false;
@@ -178,23 +178,25 @@ __device__ __forceinline__ Choice choice_of(const Places& to, int token, int j) 
     return c;
 }
 
-// One block per row of x; a warp takes 512 values at a time, 16 per lane (a block with its
-// scale), which stay in registers between the row's maximum and the codes, so x is read
-// once.  A token's codes are written to the places of all of its choices.
+// One block per row of x, or one warp; a warp takes 512 values at a time, 16 per lane (a
+// block with its scale), which stay in registers between the row's maximum and the codes,
+// so x is read once.  A token's codes are written to the places of all of its choices.
 //
-// Bound by memory (4096 rows of 17408: 29.5 us, 6.2 TB/s; 16384 of 2048: 17.1, 5.0).  With
+// Bound by memory (4096 rows of 17408: 29.5 us, 6.2 TB/s; 16384 of 2048: 14.2, 6.1).  With
 // 8 values per lane, two lanes to a scale, it issued 96 instructions for them, in two of
 // three cycles, and took 35.5 and 18.5 us.  56 registers let four blocks of 9 warps share
 // an SM (30.5 us without).
-template <int kIter>
-__global__ void __maxnreg__(56) quantize_kernel(const uint4* __restrict__ x, int K,
-                                                        int k_blocks, const Places to,
-                                                        uint8_t* __restrict__ rows,
-                                                        float* __restrict__ row_scales) {
+template <int kIter, bool kRowPerWarp>
+__global__ void __maxnreg__(56)
+    quantize_kernel(const uint4* __restrict__ x, int K, int k_blocks, const Places to, int count,
+                    uint8_t* __restrict__ rows, float* __restrict__ row_scales) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int row = blockIdx.x, vecs = K / 16;
+    const int lane = threadIdx.x & 31, vecs = K / 16;
+    // the row's warps, and which of them this one is
+    const int warps = kRowPerWarp ? 1 : blockDim.x / 32, warp = kRowPerWarp ? 0 : threadIdx.x / 32;
+    const int row = kRowPerWarp ? blockIdx.x * kRowsAtOnce + threadIdx.x / 32 : blockIdx.x;
+    if (row >= count) return;
     const uint4* const src = x + (size_t)row * (K / 8);
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
     uint32_t v[kIter][8];
@@ -224,11 +226,13 @@ __global__ void __maxnreg__(56) quantize_kernel(const uint4* __restrict__ x, int
         top[i] = max(m & 0x7fffu, m >> 16 & 0x7fffu);
         most = max(most, top[i]);
     }
-    __shared__ uint32_t part[32];
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) part[warp] = most;
-    __syncthreads();
-    const uint32_t amax = __reduce_max_sync(0xffffffffu, lane < warps ? part[lane] : 0);
+    uint32_t amax = __reduce_max_sync(0xffffffffu, most);
+    if constexpr (!kRowPerWarp) {
+        __shared__ uint32_t part[32];
+        if (lane == 0) part[warp] = amax;
+        __syncthreads();
+        amax = __reduce_max_sync(0xffffffffu, lane < warps ? part[lane] : 0);
+    }
     int e = 0;  // of r
     if (amax) {
         // 2688 = 1.3125 * 2^11, and 0x3fa8 is 1.3125
@@ -267,7 +271,7 @@ __global__ void __maxnreg__(56) quantize_kernel(const uint4* __restrict__ x, int
         scales[i] = sc;
     }
     auto write = [&](int at_row) {
-        if (tid == 0) row_scales[at_row] = scale;
+        if (warp == 0 && lane == 0) row_scales[at_row] = scale;
         // a warp's values are those of two tiles
         const int kb0 = 2 * warp + lane / 16;
         uint8_t* tile = rows + ((size_t)block * k_blocks + kb0) * kW4Tile;
@@ -368,25 +372,37 @@ cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, u
 
 namespace {
 
-cudaError_t quantize(const void* x, int blocks, int M, int K, const Places& to, void* rows,
+cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, void* rows,
                      cudaStream_t s) {
     const int k_blocks = w4_k_blocks(K);
-    // Two warps per row as long as 4 vectors per lane hold it: small blocks, whose loads and
-    // stores overlap others'.
-    // Few rows leave room for eight, each with less to write (64 tokens of 4096 values for 8
-    // experts each: 3.0 us, with two warps 4.1).
-    const int passes = (K + 511) / 512, most = blocks <= kFewRows ? 8 : 2;
+    // A row per warp as long as 4 passes hold it, four rows to a block, with no barrier and
+    // fewer blocks to start (16384 rows of 2048 14.2 us, with a block of two warps each 17.1;
+    // 8192 of 528: 3.5, 8.9).  Longer ones two warps, as long as 8 passes hold it: small
+    // blocks, whose loads and stores overlap others'.  Few rows leave room for eight, each
+    // with less to write (64 tokens of 4096 values for 8 experts each: 3.0 us, with two warps
+    // 4.1).
+    const int passes = (K + 511) / 512;
+    const bool few = count <= kFewRows, row_per_warp = passes <= 4 && !few;
+    const int most = few ? 8 : row_per_warp ? 1 : 2;
     int iter = 1;
     while (iter < 4 && passes > most * iter) iter *= 2;
     const int warps = (passes + iter - 1) / iter;
-    auto kernel = iter == 1   ? quantize_kernel<1>
-                  : iter == 2 ? quantize_kernel<2>
-                              : quantize_kernel<4>;
     uint8_t* const base = reinterpret_cast<uint8_t*>(rows);
     float* const scales =
         reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, to.groups.experts));
-    return launch(kernel, blocks, warps * 32, s, reinterpret_cast<const uint4*>(x), K, k_blocks, to,
-                  base, scales);
+    auto go = [&](auto kernel, int blocks, int threads) {
+        return launch(kernel, blocks, threads, s, reinterpret_cast<const uint4*>(x), K, k_blocks, to,
+                      count, base, scales);
+    };
+    if (row_per_warp) {
+        const int blocks = (count + kRowsAtOnce - 1) / kRowsAtOnce, threads = kRowsAtOnce * 32;
+        return iter == 1   ? go(quantize_kernel<1, true>, blocks, threads)
+               : iter == 2 ? go(quantize_kernel<2, true>, blocks, threads)
+                           : go(quantize_kernel<4, true>, blocks, threads);
+    }
+    return iter == 1   ? go(quantize_kernel<1, false>, count, warps * 32)
+           : iter == 2 ? go(quantize_kernel<2, false>, count, warps * 32)
+                       : go(quantize_kernel<4, false>, count, warps * 32);
 }
 
 }  // namespace

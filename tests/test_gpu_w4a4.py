@@ -89,6 +89,22 @@ def test_quantize_rows_that_begin_on_16_bytes(dev, M, K):
     assert torch.equal(ffi.w4a4_dequantize(ffi.w4a4_quantize(x)).double(), ref.values(x))
 
 
+@pytest.mark.parametrize("K", [16, 512, 528, 1040, 2048, 2064, 4096, 4112, 5120])
+@pytest.mark.parametrize("M", [152, 153, 155, 156])
+def test_quantize_short_and_long_rows_few_and_many(dev, M, K):
+    """Both sides of each rule on rows per block and warps per row, dense and by expert."""
+    x = draw(M, K, M + K, dev)
+    want = ref.values(x)
+    assert torch.equal(ffi.w4a4_dequantize(ffi.w4a4_quantize(x)).double(), want)
+    lens = [0, 1, 0, 0, 63, 0, 70, 5]  # rows behind the last expert's
+    start = starts(lens, 2, dev)
+    rows = ffi.w4a4_quantize(x, start=start)
+    out = torch.full((M, K), 7.0, dtype=BF, device=dev)
+    ffi.w4a4_dequantize(rows, out=out)
+    assert torch.equal(out[2:141].double(), want[2:141])
+    assert bool((out[:2] == 7.0).all()) and bool((out[141:] == 7.0).all())
+
+
 @pytest.mark.parametrize("at", [0, 15, 16, 511, 512, 1037])
 @pytest.mark.parametrize("bad", [0x7f80, 0xff80, 0x7fc0, 0xffc0, 0x7f81, 0xffff])
 def test_quantize_rows_with_any_value_that_is_not_finite(dev, at, bad):
