@@ -6,9 +6,9 @@
 //
 // Two shapes, by the rows of an expert (of the call, without experts) on average.
 //
-// Up to 128: a block has 128 rows of the weight as the lanes of its accumulators and the
-// tokens as columns, as many as there are, so a few tokens cost few columns.  Bound by
-// the weight's bytes; two accumulators take turns.
+// Up to 128, or tiles that fit in one turn: a block has 128 rows of the weight as the lanes
+// of its accumulators and the tokens as columns, as many as there are, so a few tokens cost
+// few columns.  Bound by the weight's bytes; two accumulators take turns.
 //
 // More: a pair of blocks (two SMs, one product of 256 x 256 x 64 at a time) has tokens as
 // lanes, so that the epilogue stores 32 bytes of a token's features per lane; with
@@ -981,15 +981,25 @@ cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s)
     e = cudaLaunchKernelEx(&cfg, w4a4_gemm_kernel<kTokens, kGated>, a, maps);
     if (!a.cut || e != cudaSuccess) return e;
     const int pairs = num_sms / Shape<kTokens>::kBlocks;
-    cfg.gridDim = dim3(left_over<kTokens>(a, pairs), kTokens == 256 ? 16 : (a.M + 7) / 8);
+    cfg.gridDim = dim3(left_over<kTokens>(a, pairs), kTokens == 256 ? 16 : (std::min(a.M, kTokens) + 7) / 8);
     cfg.blockDim = dim3(kW4Rows);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, w4a4_join_kernel<kTokens, kGated>, a, pairs);
 }
 
-// Tokens per tile: rows of an expert on average, as far as the host knows them.
+// Whether a product may take pairs' tiles: by the rows of an expert on average, as far as
+// the host knows them (16 experts, 4096 x 4096: 96 rows each 33.0 us with single blocks, 37.0
+// with pairs, 128 rows 35.2, 37.9, 160 rows 43.2, 38.5).
 bool wide(int M, int experts) { return M > 128LL * experts; }
+
+// And whether it does: not a dense one whose 128 x 128 tiles fit in one turn, which then use
+// twice as many SMs (K = 5120: 256 x 5120 9.6 us with single blocks, 11.2 with pairs, 384 x
+// 5120 9.8, 12.0; more than a turn 512 x 5120 16.3, 12.1, 160 x 17408 16.3, 16.1).
+bool pairs(const W4Product& p, int weight_blocks, int num_sms) {
+    const long long tiles = (p.M + kW4Rows - 1LL) / kW4Rows * weight_blocks;
+    return wide(p.M, p.groups.experts) && (p.groups.start || tiles > num_sms);
+}
 
 }  // namespace
 
@@ -1025,7 +1035,7 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, void* partials, int 
     a.wait_ns = test_wait_ns();
     a.stall = test_stall();
     Maps maps{};
-    if (wide(p.M, p.groups.experts)) {
+    if (pairs(p, a.row_blocks, num_sms)) {
         const long long blocks = w4_token_blocks(p.M, p.groups.experts);
         const long long weights = (long long)a.experts * a.row_blocks;
         if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024) ||

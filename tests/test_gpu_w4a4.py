@@ -133,12 +133,12 @@ def test_quantize_every_tie(dev):
 
 
 def test_zero_rows_and_rows_that_are_not_finite(dev):
-    x = draw(140, 512, 3, dev)
+    x = draw(10000, 512, 3, dev)
     x[5] = 0
     x[7, 100], x[20, 0], x[139, 511] = math.inf, -math.inf, math.nan
     w = draw_weight(64, 512, 4, dev)
     packed = ffi.w4a4_repack(*w[:2])
-    for M in (40, 140):  # both kernels
+    for M in (40, 140, 10000):  # both kernels
         rows = ffi.w4a4_quantize(x[:M].contiguous())
         y = ffi.w4a4_gemm(rows, packed, w[2], 64)
         bad = [r for r in (7, 20, 139) if r < M]
@@ -187,13 +187,19 @@ def test_a_weight_of_the_library_s_quantiser(dev):
 SIZES = [(1, 256, 128), (1, 16, 1), (2, 272, 77), (15, 512, 128), (16, 512, 130), (17, 1024, 300),
          (31, 48, 257), (33, 4096, 64), (64, 1040, 128), (100, 5376, 513), (127, 256, 2000),
          (128, 2048, 20000), (8, 768, 40000), (128, 5120, 5120),
-         # pairs of blocks from 129 rows on: whole and partial tiles, cut ones from 32 K blocks on
+         # more than one tile of tokens, whole and partial ones, cut ones
          (129, 256, 16), (130, 16, 1), (144, 512, 256), (255, 272, 300), (256, 4096, 256),
          (257, 8192, 130), (300, 8208, 264), (333, 5376, 5376), (700, 10240, 1111),
          (1000, 1024, 1000), (2048, 2048, 2056), (1025, 16384, 3000), (513, 8992, 2432)]
 
 
 SIZES += [(5, 17408, 130), (128, 8192, 264), (77, 65536, 48), (300, 65536, 48), (40, 21504, 5376)]
+# pairs of blocks, from 129 rows and 153 tiles of 128 x 128 on: whole and partial tiles, and those
+# of the last turn cut in 9, 4, 3 and 2 parts
+PAIRS = [(300, 272, 13000), (257, 48, 13100), (1301, 1040, 1801), (2600, 528, 1030), (20000, 64, 130),
+         (129, 256, 20000), (384, 5120, 6656), (1000, 8192, 5000), (1280, 16384, 5120),
+         (4864, 18432, 1040), (1024, 18432, 5376), (1500, 16384, 4864)]
+SIZES += PAIRS
 
 
 @pytest.mark.parametrize("M,K,N", SIZES)
@@ -214,7 +220,8 @@ def test_gemm(dev, M, K, N):
 @pytest.mark.parametrize("M,H,I", [(1, 16, 16), (1, 5120, 512), (20, 272, 208), (48, 4096, 1024),
                                    (128, 512, 4000), (129, 256, 64), (200, 1040, 336),
                                    (600, 8192, 1040), (2000, 512, 1024), (128, 12288, 272),
-                                   (300, 16384, 528)])
+                                   (300, 16384, 528), (1000, 8192, 2496), (700, 272, 2064),
+                                   (10000, 256, 48), (1280, 16384, 2560)])
 def test_gate_up(dev, M, H, I, kind):
     x, gate, up = draw(M, H, M, dev), draw_weight(I, H, 1, dev), draw_weight(I, H, 2, dev)
     packed = ffi.w4a4_repack_gate_up(*gate[:2], *up[:2])
@@ -231,22 +238,22 @@ def test_gated_products_that_are_ties_of_bf16(dev):
     codes[:, 0] = 2  # weight 1 at element 0
     scales = torch.full((I, H // 16), 0x38, dtype=torch.uint8, device=dev)  # 1
     packed = ffi.w4a4_repack_gate_up(codes, scales, codes, scales)
-    x = torch.zeros((300, H), device=dev)
+    x = torch.zeros((10000, H), device=dev)
     x[:, 0] = 6.0
-    few, many = [ffi.w4a4_quantize(x[:n].to(BF)) for n in (20, 300)]
+    few, many, pairs = [ffi.w4a4_quantize(x[:n].to(BF)) for n in (20, 300, 10000)]
     # g * u = 8 * 315, 16 * 323, 64 * 323, 128 * 315, 128 * 325: half a step from both neighbours
     for g, u, silu, gelu in ((20, 126, 2512, 2528), (34, 152, 5152, 5184), (34, -152, -5152, -5184),
                              (136, 152, 20736, 20736), (168, 240, 40448, 40448),
                              (200, 208, 41472, 41472)):
         for kind, want in ((0, silu), (1, gelu)):
-            for rows in few, many:
+            for rows in few, many, pairs:
                 got = ffi.w4a4_gate_up(rows, packed, g / 6, u / 6, I, kind)
                 assert bool((got == want).all()), (g, u, kind)
 
 
 def test_wide_and_narrow_agree(dev):
-    """The same rows through both kernels (of 128 rows and of more) within the bound of either."""
-    x, w = draw(256, 1024, 1, dev), draw_weight(512, 1024, 2, dev)
+    """The same rows through both kernels within the bound of either."""
+    x, w = draw(6000, 1024, 1, dev), draw_weight(512, 1024, 2, dev)
     packed = ffi.w4a4_repack(*w[:2])
     many = ffi.w4a4_gemm(ffi.w4a4_quantize(x), packed, w[2], 512)
     few = ffi.w4a4_gemm(ffi.w4a4_quantize(x[:100].contiguous()), packed, w[2], 512)
@@ -255,7 +262,7 @@ def test_wide_and_narrow_agree(dev):
     check(few, want[:100], off[:100])
 
 
-@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("M", [40, 300, 10000])
 @pytest.mark.parametrize("N,shift", [(48, 0), (48, 8), (40, 0), (40, 8), (50, 0), (33, 8)])
 def test_outputs_of_every_alignment(dev, M, N, shift):
     """Rows of 32-, 16- and 2-byte alignment, of a buffer that begins on 16 bytes; nothing beside
@@ -273,7 +280,8 @@ def test_outputs_of_every_alignment(dev, M, N, shift):
 
 @pytest.mark.parametrize("kind", [0, 1])
 @pytest.mark.parametrize("M,H,I", [(1, 256, 512), (7, 16, 16), (65, 528, 1040), (128, 1024, 256),
-                                   (300, 512, 2048), (1100, 256, 528)])
+                                   (300, 512, 2048), (1100, 256, 528), (5000, 528, 528),
+                                   (1000, 5120, 2496)])
 def test_ffn_is_its_parts(dev, M, H, I, kind):
     x = draw(M, H, M, dev)
     gate, up, down = draw_weight(I, H, 1, dev), draw_weight(I, H, 2, dev), draw_weight(H, I, 3, dev)

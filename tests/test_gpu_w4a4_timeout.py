@@ -25,10 +25,12 @@ def dev():
 
 @pytest.mark.parametrize("lens", [None, [30, 0, 250]])
 @pytest.mark.parametrize("M,K,N", [(280, 8192, 512), (280, 512, 6000), (30, 5120, 300),
-                                   (30, 1024, 30000)])
+                                   (30, 1024, 30000), (1000, 8192, 5000), (280, 512, 7000)])
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(dev, M, K, N, lens):
     if lens and M < sum(lens):
         lens = [10, 0, 20]
+    elif lens and M > 2 * sum(lens):
+        lens = [500, 0, 500]
     start = starts(lens, 0, dev) if lens else None
     x, w = draw(M, K, 1, dev), draw_weight(N, K, 2, dev, len(lens) if lens else None)
     rows, packed = ffi.w4a4_quantize(x, start=start), ffi.w4a4_repack(*w[:2])
