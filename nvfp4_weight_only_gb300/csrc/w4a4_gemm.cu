@@ -107,7 +107,9 @@ struct Args {
 // Tiles as tensors of kilobytes, [block][K block][18][256 x 4 bytes], for the copies of
 // pairs: what one block copies is reported to the other's barrier, which the plain bulk
 // copies cannot.  (With a thread that passed the word on, a stage took 545 ns or more.)
-// Boxes: a whole tile, a tile's codes, a tile's scales.
+// Boxes: a whole tile, a tile's codes, the scales of two tiles: each block takes
+// all of the columns' scales itself, since a copy that both received would be sound only for
+// a weight in this GPU's own memory, and was no faster (4096 x 17408 x 5120 113 us with either).
 struct Maps {
     CUtensorMap rows, codes, scales;  // the rows' whole tiles; the weight's
 };
@@ -306,24 +308,15 @@ __device__ __forceinline__ uint32_t in_first(uint32_t at) {
     return r;
 }
 
-// One box of a tile (see Maps) from kilobyte y of tile (kb, block) on, into this block's
-// memory, or to the same place in both blocks of the pair; `bar` is the first block's, to
-// which the copies into either are reported.
-template <bool kBoth>
+// One box (see Maps) from kilobyte y of tile (kb, block) on, into this block's memory; `bar`
+// is the first block's, to which the copies into either are reported.
 __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int y, int kb,
                                          int block, uint32_t bar) {
-    if constexpr (kBoth)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".multicast::cluster.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(to),
-            "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar), "h"((uint16_t)3)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
-            "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+        "l"(map), "r"(0), "r"(y), "r"(kb), "r"(block), "r"(bar)
+        : "memory");
 }
 
 // True for one thread of the warp, which calls it together.
@@ -694,13 +687,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             bulk_copy_g2s(at, t, kW4Tile, bar);
                         }
                     } else if (rows) {
-                        copy_box<false>(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
+                        copy_box(at, &maps.rows, 0, kb, (int)it.block + rank, in_first(bar));
                     } else {
                         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
                         bar = in_first(bar);
-                        copy_box<false>(at + S::kBAt, &maps.codes, 0, kb, weight, bar);
-                        copy_box<true>(at + S::kBScalesAt + rank * kW4Scales, &maps.scales,
-                                       kW4Codes / 1024, kb, weight, bar);
+                        copy_box(at + S::kBAt, &maps.codes, 0, kb, weight, bar);
+                        copy_box(at + S::kBScalesAt, &maps.scales, kW4Codes / 1024, kb,
+                                 weight - rank, bar);
                     }
                 }
                 __syncwarp();
@@ -919,13 +912,14 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A map of `blocks` row blocks of tiles for boxes of `rows` kilobytes.
-bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, int rows) {
+// A map of `blocks` row blocks of tiles for boxes of `rows` kilobytes of `tiles` neighbours.
+bool tile_map(CUtensorMap* map, const void* at, int k_blocks, long long blocks, int rows,
+              int tiles) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const cuuint64_t size[4] = {256, kW4Tile / 1024, (cuuint64_t)k_blocks, (cuuint64_t)blocks};
     const cuuint64_t stride[3] = {1024, kW4Tile, (cuuint64_t)k_blocks * kW4Tile};
-    const cuuint32_t box[4] = {256, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {256, (cuuint32_t)rows, 1, (cuuint32_t)tiles}, step[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, const_cast<void*>(at), size, stride, box,
                   step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1038,9 +1032,9 @@ cudaError_t launch_w4_gemm(const W4Product& p, int* status, void* partials, int 
     if (pairs(p, a.row_blocks, num_sms)) {
         const long long blocks = w4_token_blocks(p.M, p.groups.experts);
         const long long weights = (long long)a.experts * a.row_blocks;
-        if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024) ||
-            !tile_map(&maps.codes, p.packed, a.k_blocks, weights, kW4Codes / 1024) ||
-            !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024))
+        if (!tile_map(&maps.rows, p.rows, a.k_blocks, blocks, kW4Tile / 1024, 1) ||
+            !tile_map(&maps.codes, p.packed, a.k_blocks, weights, kW4Codes / 1024, 1) ||
+            !tile_map(&maps.scales, p.packed, a.k_blocks, weights, kW4Scales / 1024, 2))
             return cudaErrorInvalidValue;
         a.row_blocks /= Shape<256>::kBlocks;
         a.cut = cuts<256>(a, num_sms) ? a.k_blocks : 0;
