@@ -562,12 +562,11 @@ nvfp4_status kv8_attention(const void* q, int64_t q_stride, int tokens, int head
  * which keep activations in bf16: a user chooses.  These calls take any number of
  * rows up to 2^22 (RANGE beyond), K, H and I multiples of 16 up to 65536, N up to
  * 2^20.  They are asynchronous and use programmatic dependent launch; their results
- * are bit-reproducible.  The dense products w4a4_gemm and w4a4_gate_up begin to read
- * their packed weight while the preceding kernel on `stream` is still finishing, so that
- * kernel must not write it (the repack calls may precede them); nothing else is read
- * before it has completed, and by the other calls nothing at all.  Blocks of different
- * pairs do not wait for one another, so calls on different streams may overlap if their
- * workspaces (and rows buffers) differ.
+ * are bit-reproducible.  They read nothing, their weights neither, before the preceding
+ * kernel on `stream` has completed, so that kernel may write any of their inputs; and the
+ * kernel behind them is not launched before it has.  Blocks of different pairs do not wait
+ * for one another, so calls on different streams may overlap if their workspaces (and rows
+ * buffers) differ.
  *
  * A row of x [M, K] becomes a scale r per row, one E4M3 scale per 16 values and
  * E2M1 codes (all to nearest, ties to even, saturating):

@@ -284,7 +284,7 @@ nvfp4_status ffn_swiglu_w4a4(const void* x, int M, int H, int I, const void* gat
     e = w4a4_gate_up(w + l.x_rows, M, H, gate_up_packed, gate_scale2, up_scale2, I, act, w + l.h, ws,
                      l.front, stream);
     if (e != NVFP4_OK) return e;
-    // what is in front of the first quantisation was done before the gated product began
+    // the next kernel, a product, reads nothing before this one is done
     e = cuda_status(
         nvf::launch_w4_quantize(w + l.h, M, I, groups_of(nullptr), true, w + l.h_rows, stream));
     if (e != NVFP4_OK) return e;

@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const int* __restr
                                                               int* __restrict__ start,
                                                               int* __restrict__ source,
                                                               int* __restrict__ place) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const unsigned expert = blockIdx.x;
     const bool rest = (int)expert == experts;
@@ -124,8 +124,8 @@ __device__ __forceinline__ int chunk_end(int chunk, int chunks, int pairs) {
 
 __global__ void __launch_bounds__(kChunk) chunk_count_kernel(const int* __restrict__ ids, int pairs,
                                                              int experts, int* __restrict__ place) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int counts[kW4MaxExperts];
     const int tid = threadIdx.x, begin = blockIdx.x * kChunk;
     const int end = chunk_end(blockIdx.x, gridDim.x, pairs);
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kChunk) chunk_count_kernel(const int* __restri
 __global__ void __launch_bounds__(1024) chunk_sum_kernel(int chunks, int experts,
                                                          int* __restrict__ start,
                                                          int* __restrict__ place) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int total[kW4MaxExperts], part[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < experts; e += 1024) total[e] = 0;
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(kChunk) chunk_place_kernel(const int* __restri
                                                              const int* __restrict__ start,
                                                              int* __restrict__ source,
                                                              int* __restrict__ place) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ int counts[];
     __shared__ int first[kW4MaxExperts];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const uint4* __restric
                                                           const float* __restrict__ weights,
                                                           int tokens, int choices, int vecs,
                                                           int share, uint4* __restrict__ out) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int token = blockIdx.x * (kSumThreads / share) + threadIdx.x / share;
     const int c = blockIdx.y * share + threadIdx.x % share;
     if (token >= tokens || c >= vecs) return;

@@ -319,6 +319,11 @@ __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, in
         : "memory");
 }
 
+// Asks for `bytes` (a multiple of 16) at `from` in L2.
+__device__ __forceinline__ void prefetch_l2(const uint8_t* from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
 // True for one thread of the warp, which calls it together.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -580,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kWeightWarp = 0, kIssueWarp = 1, kRowsWarp = 2 + kEpilogueWarps;
     const int rank = blockIdx.x % S::kBlocks;  // in the pair
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kIssueWarp) tmem_alloc<S::kBlocks>(smem_addr(&tmem_at));
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -595,10 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort = 0;
         fence_mbar_init();
     }
-    // Without lists to read, the weight's first tiles are copied while the preceding kernel
-    // is still at work.
-    const bool early = a.start == nullptr;
-    if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.start) asm volatile("griddepcontrol.wait;" ::: "memory");
     // token tiles of each expert; one whose rows are not all inside has none, and none has
     // any where the list decreases (shares that overlap could be more than tiles are counted)
     if (tid == 0) prefix[0] = 0;
@@ -648,23 +649,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     Schedule<kTokens> schedule(a, prefix, gridDim.x / S::kBlocks, blockIdx.x / S::kBlocks);
     Item it{};
+    auto row_block = [&] { return (it.expert * a.row_blocks + it.weight) * S::kBlocks + rank; };
+    if (!a.start) {
+        // Without lists to read, the work is known before the preceding kernel is done: the
+        // weight's first tiles come into L2 meanwhile.  They are not read before it is done,
+        // as it may be what writes them.
+        if (warp == kWeightWarp) {
+            Schedule<kTokens> first = schedule;
+            if (first.take(it) && elect_one())
+                prefetch_l2(a.packed + ((size_t)row_block() * a.k_blocks + it.kb0) * kW4Tile,
+                            min(it.kb1 - it.kb0, S::kStages) * kW4Tile);
+            __syncwarp();
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    // Not before: the next kernel may begin on what it takes to be finished, the kernels in
+    // front of this one.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kWeightWarp || warp == kRowsWarp) {
         // Two warps, since a copy takes its thread about 200 cycles.
         const bool issuer = elect_one(), rows = warp == kRowsWarp;
-        if (rows && early) asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned n = 0;  // stages filled
         bool ok = true;
         while (ok && schedule.take(it)) {
-            const int weight = (it.expert * a.row_blocks + it.weight) * S::kBlocks + rank;
+            const int weight = row_block();
             const uint8_t* const from = rows ? a.rows + (size_t)it.block * a.k_blocks * kW4Tile
                                              : a.packed + (size_t)weight * a.k_blocks * kW4Tile;
             const int codes = S::columns(it.tokens) * 128;  // of the rows, to one block alone
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % S::kStages;
                 if (n >= S::kStages) {
-                    // a limited wait does not begin before the preceding kernel is done
-                    if (n == S::kStages && early && !rows)
-                        asm volatile("griddepcontrol.wait;" ::: "memory");
                     ok = wait(bars.empty[stage], n / S::kStages - 1);
                     if (!ok) break;
                 }
@@ -700,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // the last products' word has come before the barriers that it goes to are left
-        if (early && !rows) asm volatile("griddepcontrol.wait;" ::: "memory");
         for (unsigned i = n > S::kStages ? n - S::kStages : 0; i < n && ok; ++i)
             ok = wait(bars.empty[i % S::kStages], i / S::kStages);
         if (abort) {
@@ -721,7 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the start, each of these instructions took about 60 cycles (their operands have to
         // be the same for the warp), 1030 for a stage's.
         const bool issuer = elect_one();
-        if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned n = 0, items = 0;
         bool ok = true;
         while (ok && schedule.take(it)) {
@@ -777,7 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_bounded(smem_addr(&bars.drained), 0, &none);
         }
     } else if (warp > kIssueWarp) {  // the epilogue
-        if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
         // a warp reads 32 lanes of a share of the columns
         constexpr int kShare = kTokens * 4 / kEpilogueWarps;
         const int quadrant = warp & 3, eid = tid - 64;
@@ -869,8 +880,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of one block's tile of 1 token 7 us, of 128 tokens 15 us.)
 template <int kTokens, bool kGated>
 __global__ void __launch_bounds__(kW4Rows) w4a4_join_kernel(const Args a, int pairs) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int prefix[2] = {0, (a.M + kTokens - 1) / kTokens};
     const Schedule<kTokens> schedule(a, prefix, pairs, 0);
     Item it{};

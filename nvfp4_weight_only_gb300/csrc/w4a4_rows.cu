@@ -60,9 +60,6 @@ __global__ void __launch_bounds__(kThreads) repack_kernel(
         *reinterpret_cast<uint4*>(out + w4_code_at(r, piece * 16)) = w;
         *reinterpret_cast<uint16_t*>(out + w4_scale_at(r, piece * 2)) = (uint16_t)sc;
     }
-    // Visible GPU-wide before this block exits: the product may start on its weights as
-    // soon as every block has.
-    __threadfence();
 }
 
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ packed,
@@ -190,9 +187,9 @@ template <int kIter, bool kRowPerWarp>
 __global__ void __maxnreg__(56)
     quantize_kernel(const uint4* __restrict__ x, int K, int k_blocks, const Places to, int count,
                     bool at_once, uint8_t* __restrict__ rows, float* __restrict__ row_scales) {
-    // A product begins to read its weight when it is launched: not before all kernels in front
-    // of this one are done, unless they are known not to write it (48 rows, H=4096 I=12288:
-    // 31.9 us with both quantisations so, 33.0 with neither).
+    // The decode products read their weights as soon as they are launched, so the next kernel
+    // is launched when all kernels in front of this one are done; at once where it is known to
+    // read nothing early (48 rows, H=4096 I=12288: 31.9 us so, 33.0 without).
     if (at_once) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!at_once) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -312,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __r
                                                               int K, int k_blocks,
                                                               const W4Groups g,
                                                               uint4* __restrict__ out) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int row = blockIdx.x;
     long long block;
     int r;
