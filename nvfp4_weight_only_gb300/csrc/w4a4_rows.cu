@@ -11,6 +11,9 @@
 // 13 bits.  For E2M1 (ties are multiples of 1/4 up to 5) a quotient is 2^-10 or more away
 // from a tie that it is not; the grid is 2^-14 (768 is added and taken away).  So codes
 // are those of the exact quotients, without a division.
+#include <algorithm>
+
+#include "internal.h"
 #include "kv8.cuh"
 #include "w4a4.h"
 
@@ -20,7 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinExp = -100, kMaxExp = 117;
-constexpr int kFewRows = 152;   // as many as SMs
 constexpr int kRowsAtOnce = 4;  // of a block, a warp each, that are short
 
 // One thread per 16 code bytes of a tile (two scale bytes with them).
@@ -347,8 +349,8 @@ cudaError_t launch(void (*kernel)(Args...), int blocks, int threads, cudaStream_
 }
 
 int grid_of(long long work) {
-    const long long want = (work + kThreads - 1) / kThreads, most = 16LL * 152;
-    return (int)(want < most ? want : most);
+    const long long want = (work + kThreads - 1) / kThreads;
+    return (int)std::min(want, 16LL * std::max(1, device_sm_count()));
 }
 
 }  // namespace
@@ -379,11 +381,11 @@ cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, b
     // A row per warp as long as 4 passes hold it, four rows to a block, with no barrier and
     // fewer blocks to start (16384 rows of 2048 14.2 us, with a block of two warps each 17.1;
     // 8192 of 528: 3.5, 8.9).  Longer ones two warps, as long as 8 passes hold it: small
-    // blocks, whose loads and stores overlap others'.  Few rows leave room for eight, each
-    // with less to write (64 tokens of 4096 values for 8 experts each: 3.0 us, with two warps
-    // 4.1).
+    // blocks, whose loads and stores overlap others'.  Few rows, as many as SMs, leave room
+    // for eight, each with less to write (64 tokens of 4096 values for 8 experts each: 3.0
+    // us, with two warps 4.1).
     const int passes = (K + 511) / 512;
-    const bool few = count <= kFewRows, row_per_warp = passes <= 4 && !few;
+    const bool few = count <= device_sm_count(), row_per_warp = passes <= 4 && !few;
     const int most = few ? 8 : row_per_warp ? 1 : 2;
     int iter = 1;
     while (iter < 4 && passes > most * iter) iter *= 2;
