@@ -384,7 +384,12 @@ __device__ __forceinline__ void sync_blocks() {
 __device__ __forceinline__ float gated(int act, float g, float u) {
     const float y = act == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float e = __expf(-fabsf(y)), s = __fdividef(e, 1.0f + e);  // sigmoid(-|y|)
-    if (!(y > 0.0f)) return g * s * u;
+    if (!(y > 0.0f)) {
+        // far below 0 the sigmoid is e^y, which leaves fp32's normal numbers from -87 on, where a
+        // product with a large u does not: in two halves
+        const float half = __expf(0.5f * y);
+        return y < -64.0f ? g * half * u * half : g * s * u;
+    }
     const float t = g * u;
     const float p = fabsf(t) < INFINITY ? fmaf(-t, s, t) : t;
     const uint32_t bits = __float_as_uint(p);
