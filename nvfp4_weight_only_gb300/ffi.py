@@ -489,8 +489,17 @@ def ffn_swiglu_w8a16(x: torch.Tensor, gate_up_packed: torch.Tensor, down_packed:
 # read each tensor attribute once and pass plain numbers.
 
 _BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
-# The current stream's handle by device index, without a Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _raw_stream(device):
+    """The current stream's handle (without a Stream object) on `device`, which has to be the
+    current one: the library launches there."""
+    if device != _current_device():
+        raise ValueError(f"tensors on device {device} need it as the current device, but the "
+                         f"current device is {_current_device()}")
+    return _current_raw_stream(device)
 
 
 def _plain(t, name, dtype, shape, device):
