@@ -31,9 +31,10 @@
 // the workspace, and a second launch adds them up in the order of the ranges.  So results
 // do not depend on timing, and no block waits for one that is not of its pair.
 //
-// Measured (us, of it the rate): 4096 x 17408 x 5120 109 (6.7 Pflop/s), 2048 x 5120 x
-// 34816 with SiLU 115 (6.3), 59 rows of 64 experts, 4096 x 4096 with SiLU 83.5 (7.2 TB/s
-// of weights), 1 x 5120 x 7168 8.5 (2.4 TB/s: start, first copies and end take 6 of it).
+// Measured (us, of it the rate): 4096 x 17408 x 5120 111 (6.6 Pflop/s), 2048 x 5120 x
+// 34816 with SiLU 119 (6.1), 59 rows of 64 experts, 4096 x 4096 with SiLU 83.5 (7.2 TB/s
+// of weights), 1 x 5120 x 7168 with the weight in L2 7.9 (2.6 TB/s: start, first copies and
+// end take 6 of it), out of memory 8.8.
 #include <cuda.h>
 
 #include <algorithm>
