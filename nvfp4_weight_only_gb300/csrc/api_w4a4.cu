@@ -182,7 +182,7 @@ nvfp4_status w4a4_quantize(const void* x, int M, int K, const w4a4_groups* group
     if (!aligned(x, 16) || !aligned(rows, 16)) return NVFP4_ERR_ALIGN;
     if (overlap(x, (size_t)M * K * 2, rows, rows_bytes(M, K, g.experts)))
         return NVFP4_ERR_ALIAS;
-    return cuda_status(nvf::launch_w4_quantize(x, M, K, g, false, rows, stream));
+    return cuda_status(nvf::launch_w4_quantize(x, M, K, g, rows, stream));
 }
 
 nvfp4_status w4a4_quantize_routed(const void* x, int tokens, int K, const int* ids,
@@ -284,9 +284,7 @@ nvfp4_status ffn_swiglu_w4a4(const void* x, int M, int H, int I, const void* gat
     e = w4a4_gate_up(w + l.x_rows, M, H, gate_up_packed, gate_scale2, up_scale2, I, act, w + l.h, ws,
                      l.front, stream);
     if (e != NVFP4_OK) return e;
-    // the next kernel, a product, reads nothing before this one is done
-    e = cuda_status(
-        nvf::launch_w4_quantize(w + l.h, M, I, groups_of(nullptr), true, w + l.h_rows, stream));
+    e = w4a4_quantize(w + l.h, M, I, nullptr, w + l.h_rows, stream);
     if (e != NVFP4_OK) return e;
     return w4a4_gemm(w + l.h_rows, M, I, down_packed, down_scale2, H, out, ws, l.front, stream);
 }

@@ -68,10 +68,8 @@ cudaError_t launch_w4_repack(const uint8_t* codes, const uint8_t* scales, const 
                              cudaStream_t s);
 cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, uint8_t* codes,
                              uint8_t* scales, cudaStream_t s);
-// at_once: the next kernel is launched before those in front of this one are done (it reads
-// nothing until they and this one are).
-cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, bool at_once,
-                               void* rows, cudaStream_t s);
+cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
+                               cudaStream_t s);
 // Each token's row, at the places of its choices (ids, place [tokens, choices]).
 cudaError_t launch_w4_quantize_routed(const void* x, int tokens, int K, const int* ids,
                                       const int* place, int choices, const W4Groups& g, void* rows,

@@ -1005,8 +1005,8 @@ cudaError_t launch(const Args& a, const Maps& maps, int num_sms, cudaStream_t s)
 bool wide(int M, int experts) { return M > 128LL * experts; }
 
 // And whether it does: not a dense one whose 128 x 128 tiles fit in one turn, which then use
-// twice as many SMs (K = 5120: 256 x 5120 9.6 us with single blocks, 11.2 with pairs, 384 x
-// 5120 9.8, 12.0; more than a turn 512 x 5120 16.3, 12.1, 160 x 17408 16.3, 16.1).
+// twice as many SMs (K = 5120: 256 x 5120 9.8 us with single blocks, 11.3 with pairs, 384 x
+// 5120 10.0, 12.3; more than a turn 512 x 5120 16.3, 12.3, 160 x 17408 16.3, 15.9).
 bool pairs(const W4Product& p, int weight_blocks, int num_sms) {
     const long long tiles = (p.M + kW4Rows - 1LL) / kW4Rows * weight_blocks;
     return wide(p.M, p.groups.experts) && (p.groups.start || tiles > num_sms);

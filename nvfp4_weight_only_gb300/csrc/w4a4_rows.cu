@@ -181,20 +181,18 @@ __device__ __forceinline__ Choice choice_of(const Places& to, int token, int j) 
 // block with its scale), which stay in registers between the row's maximum and the codes,
 // so x is read once.  A token's codes are written to the places of all of its choices.
 //
-// Bound by memory (4096 rows of 17408: 29.5 us, 6.2 TB/s; 16384 of 2048: 14.2, 6.1).  With
+// Bound by memory (4096 rows of 17408: 30.0 us, 6.1 TB/s; 16384 of 2048: 14.2, 6.1).  With
 // 8 values per lane, two lanes to a scale, it issued 96 instructions for them, in two of
 // three cycles, and took 35.5 and 18.5 us.  56 registers let four blocks of 9 warps share
 // an SM (30.5 us without).
 template <int kIter, bool kRowPerWarp>
 __global__ void __maxnreg__(56)
     quantize_kernel(const uint4* __restrict__ x, int K, int k_blocks, const Places to, int count,
-                    bool at_once, uint8_t* __restrict__ rows, float* __restrict__ row_scales) {
+                    uint8_t* __restrict__ rows, float* __restrict__ row_scales) {
     // The decode products read their weights as soon as they are launched, so the next kernel
-    // is launched when all kernels in front of this one are done; at once where it is known to
-    // read nothing early (48 rows, H=4096 I=12288: 31.9 us so, 33.0 without).
-    if (at_once) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // is launched when all kernels in front of this one are done.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!at_once) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, vecs = K / 16;
     // the row's warps, and which of them this one is
     const int warps = kRowPerWarp ? 1 : blockDim.x / 32, warp = kRowPerWarp ? 0 : threadIdx.x / 32;
@@ -375,8 +373,8 @@ cudaError_t launch_w4_unpack(const uint8_t* packed, int experts, int N, int K, u
 
 namespace {
 
-cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, bool at_once,
-                     void* rows, cudaStream_t s) {
+cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, void* rows,
+                     cudaStream_t s) {
     const int k_blocks = w4_k_blocks(K);
     // A row per warp as long as 4 passes hold it, four rows to a block, with no barrier and
     // fewer blocks to start (16384 rows of 2048 14.2 us, with a block of two warps each 17.1;
@@ -395,7 +393,7 @@ cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, b
         reinterpret_cast<float*>(base + w4_rows_scale_offset(M, K, to.groups.experts));
     auto go = [&](auto kernel, int blocks, int threads) {
         return launch(kernel, blocks, threads, s, reinterpret_cast<const uint4*>(x), K, k_blocks, to,
-                      count, at_once, base, scales);
+                      count, base, scales);
     };
     if (row_per_warp) {
         const int blocks = (count + kRowsAtOnce - 1) / kRowsAtOnce, threads = kRowsAtOnce * 32;
@@ -410,16 +408,16 @@ cudaError_t quantize(const void* x, int count, int M, int K, const Places& to, b
 
 }  // namespace
 
-cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, bool at_once,
-                               void* rows, cudaStream_t s) {
-    return quantize(x, M, M, K, Places{g, nullptr, nullptr, 0, M}, at_once, rows, s);
+cudaError_t launch_w4_quantize(const void* x, int M, int K, const W4Groups& g, void* rows,
+                               cudaStream_t s) {
+    return quantize(x, M, M, K, Places{g, nullptr, nullptr, 0, M}, rows, s);
 }
 
 cudaError_t launch_w4_quantize_routed(const void* x, int tokens, int K, const int* ids,
                                       const int* place, int choices, const W4Groups& g, void* rows,
                                       cudaStream_t s) {
     const int M = tokens * choices;
-    return quantize(x, tokens, M, K, Places{g, ids, place, choices, M}, false, rows, s);
+    return quantize(x, tokens, M, K, Places{g, ids, place, choices, M}, rows, s);
 }
 
 cudaError_t launch_w4_dequantize(const void* rows, int M, int K, const W4Groups& g, void* out,

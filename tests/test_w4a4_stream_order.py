@@ -28,9 +28,7 @@ def test_kernels_wait_before_they_copy_and_before_they_launch_the_next(name, cou
     assert len(seen) == count
     for kernel, body in seen:
         waits = [m.start() for m in re.finditer(r"griddepcontrol\.wait", body)]
-        # the quantiser's word ahead of its wait is given only in front of a product of these
-        launches = [m.start() for m in re.finditer(
-            r"(?<!if \(at_once\) asm volatile\(\")griddepcontrol\.launch_dependents", body)]
+        launches = [m.start() for m in re.finditer(r"griddepcontrol\.launch_dependents", body)]
         copies = [m.start() for m in re.finditer(r"bulk_copy_g2s|copy_box\(", body)]
         assert len(launches) == 1 and launches[0] > max(waits), kernel
         assert all(at > max(waits) for at in copies), kernel
